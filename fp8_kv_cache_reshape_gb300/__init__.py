@@ -40,6 +40,7 @@ KVQ_DEV_BAD_BLOCK = 0x2
 KVQ_DEV_BAD_SEQLEN = 0x4
 KVQ_DEV_TIMEOUT = 0x8
 KVQ_DEV_BAD_QROWS = 0x10
+KVQ_DEV_BAD_GROUP = 0x20
 
 PAGE = 16
 
@@ -98,6 +99,18 @@ lib.kvq_prefill_attention_per_token.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, 
 lib.kvq_prefill_attention.restype = _i
 lib.kvq_prefill_attention.argtypes = [_p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i,
                                       _f, _i, _p, _p]
+lib.kvq_shared_prefix_workspace_size.restype = _sz
+lib.kvq_shared_prefix_workspace_size.argtypes = [_i] * 8
+lib.kvq_paged_decode_attention_shared_prefix.restype = _i
+lib.kvq_paged_decode_attention_shared_prefix.argtypes = [_p] * 11 + [_i] * 8 + [_i64, _f, _i, _p, _sz, _p, _p]
+lib.kvq_decode_weights_workspace_size.restype = _sz
+lib.kvq_decode_weights_workspace_size.argtypes = [_i] * 8
+lib.kvq_paged_decode_attention_weights.restype = _i
+lib.kvq_paged_decode_attention_weights.argtypes = [_p] * 9 + [_i64, _f, _i, _i, _i, _i, _i, _i, _i64, _f, _i, _i, _i,
+                                                              _i, _p, _sz, _p, _p]
+lib.kvq_evict_tokens.restype = _i
+lib.kvq_evict_tokens.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p, _p, _i, _i, _i, _i, _i, _i, _i64, _i,
+                                 _i, _i, _i, _p, _p]
 
 
 class KvqError(RuntimeError):
@@ -379,3 +392,103 @@ def kvq_prefill_attention_per_token(q8, q_scale, k_cache, v_cache, block_table, 
         float(sm_scale), 1 if causal else 0, _dtype_code(cache_dtype), _ptr(dev_status), _stream(stream)),
         "kvq_prefill_attention_per_token")
     return out
+
+
+def _check_tensor(t, dtype, shape, name):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+
+
+def kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix_blocks, max_blocks):
+    return lib.kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, PAGE, max_prefix_blocks, max_blocks)
+
+
+def kvq_paged_decode_attention_shared_prefix(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_lens,
+                                             group_starts, block_table, seq_lens, out, num_blocks=None, sm_scale=None,
+                                             cache_dtype="fp8_e4m3", workspace=None, dev_status=None, stream=None):
+    """One decode step of a batch whose sequences share prefixes: sequences
+    group_starts[i] .. group_starts[i + 1] - 1 attend to the first
+    prefix_lens[i] tokens of prefix_table[i] (read once for the whole group)
+    and to their own seq_lens[b] tokens of block_table[b]."""
+    B, Hq, D = q.shape
+    G, max_prefix = prefix_table.shape
+    Hkv = k_cache.shape[1]
+    _check_tensor(q, torch.bfloat16, (B, Hq, D), "q")
+    _check_tensor(out, torch.bfloat16, (B, Hq, D), "out")
+    _check_tensor(prefix_table, torch.int32, (G, max_prefix), "prefix_table")
+    _check_tensor(prefix_lens, torch.int32, (G,), "prefix_lens")
+    _check_tensor(group_starts, torch.int32, (G + 1,), "group_starts")
+    _check_tensor(block_table, torch.int32, (B, block_table.shape[1]), "block_table")
+    _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
+    max_blocks = block_table.shape[1]
+    if workspace is None:
+        need = kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix, max_blocks)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check(lib.kvq_paged_decode_attention_shared_prefix(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table), _ptr(prefix_lens),
+        _ptr(group_starts), _ptr(block_table), _ptr(seq_lens), _ptr(out), B, G, Hq, Hkv, D, PAGE, max_prefix,
+        max_blocks, k_cache.shape[0] if num_blocks is None else num_blocks,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), _dtype_code(cache_dtype), _ptr(workspace),
+        workspace.numel(), _ptr(dev_status), _stream(stream)), "kvq_paged_decode_attention_shared_prefix")
+    return out
+
+
+def kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window=-1, num_splits=0):
+    return lib.kvq_decode_weights_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, window, num_splits)
+
+
+def kvq_paged_decode_attention_weights(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, weights,
+                                       decay=1.0, num_blocks=None, sm_scale=None, window=-1, cache_dtype="fp8_e4m3",
+                                       per_token=False, num_splits=0, workspace=None, dev_status=None, stream=None):
+    """kvq_paged_decode_attention that also accumulates each cached token's
+    attention weight: weights (float32 [B][Hkv][>= max_blocks * 16]) becomes
+    decay * weights + the sum over the KV head's query heads, for the first
+    seq_lens[b] tokens.  per_token: a per-token-scaled cache (k_scale and
+    v_scale None)."""
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[1]
+    max_blocks = block_table.shape[1]
+    _check_tensor(q, torch.bfloat16, (B, Hq, D), "q")
+    _check_tensor(out, torch.bfloat16, (B, Hq, D), "out")
+    _check_tensor(block_table, torch.int32, (B, max_blocks), "block_table")
+    _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
+    _check_tensor(weights, torch.float32, (B, Hkv, weights.shape[-1]), "weights")
+    if workspace is None:
+        need = kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _check(lib.kvq_paged_decode_attention_weights(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
+        _ptr(out), _ptr(weights), weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks,
+        k_cache.shape[0] if num_blocks is None else num_blocks,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, _dtype_code(cache_dtype),
+        1 if per_token else 0, num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)),
+        "kvq_paged_decode_attention_weights")
+    return out
+
+
+def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens, dst_block_table, dst_weights,
+                     dst_seq_lens, kept, head_dim, sink=0, recent=0, num_blocks=None, cache_dtype="fp8_e4m3",
+                     per_token=False, dev_status=None, stream=None):
+    """Cut each sequence's cache to its keep_lens[b] heaviest tokens per KV
+    head (the first `sink` and last `recent` always stay), copied in order
+    into the pages dst_block_table[b]; dst_weights (float32 [B][Hkv][...]),
+    dst_seq_lens (int32 [B]) and kept (int32 [B][Hkv][max_dst_blocks * 16],
+    source positions) are written."""
+    B, max_blocks = block_table.shape
+    max_dst = dst_block_table.shape[1]
+    Hkv = k_cache.shape[1]
+    _check_tensor(weights, torch.float32, (B, Hkv, weights.shape[-1]), "weights")
+    _check_tensor(block_table, torch.int32, (B, max_blocks), "block_table")
+    _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
+    _check_tensor(keep_lens, torch.int32, (B,), "keep_lens")
+    _check_tensor(dst_block_table, torch.int32, (B, max_dst), "dst_block_table")
+    _check_tensor(dst_weights, torch.float32, (B, Hkv, dst_weights.shape[-1]), "dst_weights")
+    _check_tensor(dst_seq_lens, torch.int32, (B,), "dst_seq_lens")
+    _check_tensor(kept, torch.int32, (B, Hkv, max_dst * PAGE), "kept")
+    _check(lib.kvq_evict_tokens(
+        _ptr(weights), weights.shape[-1], _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
+        _ptr(keep_lens), _ptr(dst_block_table), _ptr(dst_weights), dst_weights.shape[-1], _ptr(dst_seq_lens),
+        _ptr(kept), B, Hkv, head_dim, PAGE, max_blocks, max_dst,
+        k_cache.shape[0] if num_blocks is None else num_blocks, sink, recent, _dtype_code(cache_dtype),
+        1 if per_token else 0, _ptr(dev_status), _stream(stream)), "kvq_evict_tokens")
+    return dst_seq_lens

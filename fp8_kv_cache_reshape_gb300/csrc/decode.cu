@@ -88,6 +88,10 @@ struct DecodeParams {
   const int64_t* slot_new;
   uint8_t* k_cache_w;
   uint8_t* v_cache_w;
+  // Scores (optional, the weights entry point): every attended token's masked
+  // base-2 scores, [B][Hkv][max_blocks * P][gp], gp = g rounded up to even
+  float* scores;
+  int gp;
   // failure-path test hook (kvq_debug_set_stall_ns): > 0 makes consumer warp
   // 0 wait up to this long on a barrier nothing arrives on before its first
   // stage, which fails like a stuck pipeline wait
@@ -416,7 +420,9 @@ constexpr int kPresent0 = 1, kPresent1 = 2, kBad0 = 4, kBad1 = 8;
 // fresh FP32 tile per stage (FP8, per-head scales only).
 // AP: the append entry point's instantiation (the new token's cache write);
 // the plain decode is compiled without it.
-template <int D, bool FP8, int NW, int NST, bool E5, bool PT, bool SL, bool AP = false, bool BAL = false>
+// SC: the weights entry point's instantiation (p.scores is written).
+template <int D, bool FP8, int NW, int NST, bool E5, bool PT, bool SL, bool AP = false, bool BAL = false,
+          bool SC = false>
 __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partial_kernel(const __grid_constant__ DecodeParams p) {
   using G = Geo<D, FP8>;
   static_assert(NST % NW == 0 && NST >= NW, "each ring slot must belong to one consumer warp");
@@ -737,6 +743,18 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
       float p00, p01, p02, p03, p10, p11, p12, p13, al0, al1;
       // online softmax over the stage's 32 tokens (base 2)
       auto softmax = [&]() {
+        if constexpr (SC) {  // eight lanes of a head pair write eight consecutive tokens: 64-byte runs and longer
+          if (2 * c < p.g) {
+            float* sp = p.scores +
+                        ((static_cast<size_t>(rg.b) * p.Hkv + rg.kvh) * p.max_blocks * kPage + tok0 + r) * p.gp + 2 * c;
+            *reinterpret_cast<float2*>(sp) = make_float2(s0[0], s0[1]);
+            *reinterpret_cast<float2*>(sp + 8 * p.gp) = make_float2(s0[2], s0[3]);
+            if (two) {
+              *reinterpret_cast<float2*>(sp + 16 * p.gp) = make_float2(s1[0], s1[1]);
+              *reinterpret_cast<float2*>(sp + 24 * p.gp) = make_float2(s1[2], s1[3]);
+            }
+          }
+        }
         float mx0 = fmaxf(fmaxf(s0[0], s0[2]), fmaxf(s1[0], s1[2]));
         float mx1 = fmaxf(fmaxf(s0[1], s0[3]), fmaxf(s1[1], s1[3]));
 #pragma unroll
@@ -1187,6 +1205,86 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
   }
 }
 
+// weights[b][kvh][j] = decay * weights[b][kvh][j] + sum over the group's query
+// heads of 2^(score - lse), j < L_b, from the scores and log-sum-exps that the
+// partial kernel left.  Bound by memory: per token and KV head 4 gp bytes of
+// scores (in L2 from the partial kernel where they fit) and 8 of weights.
+// Grid (chunks of kWeightTokens tokens, B * Hkv): each CTA merges its heads'
+// log-sum-exps (a warp per head), then one thread per token adds the heads in
+// order, so that results do not depend on timing.
+constexpr int kWeightThreads = 256;
+constexpr int kWeightTokens = 1024;
+struct WeightsParams {
+  const float* scores;
+  const float* lse_part;
+  float* weights;
+  int64_t stride;  // floats between the rows of consecutive (sequence, KV head) pairs
+  float decay;
+  int Hkv, g, gp;
+  CombinePlan cp;
+};
+// The partials of row (b, hq): first index and count.
+KVQ_DEVINL void row_partials(const CombinePlan& cp, int b, int hq, int lane, size_t& first, int& S) {
+  first = (static_cast<size_t>(b) * cp.Hq + hq) * cp.S;
+  S = cp.S;
+  if (!cp.balanced) return;
+  const BatchScan bs = batch_scan_of(cp.seq_lens, cp.B, cp.max_blocks, cp.window, lane, true, nullptr);
+  const int incl = __shfl_sync(0xffffffffu, bs.incl, b);
+  const int pages = __shfl_sync(0xffffffffu, bs.pages, b);
+  int k0 = 0, cnt = 0;
+  if (pages > 0) {
+    const int N = used_slots(cp.num_slots, bs.total);
+    k0 = slot_of(incl - pages, bs.total, N) + b;
+    cnt = slot_of(incl - 1, bs.total, N) + b - k0 + 1;
+  }
+  first = (static_cast<size_t>(hq) * cp.kseg + k0) * kNW;
+  S = cnt * kNW;
+}
+__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const WeightsParams p) {
+  __shared__ float lse_s[8];
+  const int pair = blockIdx.y, b = pair / p.Hkv, kvh = pair - b * p.Hkv;
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  grid_dependency_wait();
+  const int L = seq_len_of(p.cp.seq_lens, b, p.cp.max_blocks, nullptr, false);
+  const int lo = (p.cp.window > 0 && L > p.cp.window) ? L - p.cp.window : 0;
+  const int t0 = blockIdx.x * kWeightTokens;
+  if (t0 >= L) return;
+  if (wid < p.g) {
+    size_t first;
+    int S;
+    row_partials(p.cp, b, kvh * p.g + wid, lane, first, S);
+    float m = -INFINITY;
+    for (int s = lane; s < S; s += 32) m = fmaxf(m, __ldg(p.lse_part + first + s));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float sum = 0.f;
+    if (m != -INFINITY)
+      for (int s = lane; s < S; s += 32) sum += ex2(__ldg(p.lse_part + first + s) - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // a head that attends to nothing: every score is -inf, and 2^(-inf - 0) = 0
+    if (lane == 0) lse_s[wid] = sum > 0.f ? m + log2f(sum) : 0.f;
+  }
+  __syncthreads();
+  const int t1 = min(t0 + kWeightTokens, L);
+  float* w = p.weights + static_cast<size_t>(pair) * p.stride;
+  const float* sc = p.scores + static_cast<size_t>(pair) * p.cp.max_blocks * kPage * p.gp;
+  for (int t = t0 + threadIdx.x; t < t1; t += kWeightThreads) {
+    if (t < lo && p.decay == 1.f) continue;
+    float a = w[t] * p.decay;
+    if (t >= lo) {
+      float sum = 0.f;
+      for (int h = 0; h < p.g; h += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(sc + static_cast<size_t>(t) * p.gp + h);
+        sum += ex2(x.x - lse_s[h]);
+        if (h + 1 < p.g) sum += ex2(x.y - lse_s[h + 1]);
+      }
+      a += sum;
+    }
+    w[t] = a;
+  }
+}
+
 int decode_pages(int P, int max_blocks, int window) {
   int pages = max_blocks;
   if (window > 0) {
@@ -1236,11 +1334,13 @@ size_t partial_count(int B, int Hq, int S) {
   return static_cast<size_t>(B) * Hq * S * kNW;
 }
 
-template <int D, bool FP8, bool E5 = false, bool PT = false, bool SL = false, bool AP = false, bool BAL = false>
-kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream_t s) {
+template <int D, bool FP8, bool E5 = false, bool PT = false, bool SL = false, bool AP = false, bool BAL = false,
+          bool SC = false>
+kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream_t s,
+                           WeightsParams* weights = nullptr, bool partials_only = false) {
   constexpr int NST = stages_for<D, FP8, PT>();
   constexpr size_t smem = decode_smem_bytes<D, FP8, NST, PT>();
-  auto kern = decode_partial_kernel<D, FP8, kNW, NST, E5, PT, SL, AP, BAL>;
+  auto kern = decode_partial_kernel<D, FP8, kNW, NST, E5, PT, SL, AP, BAL, SC>;
   static int configured_mask = 0;  // devices whose attribute is set
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1256,7 +1356,8 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
   q.out = out;
   // one page range per (sequence, KV head) and every item in its own CTA: the
   // CTAs write the output themselves
-  q.direct = (p.num_splits == 1 && p.num_items <= grid) ? 1 : 0;
+  // (the weights need the partials' log-sum-exps)
+  q.direct = (!SC && !partials_only && p.num_splits == 1 && p.num_items <= grid) ? 1 : 0;
   if (grid > p.num_items) grid = p.num_items;
   // A grid smaller than the resident capacity asks for enough shared memory
   // that at most ceil(grid / SMs) CTAs fit on one SM: its CTAs then spread
@@ -1279,7 +1380,7 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, q);
   if (e != cudaSuccess) return cuda_status(e, "decode partial launch");
-  if (q.direct) return KVQ_OK;
+  if (q.direct || partials_only) return KVQ_OK;
   cfg.gridDim = dim3(p.B * p.Hq, D / 32);
   cfg.dynamicSmemBytes = 0;
   CombinePlan cp;
@@ -1310,6 +1411,14 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
     cfg.blockDim = dim3(32 * 32);
     e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<32>, op, lp, out, cp, D);
   }
+  if constexpr (SC) {
+    if (e != cudaSuccess) return cuda_status(e, "decode combine launch");
+    weights->cp = cp;
+    cfg.gridDim = dim3((p.max_blocks * kPage + kWeightTokens - 1) / kWeightTokens, p.B * p.Hkv);
+    cfg.blockDim = dim3(kWeightThreads);
+    e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, *weights);
+    return cuda_status(e, "decode weights launch");
+  }
   return cuda_status(e, "decode combine launch");
 }
 
@@ -1318,6 +1427,53 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
 }  // namespace kvq
 
 using namespace kvq;
+
+// The per-sequence plan's partials without the combine (a caller with further
+// partials of the same rows merges them itself).
+DecodePartialPlan kvq::decode_partial_plan(int B, int Hq, int Hkv, int D, int max_blocks) {
+  int S, pps;
+  split_plan(B, Hkv, D, kPage, max_blocks, -1, 0, &S, &pps);
+  DecodePartialPlan d;
+  d.splits = S;
+  d.per_row = S * kNW;
+  d.rows = static_cast<size_t>(B) * Hq * S * kNW;
+  return d;
+}
+
+kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, cudaStream_t s) {
+  DecodeParams prm = {};
+  prm.q = a.q;
+  prm.k_cache = a.k_cache;
+  prm.v_cache = a.v_cache;
+  prm.k_scale = a.k_scale;
+  prm.v_scale = a.v_scale;
+  prm.block_table = a.block_table;
+  prm.seq_lens = a.seq_lens;
+  prm.o_part = a.o_part;
+  prm.lse_part = a.lse_part;
+  prm.B = a.B;
+  prm.Hq = a.Hq;
+  prm.Hkv = a.Hkv;
+  prm.g = a.Hq / a.Hkv;
+  prm.max_blocks = a.max_blocks;
+  prm.num_blocks = a.num_blocks;
+  prm.sm_scale = a.sm_scale;
+  prm.window = -1;
+  prm.num_splits = a.splits;
+  prm.num_items = a.B * a.Hkv * a.splits;
+  prm.dev_status = a.dev_status;
+  prm.stall_ns = stall_ns();
+  const int64_t page_b = static_cast<int64_t>(kPage) * a.D;
+  const PageStrides ps = page_strides(a.k_cache, a.v_cache, page_b, page_b);
+  prm.k_str = ps.k;
+  prm.v_str = ps.v;
+  prm.paired = ps.paired ? 1 : 0;
+  if (a.e5m2)
+    return a.D == 128 ? launch_decode<128, true, true>(prm, nullptr, s, nullptr, true)
+                      : launch_decode<64, true, true>(prm, nullptr, s, nullptr, true);
+  return a.D == 128 ? launch_decode<128, true>(prm, nullptr, s, nullptr, true)
+                    : launch_decode<64, true>(prm, nullptr, s, nullptr, true);
+}
 
 extern "C" int kvq_decode_num_splits(int B, int Hkv, int D, int P, int max_blocks, int window, int num_splits) {
   if (B < 1 || Hkv < 1 || D < 1 || P < 1 || max_blocks < 1 || num_splits < 0) return 0;
@@ -1345,6 +1501,19 @@ struct AppendArgs {
   const int64_t* slot_new;
 };
 
+// The weights of each cached token for the weights entry point.
+struct WeightsArgs {
+  float* weights;
+  int64_t stride;
+  float decay;
+};
+
+int even_group(int g) { return g + (g & 1); }
+// Bytes of the base-2 scores [B][Hkv][max_blocks * P][even group].
+size_t score_bytes(int B, int Hq, int Hkv, int max_blocks) {
+  return static_cast<size_t>(B) * Hkv * max_blocks * kPage * even_group(Hq / Hkv) * sizeof(float);
+}
+
 // Shared by the per-head and the per-token entry points.  per_token: the
 // scales sit in the tail of each V page; k_scale and v_scale are unused.
 kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -1352,7 +1521,7 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
                           int Hq, int Hkv, int D, int P, int max_blocks, int64_t num_blocks, float sm_scale, int window,
                           kvq_dtype_t cache_dtype, int num_splits, void* workspace, size_t workspace_bytes,
                           int* dev_status, kvq_stream_t stream, bool per_token, bool single_level = false,
-                          const AppendArgs* app = nullptr) {
+                          const AppendArgs* app = nullptr, const WeightsArgs* wts = nullptr) {
   if (B < 1 || Hq < 1 || Hkv < 1 || max_blocks < 1 || num_blocks < 1 || num_splits < 0)
     return fail(KVQ_ERR_INVALID_ARG, "paged_decode: bad sizes");
   if (Hq % Hkv != 0) return fail(KVQ_ERR_INVALID_ARG, "paged_decode: Hq %% Hkv != 0");
@@ -1376,9 +1545,23 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(workspace, 16) ||
       !aligned(out, 4))
     return fail(KVQ_ERR_INVALID_ARG, "paged_decode: misaligned pointer");
+  if (wts) {
+    if (!wts->weights || !aligned(wts->weights, 4))
+      return fail(KVQ_ERR_INVALID_ARG, "paged_decode_weights: weights null or misaligned");
+    if (wts->stride < static_cast<int64_t>(max_blocks) * P)
+      return fail(KVQ_ERR_INVALID_ARG, "paged_decode_weights: weights_stride %lld < max_blocks * P",
+                  static_cast<long long>(wts->stride));
+    if (!(wts->decay >= 0.f) || !(wts->decay <= 1.f))
+      return fail(KVQ_ERR_INVALID_ARG, "paged_decode_weights: decay must be in [0, 1]");
+    if (static_cast<int64_t>(B) * Hkv > 65535)
+      return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: more than 65535 (sequence, KV head) pairs");
+    if (static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFF - kWeightTokens)
+      return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: block table too long");
+  }
   int S, pps;
   split_plan(B, Hkv, D, P, max_blocks, window, num_splits, &S, &pps);
-  const size_t need = kvq_decode_workspace_size(B, Hq, Hkv, D, P, max_blocks, window, num_splits);
+  const size_t partial_bytes = kvq_decode_workspace_size(B, Hq, Hkv, D, P, max_blocks, window, num_splits);
+  const size_t need = partial_bytes + (wts ? score_bytes(B, Hq, Hkv, max_blocks) : 0);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_INVALID_ARG, "paged_decode: workspace %zu bytes < %zu needed", workspace_bytes, need);
   const long items = static_cast<long>(B) * Hkv * S;
@@ -1418,6 +1601,8 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   prm.k_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(k_cache)) : nullptr;
   prm.v_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(v_cache)) : nullptr;
   prm.stall_ns = stall_ns();
+  prm.scores = wts ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + partial_bytes) : nullptr;
+  prm.gp = even_group(prm.g);
   {
     const int64_t page_b = static_cast<int64_t>(kPage) * D * (fp8 ? 1 : 2);
     const PageStrides ps = page_strides(k_cache, v_cache, page_b, page_b + (per_token ? kScaleTailBytes : 0));
@@ -1428,6 +1613,34 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto o = static_cast<__nv_bfloat16*>(out);
   const bool e5 = cache_dtype == KVQ_DTYPE_FP8_E5M2;
+  if (wts) {
+    WeightsParams wp;
+    wp.scores = prm.scores;
+    wp.lse_part = prm.lse_part;
+    wp.weights = wts->weights;
+    wp.stride = wts->stride;
+    wp.decay = wts->decay;
+    wp.Hkv = Hkv;
+    wp.g = prm.g;
+    wp.gp = prm.gp;
+    if (per_token) {
+      if (D == 128)
+        return e5 ? launch_decode<128, true, true, true, false, false, false, true>(prm, o, s, &wp)
+                  : launch_decode<128, true, false, true, false, false, false, true>(prm, o, s, &wp);
+      return e5 ? launch_decode<64, true, true, true, false, false, false, true>(prm, o, s, &wp)
+                : launch_decode<64, true, false, true, false, false, false, true>(prm, o, s, &wp);
+    }
+    if (e5)
+      return D == 128 ? launch_decode<128, true, true, false, false, false, false, true>(prm, o, s, &wp)
+                      : launch_decode<64, true, true, false, false, false, false, true>(prm, o, s, &wp);
+    if (D == 128) {
+      if (prm.balanced) return launch_decode<128, true, false, false, false, false, true, true>(prm, o, s, &wp);
+      return fp8 ? launch_decode<128, true, false, false, false, false, false, true>(prm, o, s, &wp)
+                 : launch_decode<128, false, false, false, false, false, false, true>(prm, o, s, &wp);
+    }
+    return fp8 ? launch_decode<64, true, false, false, false, false, false, true>(prm, o, s, &wp)
+               : launch_decode<64, false, false, false, false, false, false, true>(prm, o, s, &wp);
+  }
   if (single_level) {
     if (cache_dtype != KVQ_DTYPE_FP8_E4M3 || per_token)
       return fail(KVQ_ERR_UNSUPPORTED, "paged_decode: single-level accumulation covers E4M3 per-head caches");
@@ -1509,6 +1722,25 @@ extern "C" kvq_status_t kvq_paged_decode_attention_per_token(
   return paged_decode(q, k_cache, v_cache, nullptr, nullptr, block_table, seq_lens, out, B, Hq, Hkv, D, P,
                       max_blocks, num_blocks, sm_scale, window, cache_dtype, num_splits, workspace, workspace_bytes,
                       dev_status, stream, true);
+}
+
+extern "C" size_t kvq_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks, int window,
+                                                    int num_splits) {
+  const size_t n = kvq_decode_workspace_size(B, Hq, Hkv, D, P, max_blocks, window, num_splits);
+  return n == 0 || Hq % Hkv != 0 ? 0 : n + score_bytes(B, Hq, Hkv, max_blocks);
+}
+
+extern "C" kvq_status_t kvq_paged_decode_attention_weights(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* block_table, const int32_t* seq_lens, void* out, float* weights, int64_t weights_stride, float decay,
+    int B, int Hq, int Hkv, int D, int P, int max_blocks, int64_t num_blocks, float sm_scale, int window,
+    kvq_dtype_t cache_dtype, int per_token, int num_splits, void* workspace, size_t workspace_bytes, int* dev_status,
+    kvq_stream_t stream) {
+  clear_error();
+  const WeightsArgs wts{weights, weights_stride, decay};
+  return paged_decode(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, B, Hq, Hkv, D, P,
+                      max_blocks, num_blocks, sm_scale, window, cache_dtype, num_splits, workspace, workspace_bytes,
+                      dev_status, stream, per_token != 0, false, nullptr, &wts);
 }
 
 // ---------------------------------------------------------------------------

@@ -1,0 +1,462 @@
+// kvq_evict_tokens: cut each sequence's cache to its heaviest tokens.
+//
+// Two kernels.  Selection: per (sequence, KV head), the n - s - r largest of
+// the L - s - r weights between the protected first s and last r tokens, ties
+// to the lowest position: a radix selection of the threshold (11, 11 and 10
+// bits of an order-preserving integer image of the weight), then an ordered
+// compaction of the positions.  Move: the kept tokens' K rows and V columns
+// are copied into the destination pages.
+#include <cooperative_groups.h>
+
+#include "kvq_device.cuh"
+#include "kvq_host.h"
+
+namespace kvq {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+struct EvictParams {
+  const float* weights;
+  int64_t weights_stride;
+  uint8_t* k_cache;
+  uint8_t* v_cache;
+  int64_t k_str, v_str;  // bytes between consecutive (block, KV head) pages of each cache
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* keep_lens;
+  const int32_t* dst_table;
+  float* dst_weights;
+  int64_t dst_stride;
+  int32_t* dst_lens;
+  int32_t* kept;  // [B][Hkv][max_dst * P] source positions, ascending
+  int Hkv, max_blocks, max_dst;
+  int64_t num_blocks;
+  int sink, recent;
+  int seg_cap;  // keys of a CTA's segment held in shared memory (0: read from global memory each pass)
+  int* dev_status;
+};
+
+// ------------------------------------------------------------- selection ---
+constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+
+// Order-preserving image of a weight: a < b <=> image(a) < image(b); the two
+// zeros are equal, NaN ranks below everything.
+KVQ_DEVINL uint32_t weight_key(float x) {
+  uint32_t u = __float_as_uint(x);
+  if (x != x) return 0u;
+  if (u == 0x80000000u) u = 0u;
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+// What sequence b keeps: L tokens cut to n, of which the first s and the last
+// r are protected.
+struct Cut {
+  int L, n, s, r;
+};
+KVQ_DEVINL Cut cut_of(const EvictParams& p, int b, bool report) {
+  Cut c;
+  c.L = p.seq_lens[b];
+  const int cap = p.max_blocks * kPage, dst_cap = p.max_dst * kPage;
+  bool bad = false;
+  if (c.L < 0 || c.L > cap) {
+    bad = true;
+    c.L = c.L < 0 ? 0 : cap;
+  }
+  int keep = p.keep_lens[b];
+  if (keep < 0) {
+    bad = true;
+    keep = 0;
+  }
+  c.n = min(c.L, keep);
+  if (c.n > dst_cap) {
+    bad = true;
+    c.n = dst_cap;
+  }
+  if (bad && report) set_status(p.dev_status, KVQ_DEV_BAD_SEQLEN);
+  c.s = min(p.sink, c.n);
+  c.r = min(p.recent, c.n - c.s);
+  return c;
+}
+
+// Exclusive prefix over the warp of x; total in the last argument.
+KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
+  int v = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  total = __shfl_sync(0xffffffffu, v, 31);
+  return v - x;
+}
+
+// Grid (cluster size, Hkv, B), one cluster per (sequence, KV head): CTA k of C
+// owns the k-th of C equal segments of the candidate positions.  Histograms
+// and counts meet through distributed shared memory.
+__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
+  extern __shared__ __align__(16) uint32_t dyn[];
+  uint32_t* keys = dyn;  // [seg_cap]
+  __shared__ uint32_t hist[kBins];
+  __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
+  __shared__ int totals[2];  // this CTA's counts above and at the threshold, read by the cluster
+  __shared__ uint32_t found[2];  // chosen bin, keys still needed inside it
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = static_cast<int>(cluster.num_blocks());
+  const int rank = static_cast<int>(cluster.block_rank());
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  grid_dependency_wait();
+  const Cut cut = cut_of(p, b, tid == 0 && rank == 0 && h == 0);
+  const size_t pair = static_cast<size_t>(b) * p.Hkv + h;
+  const float* w = p.weights + pair * p.weights_stride;
+  float* dw = p.dst_weights + pair * p.dst_stride;
+  int32_t* kept = p.kept + pair * p.max_dst * kPage;
+  const int N = cut.L - cut.r - cut.s;   // candidates
+  const int m = cut.n - cut.r - cut.s;   // chosen among them
+  if (rank == 0 && h == 0 && tid == 0) p.dst_lens[b] = cut.n;
+  const int gtid = rank * kSelThreads + tid, gthreads = C * kSelThreads;
+  // the protected ends, and zeros behind the kept tokens
+  for (int i = gtid; i < cut.s; i += gthreads) {
+    kept[i] = i;
+    dw[i] = w[i];
+  }
+  for (int i = gtid; i < cut.r; i += gthreads) {
+    const int src = cut.L - cut.r + i, pos = cut.n - cut.r + i;
+    kept[pos] = src;
+    dw[pos] = w[src];
+  }
+  for (int64_t i = cut.n + gtid; i < p.dst_stride; i += gthreads) dw[i] = 0.f;
+  if (m <= 0) return;  // uniform over the cluster
+  if (m == N) {
+    for (int i = gtid; i < N; i += gthreads) {
+      kept[cut.s + i] = cut.s + i;
+      dw[cut.s + i] = w[cut.s + i];
+    }
+    return;
+  }
+  const int seg = (N + C - 1) / C;
+  const int i0 = min(N, rank * seg), i1 = min(N, i0 + seg), len = i1 - i0;
+  const float* wseg = w + cut.s + i0;
+  const bool held = len <= p.seg_cap;
+  if (held)
+    for (int i = tid; i < len; i += kSelThreads) keys[i] = weight_key(wseg[i]);
+  auto key_at = [&](int i) { return held ? keys[i] : weight_key(wseg[i]); };
+
+  // threshold: the m-th largest key, digit by digit from the top
+  uint32_t prefix = 0, mask = 0;
+  int need = m;
+  constexpr int kShift[3] = {21, 10, 0};
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = kShift[pass], bins = pass < 2 ? 2048 : 1024;
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < len; i += kSelThreads) {
+      const uint32_t k = key_at(i);
+      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    }
+    cluster.sync();
+    // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
+    uint32_t c0 = 0, c1 = 0;
+    const int hi = kBins - 1 - 2 * tid;
+    for (int k = 0; k < C; ++k) {
+      const uint32_t* other = cluster.map_shared_rank(hist, k);
+      c0 += other[hi];
+      c1 += other[hi - 1];
+    }
+    int tot;
+    const int excl = warp_scan_excl(static_cast<int>(c0 + c1), lane, tot);
+    if (lane == 0) warp_gt[wid] = tot;
+    __syncthreads();
+    int before = excl;
+    {
+      int all;
+      const int wx = warp_scan_excl(warp_gt[lane], lane, all);
+      before += __shfl_sync(0xffffffffu, wx, wid);
+    }
+    if (before < need && before + static_cast<int>(c0 + c1) >= need) {  // exactly one thread
+      const bool first = before + static_cast<int>(c0) >= need;
+      found[0] = first ? hi : hi - 1;
+      found[1] = need - (first ? before : before + static_cast<int>(c0));
+    }
+    cluster.sync();  // every CTA has read this histogram; found is set
+    prefix |= found[0] << shift;
+    mask |= static_cast<uint32_t>(bins - 1) << shift;
+    need = static_cast<int>(found[1]);
+  }
+  // prefix is the threshold; of the keys equal to it the first `need` are taken
+  const int sub = (((len + kSelWarps - 1) / kSelWarps) + 31) / 32 * 32;
+  const int j0 = min(len, wid * sub), j1 = min(len, j0 + sub);
+  int gt = 0, eq = 0;
+  for (int j = j0; j < j1; j += 32) {
+    const int i = j + lane;
+    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < j1 && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i < j1 && k == prefix));
+  }
+  if (lane == 0) {
+    warp_gt[wid] = gt;
+    warp_eq[wid] = eq;
+  }
+  __syncthreads();
+  int gt_all, eq_all;
+  const int gx = warp_scan_excl(warp_gt[lane], lane, gt_all), ex = warp_scan_excl(warp_eq[lane], lane, eq_all);
+  if (tid == 0) {
+    totals[0] = gt_all;
+    totals[1] = eq_all;
+  }
+  cluster.sync();
+  int gt_before = __shfl_sync(0xffffffffu, gx, wid), eq_before = __shfl_sync(0xffffffffu, ex, wid);
+  for (int k = 0; k < rank; ++k) {
+    const int* other = cluster.map_shared_rank(totals, k);
+    gt_before += other[0];
+    eq_before += other[1];
+  }
+  cluster.sync();  // no CTA leaves while its totals may be read
+  const uint32_t below = (1u << lane) - 1u;
+  for (int j = j0; j < j1; j += 32) {
+    const int i = j + lane;
+    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    const uint32_t g = __ballot_sync(0xffffffffu, i < j1 && k > prefix);
+    const uint32_t e = __ballot_sync(0xffffffffu, i < j1 && k == prefix);
+    const int eq_rank = eq_before + __popc(e & below);
+    const bool take = ((g >> lane) & 1u) || (((e >> lane) & 1u) && eq_rank < need);
+    if (take) {
+      const int pos = cut.s + gt_before + __popc(g & below) + min(eq_rank, need);
+      kept[pos] = cut.s + i0 + i;
+      dw[pos] = wseg[i];
+    }
+    gt_before += __popc(g);
+    eq_before += __popc(e);
+  }
+}
+
+// ------------------------------------------------------------------ move ---
+constexpr int kMoveWarps = 4;
+
+// One warp per (sequence, KV head, destination page).  K: 16-byte chunks, row
+// by row, each swizzled for its source and its destination row.  V: a lane per
+// dimension row; the row's 16 tokens come from up to 16 source pages, one
+// 32-bit word each, and are put together with byte permutes.
+template <int D, int ESZ, bool PT>
+__global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int ROWB = D * ESZ;
+  constexpr int CH = ROWB / 16;           // chunks per K row
+  constexpr int PAGE_BYTES = kPage * ROWB;
+  const int lane = threadIdx.x & 31;
+  const int h = blockIdx.y, b = blockIdx.z;
+  const int page = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
+  grid_dependency_wait();
+  const int n = p.dst_lens[b];
+  if (page * kPage >= n) return;
+  const size_t pair = static_cast<size_t>(b) * p.Hkv + h;
+  const int dst_blk = p.dst_table[static_cast<size_t>(b) * p.max_dst + page];
+  if (dst_blk < 0 || static_cast<int64_t>(dst_blk) >= p.num_blocks) {
+    if (lane == 0) set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+    return;
+  }
+  // lane t < 16: token t's source page (block * Hkv + h) and offset in it
+  int64_t src_page = -1;
+  int src_off = 0;
+  if (lane < kPage && page * kPage + lane < n) {
+    const int pos = p.kept[pair * p.max_dst * kPage + page * kPage + lane];
+    const int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPage];
+    src_off = pos % kPage;
+    if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks)
+      set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+    else
+      src_page = static_cast<int64_t>(blk) * p.Hkv + h;
+  }
+  const uint32_t live = __ballot_sync(0xffffffffu, src_page >= 0);
+  const int64_t dst_page = static_cast<int64_t>(dst_blk) * p.Hkv + h;
+  auto k_off = [](int t, int j) { return ESZ == 1 ? fp8_k_offset(t, j, D) : k_chunk_offset(t, j, ROWB); };
+  uint8_t* kd = p.k_cache + dst_page * p.k_str;
+  uint8_t* vd = p.v_cache + dst_page * p.v_str;
+#pragma unroll
+  for (int u = 0; u < kPage * CH / 32; ++u) {
+    const int t = (u * 32 + lane) / CH, j = (u * 32 + lane) % CH;
+    const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
+    const int so = __shfl_sync(0xffffffffu, src_off, t);
+    if (sp >= 0)
+      *reinterpret_cast<uint4*>(kd + k_off(t, j)) =
+          *reinterpret_cast<const uint4*>(p.k_cache + sp * p.k_str + k_off(so, j));
+  }
+  constexpr int WORDS = kPage * ESZ / 4;  // 32-bit words of a V row
+  for (int d = lane; d < D; d += 32) {
+    uint32_t row[WORDS];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(vd + d * kPage * ESZ);
+    if (live != 0xFFFFu) {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) row[i] = dst[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < WORDS; ++i) row[i] = 0u;
+    }
+#pragma unroll
+    for (int t = 0; t < kPage; ++t) {
+      const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
+      const int so = __shfl_sync(0xffffffffu, src_off, t);
+      if (sp < 0) continue;  // uniform
+      const int from = ESZ == 1 ? d * kPage + fp8_v_slot(so) : bf16_v_offset(d, so);
+      const uint32_t word = *reinterpret_cast<const uint32_t*>(p.v_cache + sp * p.v_str + (from & ~3));
+      const uint32_t at = from & 3;
+      if constexpr (ESZ == 1) {
+        const int slot = fp8_v_slot(t);  // compile time
+        const uint32_t sel = (0x3210u & ~(0xFu << (4 * (slot & 3)))) | ((4u + at) << (4 * (slot & 3)));
+        row[slot >> 2] = __byte_perm(row[slot >> 2], word, sel);
+      } else {
+        // the halves of the row swap with d: the word index depends on the lane
+        const uint32_t pair_sel = at ? 0x76u : 0x54u;
+        const uint32_t sel = (t & 1) ? (0x0010u | (pair_sel << 8)) : (0x3200u | pair_sel);
+        const bool swap = (d >> 2) & 1;
+        const int w0 = (t >> 1), w1 = (t >> 1) ^ 4;
+        if (!swap) row[w0] = __byte_perm(row[w0], word, sel);
+        else row[w1] = __byte_perm(row[w1], word, sel);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4)
+      *reinterpret_cast<uint4*>(dst + i) = make_uint4(row[i], row[i + 1], row[i + 2], row[i + 3]);
+  }
+  if constexpr (PT) {
+    if (src_page >= 0) {
+      const float* st = reinterpret_cast<const float*>(p.v_cache + src_page * p.v_str + PAGE_BYTES);
+      float* dt = reinterpret_cast<float*>(vd + PAGE_BYTES);
+      dt[lane] = st[src_off];
+      dt[kPage + lane] = st[kPage + src_off];
+    }
+  }
+}
+
+constexpr int kMaxCluster = 8;
+constexpr int kKeysMax = 48 * 1024;  // keys a CTA holds in shared memory (192 KiB)
+
+// CTAs per (sequence, KV head): a cluster large enough that a CTA's segment is
+// at most 4,096 candidates.
+int select_cluster(int64_t tokens) {
+  int c = 1;
+  while (c < kMaxCluster && tokens > 4096ll * c) c *= 2;
+  return c;
+}
+
+template <int D, int ESZ, bool PT>
+cudaError_t launch_move(cudaLaunchConfig_t cfg, const EvictParams& p) {
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel<D, ESZ, PT>, p);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_stride, void* k_cache, void* v_cache,
+                                         const int32_t* block_table, const int32_t* seq_lens,
+                                         const int32_t* keep_lens, const int32_t* dst_block_table, float* dst_weights,
+                                         int64_t dst_weights_stride, int32_t* dst_seq_lens, int32_t* kept, int B,
+                                         int Hkv, int D, int P, int max_blocks, int max_dst_blocks, int64_t num_blocks,
+                                         int sink, int recent, kvq_dtype_t cache_dtype, int per_token, int* dev_status,
+                                         kvq_stream_t stream) {
+  clear_error();
+  if (B < 1 || Hkv < 1 || max_blocks < 1 || max_dst_blocks < 1 || num_blocks < 1)
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: bad sizes");
+  if (sink < 0 || recent < 0) return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: sink and recent must be >= 0");
+  if (P != kPage) return fail(KVQ_ERR_UNSUPPORTED, "evict_tokens: page size %d (only 16)", P);
+  if (cache_dtype != KVQ_DTYPE_FP8_E4M3 && cache_dtype != KVQ_DTYPE_FP8_E5M2 && cache_dtype != KVQ_DTYPE_BF16)
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: bad cache dtype");
+  const bool fp8 = cache_dtype != KVQ_DTYPE_BF16;
+  if (per_token && !fp8) return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: per-token scales need an FP8 cache");
+  if (D != 64 && D != 128 && !(fp8 && !per_token && D == 256))
+    return fail(KVQ_ERR_UNSUPPORTED, "evict_tokens: head_dim %d (64 or 128; 256 for FP8 with per-head scales)", D);
+  if (B > 65535 || Hkv > 65535) return fail(KVQ_ERR_UNSUPPORTED, "evict_tokens: grid too large");
+  const int64_t cap = static_cast<int64_t>(max_blocks) * P, dst_cap = static_cast<int64_t>(max_dst_blocks) * P;
+  if (cap > 0x7FFFFFFFll - 65536 || dst_cap > 0x7FFFFFFFll - 65536)
+    return fail(KVQ_ERR_UNSUPPORTED, "evict_tokens: block table too long");
+  if (weights_stride < cap || dst_weights_stride < dst_cap)
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: a weights row is shorter than its block table");
+  if (!weights || !k_cache || !v_cache || !block_table || !seq_lens || !keep_lens || !dst_block_table || !dst_weights ||
+      !dst_seq_lens || !kept)
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: null pointer");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(weights, 4) || !aligned(dst_weights, 4) ||
+      !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(keep_lens, 4) || !aligned(dst_block_table, 4) ||
+      !aligned(dst_seq_lens, 4) || !aligned(kept, 4))
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: misaligned pointer");
+  const size_t pairs = static_cast<size_t>(B) * Hkv;
+  if (overlap(weights, pairs * weights_stride * 4, dst_weights, pairs * dst_weights_stride * 4) ||
+      overlap(seq_lens, size_t(B) * 4, dst_seq_lens, size_t(B) * 4) ||
+      overlap(keep_lens, size_t(B) * 4, dst_seq_lens, size_t(B) * 4))
+    return fail(KVQ_ERR_INVALID_ARG, "evict_tokens: an output overlaps an input");
+  EvictParams p;
+  p.weights = weights;
+  p.weights_stride = weights_stride;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  const int64_t page_b = static_cast<int64_t>(kPage) * D * (fp8 ? 1 : 2);
+  const PageStrides ps = page_strides(k_cache, v_cache, page_b, page_b + (per_token ? kScaleTailBytes : 0));
+  p.k_str = ps.k;
+  p.v_str = ps.v;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.keep_lens = keep_lens;
+  p.dst_table = dst_block_table;
+  p.dst_weights = dst_weights;
+  p.dst_stride = dst_weights_stride;
+  p.dst_lens = dst_seq_lens;
+  p.kept = kept;
+  p.Hkv = Hkv;
+  p.max_blocks = max_blocks;
+  p.max_dst = max_dst_blocks;
+  p.num_blocks = num_blocks;
+  p.sink = sink;
+  p.recent = recent;
+  p.dev_status = dev_status;
+  const int C = select_cluster(cap);
+  const int64_t seg = (cap + C - 1) / C;
+  p.seg_cap = seg <= kKeysMax ? static_cast<int>(seg) : 0;
+  static int configured_mask = 0;  // devices whose attribute is set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(configured_mask & (1 << (dev & 31)))) {
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+    if (e != cudaSuccess) return cuda_status(e, "evict_tokens: set shared memory size");
+    configured_mask |= 1 << (dev & 31);
+  }
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = C;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C, Hkv, B);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(p.seg_cap) * 4;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  if (e != cudaSuccess) return cuda_status(e, "evict_tokens select launch");
+  cfg.gridDim = dim3((max_dst_blocks + kMoveWarps - 1) / kMoveWarps, Hkv, B);
+  cfg.blockDim = dim3(kMoveWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  if (!fp8)
+    e = D == 128 ? launch_move<128, 2, false>(cfg, p) : launch_move<64, 2, false>(cfg, p);
+  else if (per_token)
+    e = D == 128 ? launch_move<128, 1, true>(cfg, p) : launch_move<64, 1, true>(cfg, p);
+  else
+    e = D == 256   ? launch_move<256, 1, false>(cfg, p)
+        : D == 128 ? launch_move<128, 1, false>(cfg, p)
+                   : launch_move<64, 1, false>(cfg, p);
+  return cuda_status(e, "evict_tokens move launch");
+}

@@ -33,4 +33,26 @@ inline PageStrides page_strides(const void* k_cache, const void* v_cache, int64_
   return paired ? PageStrides{k_page + v_page, k_page + v_page, true} : PageStrides{k_page, v_page, false};
 }
 
+// The split-KV partials of an FP8 decode (per-head scales, no window) without
+// their combine: float32 [B][Hq][per_row][D] outputs and [B][Hq][per_row]
+// base-2 log-sum-exps.
+struct DecodePartialPlan {
+  int splits, per_row;
+  size_t rows;
+};
+DecodePartialPlan decode_partial_plan(int B, int Hq, int Hkv, int D, int max_blocks);
+struct DecodePartialArgs {
+  const void* q;
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *seq_lens;
+  float *o_part, *lse_part;
+  int B, Hq, Hkv, D, max_blocks, splits;
+  int64_t num_blocks;
+  float sm_scale;
+  bool e5m2;
+  int* dev_status;
+};
+kvq_status_t decode_partials(const DecodePartialArgs& a, cudaStream_t s);
+
 }  // namespace kvq

@@ -121,6 +121,7 @@ typedef enum kvq_accumulation {
 #define KVQ_DEV_BAD_SEQLEN   0x4  /* seq_len < 0 or > max_blocks * P: clamped */
 #define KVQ_DEV_TIMEOUT      0x8  /* a pipeline wait exceeded its bound: work abandoned */
 #define KVQ_DEV_BAD_QROWS    0x10 /* prefill: new tokens exceed seq_len: rows skipped */
+#define KVQ_DEV_BAD_GROUP    0x20 /* shared prefix: group_starts decreasing or outside [0, B]: clamped */
 
 typedef void* kvq_stream_t;   /* cudaStream_t */
 
@@ -384,6 +385,125 @@ kvq_status_t kvq_paged_decode_attention_per_token(const void* q, const void* k_c
                                                   int window, kvq_dtype_t cache_dtype, int num_splits,
                                                   void* workspace, size_t workspace_bytes,
                                                   int* dev_status, kvq_stream_t stream);
+
+/*
+ * kvq_paged_decode_attention_shared_prefix -- one decode step for sequences
+ * that share a prefix (a system prompt, a document, a beam's history): the
+ * prefix is read and contracted once for all sequences of its group instead
+ * of once per sequence.  [GTNT] section 6 (PagedAttention: pages shared
+ * between sequences).
+ *
+ * The batch is G groups of consecutive sequences: group i is sequences
+ * group_starts[i] .. group_starts[i + 1] - 1 and its prefix is the first
+ * prefix_lens[i] tokens of the pages prefix_table[i].  Sequence b attends to
+ * its group's prefix and to its own seq_lens[b] tokens of the pages
+ * block_table[b] (which start on a page of their own, whatever the prefix's
+ * length).  A sequence in no group attends to its own tokens only; one with
+ * nothing to attend to gives an all-zero output.
+ *
+ *  q             bf16 [B][Hq][D].  Query head h reads KV head h / (Hq / Hkv).
+ *  prefix_table  int32 [G][max_prefix_blocks].
+ *  prefix_lens   int32 [G]; negative or beyond the table: clamped and
+ *                KVQ_DEV_BAD_SEQLEN.
+ *  group_starts  int32 [G + 1], non-decreasing within [0, B]; otherwise
+ *                clamped and KVQ_DEV_BAD_GROUP.
+ *  Other arguments as for kvq_paged_decode_attention.  FP8 caches (E4M3 or
+ *  E5M2) with per-KV-head scales; D in {64, 128}, P == 16, Hq % Hkv == 0,
+ *  Hq / Hkv <= 8; G >= 1, max_prefix_blocks >= 1, max_blocks >= 1.
+ *  workspace     kvq_shared_prefix_workspace_size(...) bytes, 16-byte aligned;
+ *                contents on entry are ignored; calls sharing it must not
+ *                overlap.
+ *  The work split is a function of the lengths and groups alone: results are
+ *  deterministic.
+ */
+size_t kvq_shared_prefix_workspace_size(int B, int G, int Hq, int Hkv, int D, int P, int max_prefix_blocks,
+                                        int max_blocks);
+kvq_status_t kvq_paged_decode_attention_shared_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                                      const float* k_scale, const float* v_scale,
+                                                      const int32_t* prefix_table, const int32_t* prefix_lens,
+                                                      const int32_t* group_starts, const int32_t* block_table,
+                                                      const int32_t* seq_lens, void* out, int B, int G, int Hq,
+                                                      int Hkv, int D, int P, int max_prefix_blocks, int max_blocks,
+                                                      int64_t num_blocks, float sm_scale, kvq_dtype_t cache_dtype,
+                                                      void* workspace, size_t workspace_bytes, int* dev_status,
+                                                      kvq_stream_t stream);
+
+/*
+ * kvq_paged_decode_attention_weights -- kvq_paged_decode_attention that also
+ * accumulates how much weight each cached token drew: with p[b][h][j] the
+ * softmax weight of token j under query head h,
+ *   weights[b][kvh][j] = decay * weights[b][kvh][j] + sum_{h in group} p[b][h][j]
+ * for j < seq_lens[b] (p = 0 for tokens outside the window and in pages with
+ * an invalid block id); later entries are left as they were.  Accumulated over
+ * steps this is what kvq_evict_tokens ranks tokens by.  The pages have no
+ * counterpart.
+ *
+ *  weights         float32 [B][Hkv] rows, weights_stride floats apart
+ *                  (weights_stride >= max_blocks * P); read and written.  A
+ *                  token's entry starts at 0 when the token is cached.
+ *  decay           in [0, 1]; 1 = the plain sum.
+ *  per_token       nonzero: a cache of kvq_reshape_and_cache_per_token
+ *                  (k_scale and v_scale are ignored and may be NULL).
+ *  workspace       kvq_decode_weights_workspace_size(...) bytes: the decode's
+ *                  partials and float32 scores [B][Hkv][max_blocks * P][Hq /
+ *                  Hkv rounded up to even].
+ *  Other arguments, caches and the declared rounding as for
+ *  kvq_paged_decode_attention (and _per_token); the scores and sums behind
+ *  the weights are float32, and heads are added in order (no atomics), so
+ *  results are deterministic.  B * Hkv <= 65535.
+ */
+size_t kvq_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks, int window,
+                                         int num_splits);
+kvq_status_t kvq_paged_decode_attention_weights(const void* q, const void* k_cache, const void* v_cache,
+                                                const float* k_scale, const float* v_scale,
+                                                const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                                float* weights, int64_t weights_stride, float decay, int B, int Hq,
+                                                int Hkv, int D, int P, int max_blocks, int64_t num_blocks,
+                                                float sm_scale, int window, kvq_dtype_t cache_dtype, int per_token,
+                                                int num_splits, void* workspace, size_t workspace_bytes,
+                                                int* dev_status, kvq_stream_t stream);
+
+/*
+ * kvq_evict_tokens -- cut each sequence's cache to its heaviest tokens, per KV
+ * head, into other pages.  The pages have no counterpart.
+ *
+ * Sequence b with L = seq_lens[b] tokens keeps n = min(L, keep_lens[b]).  Of
+ * these the first s = min(sink, n) and the last r = min(recent, n - s) tokens
+ * are kept whatever their weight; the other n - s - r are, separately for each
+ * KV head, those of positions [s, L - r) with the largest weights (equal
+ * weights, +0 and -0 among them: the lowest position first; NaN ranks below
+ * -infinity).  Kept tokens stay in order and become tokens 0 .. n - 1 of the
+ * pages dst_block_table[b]; K, V and (per_token) scales move unchanged.
+ *
+ *  weights         float32 [B][Hkv] rows, weights_stride floats apart
+ *                  (>= max_blocks * P), as accumulated by
+ *                  kvq_paged_decode_attention_weights.
+ *  k_cache,        read through block_table, written through dst_block_table,
+ *  v_cache         any format of kvq_reshape_and_cache (per_token: of
+ *                  kvq_reshape_and_cache_per_token).  A source page may be
+ *                  shared between sequences and is not changed.  Destination
+ *                  pages must be distinct and no source page of the call.
+ *  keep_lens       int32 [B]; negative counts as 0 and sets KVQ_DEV_BAD_SEQLEN,
+ *                  as does n > max_dst_blocks * P, which is clamped.
+ *  dst_block_table int32 [B][max_dst_blocks].  A page with an invalid id is
+ *                  not written (KVQ_DEV_BAD_BLOCK), nor are tokens whose source
+ *                  page has one.  Slots behind token n - 1 are left as they were.
+ *  dst_weights     float32 [B][Hkv] rows, dst_weights_stride floats apart (>=
+ *                  max_dst_blocks * P): the kept tokens' weights, then zeros to
+ *                  the row's end (so that tokens appended later start at 0).
+ *  dst_seq_lens    int32 [B]: n.
+ *  kept            int32 [B][Hkv][max_dst_blocks * P]: the kept tokens' source
+ *                  positions, ascending; entries from n on are left as they were.
+ *  dst_weights and dst_seq_lens must not overlap weights, seq_lens or
+ *  keep_lens.  D in {64, 128} (and 256 for FP8 caches with per-head scales),
+ *  P == 16, B <= 65535, Hkv <= 65535.
+ */
+kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_stride, void* k_cache, void* v_cache,
+                              const int32_t* block_table, const int32_t* seq_lens, const int32_t* keep_lens,
+                              const int32_t* dst_block_table, float* dst_weights, int64_t dst_weights_stride,
+                              int32_t* dst_seq_lens, int32_t* kept, int B, int Hkv, int D, int P, int max_blocks,
+                              int max_dst_blocks, int64_t num_blocks, int sink, int recent, kvq_dtype_t cache_dtype,
+                              int per_token, int* dev_status, kvq_stream_t stream);
 
 /*
  * kvq_paged_decode_attention_static_scratch -- kvq_paged_decode_attention
