@@ -10,6 +10,7 @@
 
 #include "kvq_device.cuh"
 #include "kvq_host.h"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 
@@ -39,6 +40,9 @@ struct SharedParams {
   int max_units;  // bound of the batch's units
   int kseg;       // slots + max_units
   int* dev_status;
+  // failure-path test hook (kvq_debug_set_stall_ns): > 0 makes the softmax
+  // warps wait up to this long on a barrier nothing arrives on
+  uint64_t stall_ns;
 };
 
 // ------------------------------------------------------------------ plan ---
@@ -48,10 +52,10 @@ struct SharedParams {
 // batch's units are laid end to end and cut into equal slots, one per CTA; a
 // slot's part inside a unit is a segment.
 struct Group {
-  int a, nb;     // first sequence, sequences
+  int a, nb;        // first sequence, sequences
   int L, tiles, K;  // prefix tokens, row tiles, key tiles
-  int units;
-  int64_t cost;
+  KVQ_DEVINL int units() const { return (tiles + 1) / 2; }
+  KVQ_DEVINL int64_t cost() const { return static_cast<int64_t>(tiles) * K; }
 };
 KVQ_DEVINL Group group_of(const SharedParams& p, int i, bool report) {
   Group r;
@@ -73,8 +77,6 @@ KVQ_DEVINL Group group_of(const SharedParams& p, int i, bool report) {
   r.L = L;
   r.tiles = (r.nb * p.g + TR - 1) / TR;
   r.K = (L + TK - 1) / TK;
-  r.units = (r.tiles + 1) / 2;
-  r.cost = static_cast<int64_t>(r.tiles) * r.K;
   return r;
 }
 // Inclusive warp prefix sums of the cost and the units of 32 groups.
@@ -92,7 +94,7 @@ KVQ_DEVINL void scan_groups(int64_t& cost, int& units, int lane) {
 KVQ_DEVINL int64_t total_cost(const SharedParams& p, int lane, bool report) {
   int64_t W = 0;
   for (int base = 0; base < p.G; base += 32) {
-    int64_t c = base + lane < p.G ? group_of(p, base + lane, report).cost : 0;
+    int64_t c = base + lane < p.G ? group_of(p, base + lane, report).cost() : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
     W += c;
@@ -112,31 +114,43 @@ struct Segment {
 };
 
 // The segments of one slot; every lane of the warp holds the same values.
+// The groups come 32 at a time, one per lane, so that a batch of at most 32
+// groups is read once.
 struct SegWalk {
+  Group mine;  // group base + lane
+  int base;
   int64_t pos, end, gstart;
   int gi, ubase;
+  KVQ_DEVINL void load(const SharedParams& p, int at, int lane, bool report) {
+    base = at;
+    mine = Group{};
+    if (at + lane < p.G) mine = group_of(p, at + lane, report);
+  }
   KVQ_DEVINL SegWalk(const SharedParams& p, int slot, int lane, bool report) {
-    const int64_t W = total_cost(p, lane, report);
+    int64_t W = 0;
+    for (int at = 0; at < p.G; at += 32) {
+      load(p, at, lane, report);
+      int64_t c = mine.cost();
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+      W += c;
+    }
     const int64_t N = used_slots(p, W);
     pos = end = gstart = 0;
     gi = ubase = 0;
     if (slot >= N) return;
     pos = slot * W / N;
     end = (slot + 1) * W / N;
-    for (int base = 0; base < p.G; base += 32) {  // the group that pos lies in
-      int64_t c = 0;
-      int u = 0;
-      if (base + lane < p.G) {
-        const Group r = group_of(p, base + lane, false);
-        c = r.cost;
-        u = r.units;
-      }
+    for (int at = 0; at < p.G; at += 32) {  // the group that pos lies in
+      if (base != at) load(p, at, lane, false);
+      int64_t c = mine.cost();
+      int u = mine.units();
       scan_groups(c, u, lane);
       const int before = __popc(__ballot_sync(0xffffffffu, gstart + c <= pos));
       if (before < 32) {
         const int64_t cb = __shfl_sync(0xffffffffu, c, before ? before - 1 : 0);
         const int ub = __shfl_sync(0xffffffffu, u, before ? before - 1 : 0);
-        gi = base + before;
+        gi = at + before;
         if (before) {
           gstart += cb;
           ubase += ub;
@@ -148,114 +162,510 @@ struct SegWalk {
     }
     gi = p.G;
   }
-  KVQ_DEVINL bool next(const SharedParams& p, Segment& s) {
+  KVQ_DEVINL bool next(const SharedParams& p, Segment& s, int lane) {
     while (pos < end && gi < p.G) {
-      const Group r = group_of(p, gi, false);
-      if (pos >= gstart + r.cost) {
-        gstart += r.cost;
-        ubase += r.units;
+      if (gi >= base + 32) load(p, gi, lane, false);
+      const int at = gi - base;
+      const int tiles = __shfl_sync(0xffffffffu, mine.tiles, at), K = __shfl_sync(0xffffffffu, mine.K, at);
+      const int64_t cost = static_cast<int64_t>(tiles) * K;
+      if (pos >= gstart + cost) {
+        gstart += cost;
+        ubase += (tiles + 1) / 2;
         ++gi;
         continue;
       }
-      const int u = static_cast<int>((pos - gstart) / (2 * r.K));
-      const int64_t ustart = gstart + static_cast<int64_t>(u) * 2 * r.K;
-      s.nq = min(2, r.tiles - 2 * u);
-      const int64_t uend = ustart + static_cast<int64_t>(s.nq) * r.K;
+      const int u = static_cast<int>((pos - gstart) / (2 * K));
+      const int64_t ustart = gstart + static_cast<int64_t>(u) * 2 * K;
+      s.nq = min(2, tiles - 2 * u);
+      const int64_t uend = ustart + static_cast<int64_t>(s.nq) * K;
       const int64_t stop = end < uend ? end : uend;
       s.k0 = static_cast<int>((pos - ustart + s.nq - 1) / s.nq);
       s.k1 = static_cast<int>((stop - ustart + s.nq - 1) / s.nq);
-      s.a = r.a;
+      s.a = __shfl_sync(0xffffffffu, mine.a, at);
       s.row0 = u * UNIT;
-      s.rows = min(UNIT, r.nb * p.g - s.row0);
-      s.L = r.L;
+      s.rows = min(UNIT, __shfl_sync(0xffffffffu, mine.nb, at) * p.g - s.row0);
+      s.L = __shfl_sync(0xffffffffu, mine.L, at);
       s.group = gi;
       s.unit = ubase + u;
       pos = stop;
-      if (s.unit < p.max_units) return true;
-      return false;  // only with faulty group_starts (reported)
+      return s.unit < p.max_units;  // false only with faulty group_starts (reported)
     }
     return false;
   }
 };
 
 // ---------------------------------------------------------------- prefix ---
-// Grid slots * Hkv; a thread per row of the unit.
+// One CTA per (KV head, slot).  Two streams, each with its own 128 query rows,
+// score buffer and output sum in tensor memory: over a unit of two tiles the
+// streams take the two tiles and every key tile; over a unit of one tile both
+// take the same rows and alternate key tiles.  While one stream's softmax
+// runs, the tensor cores work on the other.
+//   S = Q K^T   kind::f8f6f4, K as cached (FP8); the query row enters as the
+//               sum of two E4M3 terms of q * sigma, sigma = 2^(7 - floor(log2
+//               max|q|)): exact except elements under 2^-9 of the row's
+//               maximum, which keep 2^-17 of it;
+//   O += P V    kind::f16, P = f16(2^(s - M + 8)) from tensor memory, V
+//               converted to f16 (exact) by four warps.  FP8 probabilities
+//               would lose long tails (a key at 2^-18 of the largest is half
+//               a step of E4M3), and two FP8 terms cost the tensor cores as
+//               much as f16.
+// M is a row's first tile maximum and moves only when a later one is more than
+// 2^kSlack times larger (P then reaches at most 2^(8 + kSlack)), so that the
+// rescale of O by tensor-memory round trips is rare.
+// MMAs of a CTA complete in issue order, and each S_j commit covers the P.V
+// issued before it: a stream's softmax sees O complete when S_j arrives, and
+// its P_j may lie over S_j.
+constexpr int kSoftWarps = 8;           // 0-3 stream 0, 4-7 stream 1
+constexpr int kConvWarps = 4;           // 8-11
+constexpr int W_K = 12, W_MMA = 13, W_V = 14;
+constexpr int kPrefixThreads = 512;
+constexpr int REG_SOFT = 192, REG_CONV = 64, REG_CTRL = 56;
+static_assert(kSoftWarps * 32 * REG_SOFT + kConvWarps * 32 * REG_CONV + 128 * REG_CTRL <= 65536, "register split");
+constexpr float kSlack = 7.f;
+constexpr int kInfo = 16;  // tile flags kept: more than the tiles in flight
+
+template <int D>
+struct Geo {
+  static constexpr int NST = D == 128 ? 3 : 6;      // K stages, V stages
+  static constexpr int TILE = TK * D;               // bytes of a K or V tile
+  static constexpr int PAGE = kPage * D;
+  static constexpr int QT = TR * D;                 // one term of a query tile
+  static constexpr int OFF_Q = 0;                   // [stream][term]
+  static constexpr int OFF_K = OFF_Q + 4 * QT;
+  static constexpr int OFF_V = OFF_K + NST * TILE;
+  static constexpr int OFF_VH = OFF_V + NST * TILE;  // two f16 V tiles
+  static constexpr int OFF_BAR = OFF_VH + 2 * 2 * TILE;
+  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // + alignment slack
+  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+template <int NST>
+struct Bars {
+  uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
+  uint64_t vh_full[2], vh_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t done, stall;
+  uint32_t k_bad[kInfo], v_dead[kInfo];  // bit i: page i of the tile is not there
+  uint32_t tmem_base;
+  int abort;
+};
+
 template <int D, bool E5>
-__global__ void __launch_bounds__(256) prefix_kernel(const __grid_constant__ SharedParams p) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  float* ks = reinterpret_cast<float*>(smem);  // [TK][D]
-  float* vs = ks + TK * D;                     // [TK][D]
-  __nv_bfloat162* qs = reinterpret_cast<__nv_bfloat162*>(vs + TK * D);  // [UNIT][D / 2 + 1]
-  __shared__ int bad[TK / kPage];
+__global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_constant__ SharedParams p) {
+  using G = Geo<D>;
+  constexpr int NST = G::NST;
+  using B = Bars<NST>;
+  static_assert(sizeof(B) <= 1024, "barrier block");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
+  const uint32_t sbase = smem_u32(smem);
+  B* bars = reinterpret_cast<B*>(smem + G::OFF_BAR);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kvh = blockIdx.x % p.Hkv, slot = blockIdx.x / p.Hkv;
-  const int tid = threadIdx.x, lane = tid & 31;
-  grid_launch_dependents();
-  SegWalk walk(p, slot, lane, blockIdx.x == 0 && tid < 32);
-  const float coef = p.k_scale[kvh] * p.sm_scale * kLog2e;
-  auto dec = [](uint8_t c) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, E5 ? __NV_E5M2 : __NV_E4M3);
-    return __half2float(__half(h));
-  };
-  for (Segment s; walk.next(p, s);) {
-    const int half = tid >> 7;
-    const int row = s.nq == 2 ? tid : tid & 127;
-    const bool live = row < s.rows;
-    __syncthreads();
-    if (live) {
-      const int r = s.row0 + row;
-      const __nv_bfloat162* src = reinterpret_cast<const __nv_bfloat162*>(
-          static_cast<const __nv_bfloat16*>(p.q) +
-          (static_cast<size_t>(s.a + r / p.g) * p.Hq + kvh * p.g + r % p.g) * D);
-      for (int d = 0; d < D / 2; ++d) qs[tid * (D / 2 + 1) + d] = src[d];
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&bars->k_full[i], 1);
+      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->v_full[i], 1);
+      mbar_init(&bars->v_empty[i], kConvWarps);
     }
-    float m = -INFINITY, l = 0.f, o[D];
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->vh_full[i], kConvWarps);
+      mbar_init(&bars->vh_empty[i], 1);
+      mbar_init(&bars->q_full[i], 128);
+      mbar_init(&bars->s_full[i], 1);
+      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->o_full[i], 1);
+    }
+    mbar_init(&bars->done, 1);
+    mbar_init(&bars->stall, 1);
+    bars->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == W_MMA) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&bars->tmem_base)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;  // S0 | S1 (128 columns each) | O0 | O1 (D each)
+  grid_launch_dependents();
+
+  // a wait of the whole warp; false (for good) after a timeout anywhere
+  bool ok = true;
+  auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+    if (!ok) return false;
+    const bool got = mbar_wait(bar, parity, abort_flag);
+    if (!__all_sync(0xffffffffu, got)) {
+      ok = false;
+      set_status(p.dev_status, KVQ_DEV_TIMEOUT);
+      *abort_flag = 1;
+    }
+    return ok;
+  };
+
+  if (warp >= W_K) {
+    setmaxnreg_dec<REG_CTRL>();
+    if (warp == W_K || warp == W_V) {
+      // --------------------------------------------------- K and V producers --
+      const bool is_k = warp == W_K;
+      SegWalk walk(p, slot, lane, is_k && blockIdx.x == 0);
+      uint64_t* full = is_k ? bars->k_full : bars->v_full;
+      uint64_t* empty = is_k ? bars->k_empty : bars->v_empty;
+      uint32_t* info = is_k ? bars->k_bad : bars->v_dead;
+      const uint8_t* cache = is_k ? p.k_cache : p.v_cache;
+      const int64_t str = is_k ? p.k_str : p.v_str;
+      uint8_t* ring = smem + (is_k ? G::OFF_K : G::OFF_V);
+      const uint64_t pol = policy_evict_last();
+      uint32_t it = 0;  // tiles issued
+      for (Segment s; ok && walk.next(p, s, lane);) {
+        const int n_pages = (s.L + kPage - 1) / kPage;
+        const int32_t* bt = p.prefix_table + static_cast<size_t>(s.group) * p.max_prefix;
+        // block ids of four tiles at a time, loaded a group ahead
+        auto load_ids = [&](int tile) {
+          const int page = tile * (TK / kPage) + lane;
+          return tile < s.k1 && page < n_pages ? ld_l2only_s32(bt + page) : -1;
+        };
+        int ids = load_ids(s.k0), ids_next = load_ids(s.k0 + 4);
+        for (int kt = s.k0; kt < s.k1; ++kt, ++it) {
+          const int in_group = (kt - s.k0) & 3;
+          if (in_group == 0 && kt != s.k0) {
+            ids = ids_next;
+            ids_next = load_ids(kt + 4);
+          }
+          const int st = it % NST;
+          if (!wait_all(&empty[st], ((it / NST) & 1) ^ 1)) break;
+          int blk = __shfl_sync(0xffffffffu, ids, (in_group << 3) | (lane & 7));
+          const int page = kt * (TK / kPage) + lane;
+          if (lane >= TK / kPage || page >= n_pages) {
+            blk = -1;
+          } else if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks) {
+            set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+            blk = -1;
+          }
+          const uint32_t there = __ballot_sync(0xffffffffu, blk >= 0);
+          if (lane == 0) {
+            info[it % kInfo] = ~there & 0xFFu;
+            mbar_arrive_expect_tx(&full[st], static_cast<uint32_t>(G::PAGE) * __popc(there));
+          }
+          __syncwarp();
+          if (blk >= 0)
+            bulk_g2s(ring + st * G::TILE + lane * G::PAGE, cache + (static_cast<size_t>(blk) * p.Hkv + kvh) * str, G::PAGE,
+                     &full[st], pol);
+          __syncwarp();
+        }
+      }
+      if (!ok && lane == 0) {  // abandoned: let issued copies land
+        for (uint32_t k = it > NST ? it - NST : 0; k < it; ++k) mbar_wait(&full[k % NST], (k / NST) & 1);
+      }
+    } else if (warp == W_MMA) {
+      // ------------------------------------------------------------ MMA issuer --
+      constexpr uint32_t IDESC_S = idesc_e4m3(TR, TK, E5);
+      constexpr uint32_t IDESC_O = idesc_f16(TR, D);
+      auto desc = [](uint32_t a) { return D == 128 ? desc_sw128(a) : desc_sw64(a); };
+      SegWalk walk(p, slot, lane, false);
+      uint32_t tile0 = 0;               // tiles of earlier segments
+      uint32_t np[2] = {0, 0}, nseg = 0;  // P tiles per stream, segments
+      for (Segment s; ok && walk.next(p, s, lane); ++nseg) {
+        const int n = s.k1 - s.k0;
+        const bool pair = s.nq == 2;
+        // stream x's j-th tile and its count
+        auto tile_of = [&](int x, int j) { return tile0 + (pair ? j : 2 * j + x); };
+        const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
+        auto qk = [&](int x, int j) {  // S_x = Q_x K^T
+          const uint32_t t = tile_of(x, j);
+          const int st = t % NST;
+          if (!wait_all(&bars->k_full[st], (t / NST) & 1)) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t q_s = sbase + G::OFF_Q + x * 2 * G::QT, k_s = sbase + G::OFF_K + st * G::TILE;
 #pragma unroll
-    for (int d = 0; d < D; ++d) o[d] = 0.f;
-    for (int kt = s.k0; kt < s.k1; ++kt) {
-      __syncthreads();
-      for (int i = tid; i < TK * D; i += 256) {
-        const int key = i / D, d = i % D, tok = kt * TK + key;
-        float kx = 0.f, vx = 0.f;
-        if (tok < s.L) {
-          const int blk = p.prefix_table[static_cast<size_t>(s.group) * p.max_prefix + tok / kPage];
-          const bool ok = blk >= 0 && static_cast<int64_t>(blk) < p.num_blocks;
-          if (!ok) set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
-          if (d == 0 && key % kPage == 0) bad[key / kPage] = !ok;
-          if (ok) {
-            const size_t pg = static_cast<size_t>(blk) * p.Hkv + kvh;
-            const int t = tok % kPage;
-            kx = dec(p.k_cache[pg * p.k_str + fp8_k_offset(t, d / 16, D) + d % 16]);
-            vx = dec(p.v_cache[pg * p.v_str + d * kPage + fp8_v_slot(t)]);
+            for (int kk = 0; kk < D / 32; ++kk)
+#pragma unroll
+              for (int term = 0; term < 2; ++term)
+                umma_f8(tmem + x * TK, desc(q_s + term * G::QT + kk * 32), desc(k_s + kk * 32), IDESC_S, kk + term > 0 ? 1u : 0u);
+            umma_commit(&bars->s_full[x]);
+            if (!pair || x == 1) umma_commit(&bars->k_empty[st]);
+          }
+          __syncwarp();
+        };
+        auto pv = [&](int x, int j) {  // O_x += P_x V
+          const uint32_t t = tile_of(x, j);
+          if (!wait_all(&bars->p_full[x], np[x] & 1)) return;
+          ++np[x];
+          if (!wait_all(&bars->vh_full[t & 1], (t >> 1) & 1)) return;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t v_s = sbase + G::OFF_VH + (t & 1) * 2 * G::TILE;
+#pragma unroll
+            for (int kk = 0; kk < TK / 16; ++kk)  // a page per MMA: two halves of eight tokens, D * 16 bytes apart
+              umma_f16_ta(tmem + 2 * TK + x * D, tmem + x * TK + kk * 8, desc_interleave(v_s + kk * 2 * G::PAGE, D * 16, 128),
+                          IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
+            if (!pair || x == 1) umma_commit(&bars->vh_empty[t & 1]);
+            if (j == cnt[x] - 1) umma_commit(&bars->o_full[x]);
+          }
+          __syncwarp();
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (cnt[x] > 0 && wait_all(&bars->q_full[x], nseg & 1)) qk(x, 0);
+        for (int j = 0; ok && j < cnt[0]; ++j) {
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (!ok || j >= cnt[x]) continue;
+            pv(x, j);
+            if (ok && j + 1 < cnt[x]) qk(x, j + 1);
           }
         }
-        ks[i] = kx;
-        vs[i] = vx;
+        tile0 += n;
       }
-      __syncthreads();
-      if (!live || (s.nq == 1 && ((kt - s.k0) & 1) != half)) continue;
-      const int n = min(TK, s.L - kt * TK);
-      for (int key = 0; key < n; ++key) {
-        if (bad[key / kPage]) continue;
-        float x = 0.f;
-        for (int d = 0; d < D / 2; ++d) {
-          const float2 qf = __bfloat1622float2(qs[tid * (D / 2 + 1) + d]);
-          x = fmaf(qf.x, ks[key * D + 2 * d], fmaf(qf.y, ks[key * D + 2 * d + 1], x));
+      // every MMA has completed before the tensor memory is released
+      if (lane == 0) umma_commit(&bars->done);
+      __syncwarp();
+      mbar_wait(&bars->done, 0);
+    }
+  } else if (warp >= kSoftWarps) {
+    setmaxnreg_dec<REG_CONV>();
+    // ------------------------------------------------- V to f16 (exact) --
+    // A thread per dimension row: 16 codes -> two 16-byte chunks of f16, the
+    // no-swizzle K-major operand (token slots 0-7, then 8-15).  Slots of tokens
+    // that are not there are zeroed: P is 0 for them, and 0 x NaN is NaN.
+    SegWalk walk(p, slot, lane, false);
+    const int t = threadIdx.x - kSoftWarps * 32;
+    uint32_t it = 0;
+    for (Segment s; ok && walk.next(p, s, lane);) {
+      for (int kt = s.k0; kt < s.k1; ++kt, ++it) {
+        const int st = it % NST;
+        if (!wait_all(&bars->v_full[st], (it / NST) & 1)) break;
+        if (!wait_all(&bars->vh_empty[it & 1], ((it >> 1) & 1) ^ 1)) break;
+        const uint32_t dead = reinterpret_cast<volatile uint32_t*>(bars->v_dead)[it % kInfo];
+        const int valid = s.L - kt * TK;  // tokens of the tile, if less than TK
+        const uint8_t* src = smem + G::OFF_V + st * G::TILE;
+        uint8_t* dst = smem + G::OFF_VH + (it & 1) * 2 * G::TILE;
+#pragma unroll 4
+        for (int i = t; i < TK / kPage * D; i += kConvWarps * 32) {
+          const int pg = i / D, d = i % D;
+          uint4 c = *reinterpret_cast<const uint4*>(src + i * 16);
+          const int left = valid - pg * kPage;
+          if ((dead >> pg) & 1) {
+            c = make_uint4(0, 0, 0, 0);
+          } else if (left < kPage) {
+            uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int tok = 0; tok < kPage; ++tok) {
+              const int sl = fp8_v_slot(tok);
+              if (tok >= left) w[sl >> 2] &= ~(0xFFu << (8 * (sl & 3)));
+            }
+            c = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          uint4 lo, hi;
+          fp8x4_to_f16x2x2<E5>(c.x, lo.x, lo.y);
+          fp8x4_to_f16x2x2<E5>(c.y, lo.z, lo.w);
+          fp8x4_to_f16x2x2<E5>(c.z, hi.x, hi.y);
+          fp8x4_to_f16x2x2<E5>(c.w, hi.z, hi.w);
+          uint8_t* o = dst + pg * 2 * G::PAGE + d * 16;
+          *reinterpret_cast<uint4*>(o) = lo;
+          *reinterpret_cast<uint4*>(o + D * 16) = hi;
         }
-        x *= coef;
-        const float mn = fmaxf(m, x), a = ex2(m - mn), w = ex2(x - mn);
-        l = l * a + w;
-#pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = fmaf(w, vs[key * D + d], o[d] * a);
-        m = mn;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars->v_empty[st]);
+          mbar_arrive(&bars->vh_full[it & 1]);
+        }
       }
     }
-    if (live) {
-      const size_t idx = (static_cast<size_t>(kvh) * p.kseg + slot + s.unit) * UNIT + tid;
-      const float f = l > 0.f ? p.v_scale[kvh] / l : 0.f;
-#pragma unroll
-      for (int d = 0; d < D; ++d) p.o_part[idx * D + d] = o[d] * f;
-      p.lse_part[idx] = l > 0.f ? m + log2f(l) : -INFINITY;
+  } else {
+    setmaxnreg_inc<REG_SOFT>();
+    // ------------------------------------------------------------- softmax --
+    // A thread per query row (tensor-memory lane), 128 keys of a tile each.
+    const int x = warp >> 2;                 // stream
+    const int quarter = warp & 3;
+    const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
+    const int row = quarter * 32 + lane;     // of the stream's tile
+    const uint32_t s_t = tmem + t_lane + x * TK, o_t = tmem + t_lane + 2 * TK + x * D;
+    const float kscale = __fmul_rn(__fmul_rn(p.k_scale[kvh], p.sm_scale), kLog2e);
+    const float vscale = p.v_scale[kvh];
+    SegWalk walk(p, slot, lane, false);
+    uint32_t tile0 = 0, ns = 0, nseg = 0;  // tiles of earlier segments; S tiles seen; O sums taken
+    if (!__all_sync(0xffffffffu, stall_wait(&bars->stall, p.stall_ns, abort_flag))) {
+      ok = false;
+      set_status(p.dev_status, KVQ_DEV_TIMEOUT);
+      *abort_flag = 1;
     }
+    for (Segment s; ok && walk.next(p, s, lane);) {
+      const bool pair = s.nq == 2;
+      const int n = s.k1 - s.k0;
+      const int cnt = pair ? n : x == 0 ? (n + 1) / 2 : n / 2;
+      const int r = (pair ? x * TR : 0) + row;  // row of the unit
+      const bool live = r < s.rows;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      // ---- the query row as two E4M3 terms, swizzled K-major ----
+      float coef = 0.f;
+      if (live) {
+        const int rr = s.row0 + r;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const __nv_bfloat16*>(p.q) +
+            (static_cast<size_t>(s.a + rr / p.g) * p.Hq + static_cast<size_t>(kvh) * p.g + rr % p.g) * D);
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 u = __ldcg(src + i);
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx = fmax3(mx, fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
+        }
+        int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127 : 0;
+        e2 = e2 < -100 ? -100 : e2;
+        const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+        coef = kscale * __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+        uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + row * D;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int hw = 0; hw < 2; ++hw) {
+            const uint4 u = __ldcg(src + 2 * c + hw);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int e = 0; e < 4; e += 2) {
+              float v[4] = {__uint_as_float(w[e] << 16) * sigma, __uint_as_float(w[e] & 0xFFFF0000u) * sigma,
+                            __uint_as_float(w[e + 1] << 16) * sigma, __uint_as_float(w[e + 1] & 0xFFFF0000u) * sigma};
+              const uint32_t h = f32x2_to_e4m3x2(v[0], v[1]) | (f32x2_to_e4m3x2(v[2], v[3]) << 16);
+              uint32_t f0, f1;
+              e4m3x4_to_f16x2x2(h, f0, f1);
+              const float2 a = __half22float2(*reinterpret_cast<__half2*>(&f0)), b = __half22float2(*reinterpret_cast<__half2*>(&f1));
+              hi[2 * hw + e / 2] = h;
+              lo[2 * hw + e / 2] = f32x2_to_e4m3x2(v[0] - a.x, v[1] - a.y) | (f32x2_to_e4m3x2(v[2] - b.x, v[3] - b.y) << 16);
+            }
+          }
+          const int pc = (D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4;
+          *reinterpret_cast<uint4*>(qs + pc) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(qs + G::QT + pc) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars->q_full[x]);
+
+      float M = -INFINITY, l = 0.f;
+      for (int j = 0; j < cnt; ++j, ++ns) {
+        if (!wait_all(&bars->s_full[x], ns & 1)) break;
+        tc_fence_after();
+        if (warp_live) {
+          const uint32_t t = tile0 + (pair ? j : 2 * j + x);
+          const int kt = s.k0 + (pair ? j : 2 * j + x);
+          const uint32_t bad = reinterpret_cast<volatile uint32_t*>(bars->k_bad)[t % kInfo];
+          float sv[TK];
+          {
+            uint32_t v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_t + 32 * c, v[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_pin32(v[c]);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sv[32 * c + i] = __uint_as_float(v[c][i]);
+            }
+          }
+          const int valid = s.L - kt * TK;
+          if (bad != 0 || valid < TK) {
+#pragma unroll
+            for (int k = 0; k < TK; ++k) sv[k] = (k >= valid || ((bad >> (k / kPage)) & 1)) ? -INFINITY : sv[k];
+          }
+          float mx;
+          {
+            float m1[43];
+#pragma unroll
+            for (int i = 0; i < 42; ++i) m1[i] = fmax3(sv[3 * i], sv[3 * i + 1], sv[3 * i + 2]);
+            m1[42] = fmaxf(sv[126], sv[127]);
+            float m2[15];
+#pragma unroll
+            for (int i = 0; i < 14; ++i) m2[i] = fmax3(m1[3 * i], m1[3 * i + 1], m1[3 * i + 2]);
+            m2[14] = m1[42];
+            float m3[5];
+#pragma unroll
+            for (int i = 0; i < 5; ++i) m3[i] = fmax3(m2[3 * i], m2[3 * i + 1], m2[3 * i + 2]);
+            mx = fmax3(fmaxf(m3[0], m3[1]), fmaxf(m3[2], m3[3]), m3[4]) * coef;
+          }
+          const bool move = live && mx > M + kSlack;  // M = -inf: the first tile with a live key
+          if (j > 0 && __any_sync(0xffffffffu, move)) {
+            const float a = move ? ex2(M - mx) : 1.f;
+            l *= a;
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16_async(o_t + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st16(o_t + 16 * c, o);
+            }
+          }
+          if (move) M = mx;
+          const float nb = M == -INFINITY ? 0.f : 8.f - M;  // no live key so far: every score is -inf
+          const float2 coef2 = make_float2(coef, coef), nb2 = make_float2(nb, nb);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {  // 32 keys: two pages, 16 words of two slots
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int k = 32 * c + (i >> 3) * 16 + (i & 1) * 8 + ((i & 7) >> 1) * 2;  // tokens of slots 2i, 2i + 1
+              float2 e = ffma2(make_float2(sv[k], sv[k + 1]), coef2, nb2);
+              e.x = ex2(e.x);
+              e.y = ex2(e.y);
+              sum = fadd2(sum, e);
+              w[i] = pack_f16x2(e.x, e.y);
+            }
+            tmem_st16(s_t + 16 * c, w);
+          }
+          l += sum.x + sum.y;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&bars->p_full[x]);
+      }
+      tile0 += n;
+      if (!ok) break;
+      const size_t idx = (static_cast<size_t>(kvh) * p.kseg + slot + s.unit) * UNIT + x * TR + row;
+      if (cnt > 0) {
+        if (!wait_all(&bars->o_full[x], nseg & 1)) break;
+        ++nseg;
+        tc_fence_after();
+        const float f = l > 0.f ? vscale / l : 0.f;
+        float4* dst = reinterpret_cast<float4*>(p.o_part + idx * D);
+        if (warp_live) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_t + 32 * c, o);
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                                             __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            }
+          }
+        }
+        tc_fence_before();
+      }
+      if (live) p.lse_part[idx] = l > 0.f ? M + __log2f(l) - 8.f : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == W_MMA) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
   // the decode partials' grid precedes this one and may still run: this grid
   // must not complete before it, so that the combine sees both
@@ -291,16 +701,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
     for (int base = 0; base < p.G; base += 32) {
       Group r = {};
       if (base + lane < p.G) r = group_of(p, base + lane, false);
-      int64_t c = r.cost;
-      int u = r.units;
+      int64_t c = r.cost();
+      int u = r.units();
       scan_groups(c, u, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, base + lane < p.G && b >= r.a && b < r.a + r.nb);
       if (hit) {
         const int at = __ffs(hit) - 1;
         const int a = __shfl_sync(0xffffffffu, r.a, at), K = __shfl_sync(0xffffffffu, r.K, at);
         const int tiles = __shfl_sync(0xffffffffu, r.tiles, at);
-        gstart += __shfl_sync(0xffffffffu, c - r.cost, at);
-        ubase += __shfl_sync(0xffffffffu, u - r.units, at);
+        gstart += __shfl_sync(0xffffffffu, c - r.cost(), at);
+        ubase += __shfl_sync(0xffffffffu, u - r.units(), at);
         const int row = (b - a) * p.g + hq % p.g, un = row / UNIT;
         const int nq = min(2, tiles - 2 * un);
         if (K > 0 && ubase + un < p.max_units) {
@@ -394,7 +804,7 @@ Layout layout_of(int B, int G, int Hq, int Hkv, int D, int max_blocks) {
 
 template <int D, bool E5>
 kvq_status_t launch_shared(const SharedParams& p, const MergeParams& mp, cudaStream_t s) {
-  constexpr int smem = 2 * TK * D * 4 + UNIT * (D / 2 + 1) * 4;
+  constexpr int smem = Geo<D>::SMEM;
   auto kern = prefix_kernel<D, E5>;
   static int configured_mask = 0;  // devices whose attribute is set
   int dev = 0;
@@ -409,7 +819,7 @@ kvq_status_t launch_shared(const SharedParams& p, const MergeParams& mp, cudaStr
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.slots * p.Hkv);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(kPrefixThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
@@ -523,6 +933,7 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
   p.max_units = static_cast<int>(prefix_units(B, G, p.g));
   p.kseg = p.slots + p.max_units;
   p.dev_status = dev_status;
+  p.stall_ns = stall_ns();
   MergeParams mp;
   mp.sp = p;
   mp.o_own = a.o_part;
