@@ -55,7 +55,7 @@ struct Group {
   int a, nb;        // first sequence, sequences
   int L, tiles, K;  // prefix tokens, row tiles, key tiles
   KVQ_DEVINL int units() const { return (tiles + 1) / 2; }
-  KVQ_DEVINL int64_t cost() const { return static_cast<int64_t>(tiles) * K; }
+  KVQ_DEVINL int cost() const { return tiles * K; }
 };
 KVQ_DEVINL Group group_of(const SharedParams& p, int i, bool report) {
   Group r;
@@ -80,10 +80,10 @@ KVQ_DEVINL Group group_of(const SharedParams& p, int i, bool report) {
   return r;
 }
 // Inclusive warp prefix sums of the cost and the units of 32 groups.
-KVQ_DEVINL void scan_groups(int64_t& cost, int& units, int lane) {
+KVQ_DEVINL void scan_groups(int& cost, int& units, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t c = __shfl_up_sync(0xffffffffu, cost, o);
+    const int c = __shfl_up_sync(0xffffffffu, cost, o);
     const int u = __shfl_up_sync(0xffffffffu, units, o);
     if (lane >= o) {
       cost += c;
@@ -91,21 +91,27 @@ KVQ_DEVINL void scan_groups(int64_t& cost, int& units, int lane) {
     }
   }
 }
-KVQ_DEVINL int64_t total_cost(const SharedParams& p, int lane, bool report) {
-  int64_t W = 0;
-  for (int base = 0; base < p.G; base += 32) {
-    int64_t c = base + lane < p.G ? group_of(p, base + lane, report).cost() : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    W += c;
+// The cut of a total cost W (below 2^31, checked on the host; with faulty
+// groups it may wrap, which the clamps keep in bounds) into used slots: the
+// first `rem` slots hold q + 1, the others q.
+struct Cut {
+  int q, rem, used;
+  KVQ_DEVINL Cut(const SharedParams& p, int W) {
+    used = max(0, min(W, p.slots));
+    q = used ? W / used : 0;
+    rem = used ? W - q * used : 0;
   }
-  return W;
-}
-KVQ_DEVINL int64_t used_slots(const SharedParams& p, int64_t W) { return W < p.slots ? W : p.slots; }
+  KVQ_DEVINL int start(int slot) const { return slot * q + min(slot, rem); }
+  KVQ_DEVINL int slot_of(int x) const {
+    const int y = x - rem * (q + 1);
+    return min(used - 1, y < 0 ? x / (q + 1) : rem + y / q);
+  }
+};
 
 struct Segment {
   int a;           // first sequence of the group
   int row0, rows;  // rows [row0, row0 + rows) of the group
+  bool once;       // no other unit reads these keys
   int nq;          // tiles: 2, or 1 (then the two row halves take alternate key tiles of the one tile)
   int k0, k1;      // key tiles
   int L;           // prefix tokens
@@ -119,7 +125,7 @@ struct Segment {
 struct SegWalk {
   Group mine;  // group base + lane
   int base;
-  int64_t pos, end, gstart;
+  int pos, end, gstart;
   int gi, ubase;
   KVQ_DEVINL void load(const SharedParams& p, int at, int lane, bool report) {
     base = at;
@@ -127,60 +133,53 @@ struct SegWalk {
     if (at + lane < p.G) mine = group_of(p, at + lane, report);
   }
   KVQ_DEVINL SegWalk(const SharedParams& p, int slot, int lane, bool report) {
-    int64_t W = 0;
+    int W = 0;
+#pragma unroll 1
     for (int at = 0; at < p.G; at += 32) {
       load(p, at, lane, report);
-      int64_t c = mine.cost();
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-      W += c;
+      W += __reduce_add_sync(0xffffffffu, mine.cost());
     }
-    const int64_t N = used_slots(p, W);
+    const Cut cut(p, W);
     pos = end = gstart = 0;
     gi = ubase = 0;
-    if (slot >= N) return;
-    pos = slot * W / N;
-    end = (slot + 1) * W / N;
+    if (slot >= cut.used) return;
+    pos = cut.start(slot);
+    end = cut.start(slot + 1);
+#pragma unroll 1
     for (int at = 0; at < p.G; at += 32) {  // the group that pos lies in
       if (base != at) load(p, at, lane, false);
-      int64_t c = mine.cost();
-      int u = mine.units();
+      int c = mine.cost(), u = mine.units();
       scan_groups(c, u, lane);
       const int before = __popc(__ballot_sync(0xffffffffu, gstart + c <= pos));
-      if (before < 32) {
-        const int64_t cb = __shfl_sync(0xffffffffu, c, before ? before - 1 : 0);
-        const int ub = __shfl_sync(0xffffffffu, u, before ? before - 1 : 0);
-        gi = at + before;
-        if (before) {
-          gstart += cb;
-          ubase += ub;
-        }
-        return;
+      const int last = before < 32 ? before - 1 : 31;
+      const int cb = __shfl_sync(0xffffffffu, c, last & 31), ub = __shfl_sync(0xffffffffu, u, last & 31);
+      gi = at + before;
+      if (before) {
+        gstart += cb;
+        ubase += ub;
       }
-      gstart += __shfl_sync(0xffffffffu, c, 31);
-      ubase += __shfl_sync(0xffffffffu, u, 31);
+      if (before < 32) return;
     }
-    gi = p.G;
   }
   KVQ_DEVINL bool next(const SharedParams& p, Segment& s, int lane) {
+#pragma unroll 1
     while (pos < end && gi < p.G) {
-      if (gi >= base + 32) load(p, gi, lane, false);
+      if (gi >= base + 32 || gi < base) load(p, gi & ~31, lane, false);
       const int at = gi - base;
       const int tiles = __shfl_sync(0xffffffffu, mine.tiles, at), K = __shfl_sync(0xffffffffu, mine.K, at);
-      const int64_t cost = static_cast<int64_t>(tiles) * K;
-      if (pos >= gstart + cost) {
-        gstart += cost;
+      if (pos >= gstart + tiles * K) {
+        gstart += tiles * K;
         ubase += (tiles + 1) / 2;
         ++gi;
         continue;
       }
-      const int u = static_cast<int>((pos - gstart) / (2 * K));
-      const int64_t ustart = gstart + static_cast<int64_t>(u) * 2 * K;
+      const int u = (pos - gstart) / (2 * K);
+      const int ustart = gstart + u * 2 * K;
+      s.once = tiles <= 2;
       s.nq = min(2, tiles - 2 * u);
-      const int64_t uend = ustart + static_cast<int64_t>(s.nq) * K;
-      const int64_t stop = end < uend ? end : uend;
-      s.k0 = static_cast<int>((pos - ustart + s.nq - 1) / s.nq);
-      s.k1 = static_cast<int>((stop - ustart + s.nq - 1) / s.nq);
+      const int stop = min(end, ustart + s.nq * K);
+      s.k0 = s.nq == 2 ? (pos - ustart + 1) >> 1 : pos - ustart;
+      s.k1 = s.nq == 2 ? (stop - ustart + 1) >> 1 : stop - ustart;
       s.a = __shfl_sync(0xffffffffu, mine.a, at);
       s.row0 = u * UNIT;
       s.rows = min(UNIT, __shfl_sync(0xffffffffu, mine.nb, at) * p.g - s.row0);
@@ -217,9 +216,11 @@ struct SegWalk {
 // its P_j may lie over S_j.
 constexpr int kSoftWarps = 8;           // 0-3 stream 0, 4-7 stream 1
 constexpr int kConvWarps = 4;           // 8-11
-constexpr int W_K = 12, W_MMA = 13, W_V = 14;
+constexpr int W_K = 12, W_V = 13, W_MMA = 14;  // an issuing warp per stream: 14, 15
 constexpr int kPrefixThreads = 512;
-constexpr int REG_SOFT = 192, REG_CONV = 64, REG_CTRL = 56;
+// Registers per thread: a softmax thread holds its row's 128 scores (reading
+// them twice from tensor memory instead cost 500 cycles a tile).
+constexpr int REG_SOFT = 192, REG_CONV = 64, REG_CTRL = 64;
 static_assert(kSoftWarps * 32 * REG_SOFT + kConvWarps * 32 * REG_CONV + 128 * REG_CTRL <= 65536, "register split");
 constexpr float kSlack = 7.f;
 constexpr int kInfo = 16;  // tile flags kept: more than the tiles in flight
@@ -234,7 +235,14 @@ struct Geo {
   static constexpr int OFF_K = OFF_Q + 4 * QT;
   static constexpr int OFF_V = OFF_K + NST * TILE;
   static constexpr int OFF_VH = OFF_V + NST * TILE;  // two f16 V tiles
-  static constexpr int OFF_BAR = OFF_VH + 2 * 2 * TILE;
+  // output staging: 32 rows of 32 floats per softmax warp, rows 16 bytes off
+  // each other's banks.  Head dim 128: in the warp's quarter of its stream's Q
+  // tile, whose MMAs are done by then; head dim 64, whose Q is half that: apart.
+  static constexpr int PITCH = 36;
+  static constexpr int STAGE_WARP = D == 128 ? 2 * QT / 4 : 32 * PITCH * 4;
+  static constexpr int OFF_STAGE = D == 128 ? OFF_Q : OFF_VH + 2 * 2 * TILE;
+  static_assert(32 * PITCH * 4 <= STAGE_WARP, "staging");
+  static constexpr int OFF_BAR = OFF_VH + 2 * 2 * TILE + (D == 128 ? 0 : kSoftWarps * STAGE_WARP);
   static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // + alignment slack
   static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
@@ -242,8 +250,10 @@ template <int NST>
 struct Bars {
   uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
   uint64_t vh_full[2], vh_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t done, stall;
+  uint64_t q_full[2], s_full[2], o_full[2];
+  uint64_t p_full[2][2];  // [stream][half of the tile's keys]
+  uint64_t turn[2];  // stream 0 has issued its P.V and next S (even, odd rounds): stream 1 may
+  uint64_t done[2], stall;
   uint32_t k_bad[kInfo], v_dead[kInfo];  // bit i: page i of the tile is not there
   uint32_t tmem_base;
   int abort;
@@ -267,19 +277,21 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   if (threadIdx.x == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&bars->k_full[i], 1);
-      mbar_init(&bars->k_empty[i], 1);
+      mbar_init(&bars->k_empty[i], 2);  // a release per stream
       mbar_init(&bars->v_full[i], 1);
       mbar_init(&bars->v_empty[i], kConvWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars->vh_full[i], kConvWarps);
-      mbar_init(&bars->vh_empty[i], 1);
+      mbar_init(&bars->vh_empty[i], 2);
       mbar_init(&bars->q_full[i], 128);
       mbar_init(&bars->s_full[i], 1);
-      mbar_init(&bars->p_full[i], 128);
+      mbar_init(&bars->p_full[i][0], 128);
+      mbar_init(&bars->p_full[i][1], 128);
       mbar_init(&bars->o_full[i], 1);
+      mbar_init(&bars->done[i], 1);
+      mbar_init(&bars->turn[i], 1);
     }
-    mbar_init(&bars->done, 1);
     mbar_init(&bars->stall, 1);
     bars->abort = 0;
     fence_barrier_init();
@@ -322,7 +334,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       const uint8_t* cache = is_k ? p.k_cache : p.v_cache;
       const int64_t str = is_k ? p.k_str : p.v_str;
       uint8_t* ring = smem + (is_k ? G::OFF_K : G::OFF_V);
-      const uint64_t pol = policy_evict_last();
+      const uint64_t pol_once = policy_evict_first(), pol_keep = policy_evict_last();
       uint32_t it = 0;  // tiles issued
       for (Segment s; ok && walk.next(p, s, lane);) {
         const int n_pages = (s.L + kPage - 1) / kPage;
@@ -357,78 +369,107 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           __syncwarp();
           if (blk >= 0)
             bulk_g2s(ring + st * G::TILE + lane * G::PAGE, cache + (static_cast<size_t>(blk) * p.Hkv + kvh) * str, G::PAGE,
-                     &full[st], pol);
+                     &full[st], s.once ? pol_once : pol_keep);
           __syncwarp();
         }
       }
       if (!ok && lane == 0) {  // abandoned: let issued copies land
         for (uint32_t k = it > NST ? it - NST : 0; k < it; ++k) mbar_wait(&full[k % NST], (k / NST) & 1);
       }
-    } else if (warp == W_MMA) {
-      // ------------------------------------------------------------ MMA issuer --
+    } else {
+      // ----------------------------------------------- MMA issuers, per stream --
       constexpr uint32_t IDESC_S = idesc_e4m3(TR, TK, E5);
       constexpr uint32_t IDESC_O = idesc_f16(TR, D);
-      auto desc = [](uint32_t a) { return D == 128 ? desc_sw128(a) : desc_sw64(a); };
+      const int x = warp - W_MMA;
+      // operand descriptors: the address sits in the low bits (16-byte units)
+      const uint32_t q_s = sbase + G::OFF_Q + x * 2 * G::QT;
+      const uint64_t q_desc = D == 128 ? desc_sw128(q_s) : desc_sw64(q_s);
+      const uint64_t k_desc = D == 128 ? desc_sw128(sbase + G::OFF_K) : desc_sw64(sbase + G::OFF_K);
+      const uint64_t v_desc = desc_interleave(sbase + G::OFF_VH, D * 16, 128);
+      const uint32_t s_t = tmem + x * TK, o_t = tmem + 2 * TK + x * D;
       SegWalk walk(p, slot, lane, false);
-      uint32_t tile0 = 0;               // tiles of earlier segments
-      uint32_t np[2] = {0, 0}, nseg = 0;  // P tiles per stream, segments
+      uint32_t tile0 = 0, np = 0, nseg = 0, round = 0;  // tiles of earlier segments, P tiles seen, segments, turns
+      uint32_t kn = 0, vn = 0;                          // next K and V tile to pass
       for (Segment s; ok && walk.next(p, s, lane); ++nseg) {
         const int n = s.k1 - s.k0;
-        const bool pair = s.nq == 2;
-        // stream x's j-th tile and its count
-        auto tile_of = [&](int x, int j) { return tile0 + (pair ? j : 2 * j + x); };
-        const int cnt[2] = {pair ? n : (n + 1) / 2, pair ? n : n / 2};
-        auto qk = [&](int x, int j) {  // S_x = Q_x K^T
-          const uint32_t t = tile_of(x, j);
-          const int st = t % NST;
-          if (!wait_all(&bars->k_full[st], (t / NST) & 1)) return;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t q_s = sbase + G::OFF_Q + x * 2 * G::QT, k_s = sbase + G::OFF_K + st * G::TILE;
+        if (elect_one()) {
+          const bool pair = s.nq == 2;
+          const int cnt = pair ? n : (n + 1 - x) / 2;
+          auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !mbar_wait(bar, parity, abort_flag)) {
+              ok = false;
+              set_status(p.dev_status, KVQ_DEV_TIMEOUT);
+              *abort_flag = 1;
+            }
+            return ok;
+          };
+          // Each stream passes every tile in order, the other stream's too (wait
+          // and release): a parity wait tells only neighbouring phases apart.
+          auto pass_k = [&](uint32_t upto) {
+            for (; kn < upto && wait(&bars->k_full[kn % NST], (kn / NST) & 1); ++kn) mbar_arrive(&bars->k_empty[kn % NST]);
+          };
+          auto pass_v = [&](uint32_t upto) {
+            for (; vn < upto && wait(&bars->vh_full[vn & 1], (vn >> 1) & 1); ++vn) mbar_arrive(&bars->vh_empty[vn & 1]);
+          };
+          auto qk = [&](int j) {  // S = Q K^T
+            const uint32_t t = tile0 + (pair ? j : 2 * j + x);
+            pass_k(t);
+            const int st = t % NST;
+            if (!wait(&bars->k_full[st], (t / NST) & 1)) return;
+            ++kn;
+            tc_fence_after();
+            const uint64_t kd = k_desc + st * (G::TILE >> 4);
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
 #pragma unroll
               for (int term = 0; term < 2; ++term)
-                umma_f8(tmem + x * TK, desc(q_s + term * G::QT + kk * 32), desc(k_s + kk * 32), IDESC_S, kk + term > 0 ? 1u : 0u);
+                umma_f8(s_t, q_desc + ((term * G::QT + kk * 32) >> 4), kd + ((kk * 32) >> 4), IDESC_S, kk + term > 0 ? 1u : 0u);
             umma_commit(&bars->s_full[x]);
-            if (!pair || x == 1) umma_commit(&bars->k_empty[st]);
-          }
-          __syncwarp();
-        };
-        auto pv = [&](int x, int j) {  // O_x += P_x V
-          const uint32_t t = tile_of(x, j);
-          if (!wait_all(&bars->p_full[x], np[x] & 1)) return;
-          ++np[x];
-          if (!wait_all(&bars->vh_full[t & 1], (t >> 1) & 1)) return;
-          tc_fence_after();
-          if (lane == 0) {
-            const uint32_t v_s = sbase + G::OFF_VH + (t & 1) * 2 * G::TILE;
+            umma_commit(&bars->k_empty[st]);
+          };
+          if (cnt > 0 && wait(&bars->q_full[x], nseg & 1)) qk(0);
+          // Stream 1 issues a tile's P.V only after stream 0 has issued its own
+          // and its next S: left alone the streams fall into step, and the
+          // tensor cores idle while both softmaxes run.  Stream 0 is at most a
+          // round ahead (its next V tile needs stream 1 to release one), so two
+          // barriers taken in turn keep their phases apart.
+          const int rounds = pair ? n : (n + 1) / 2;
+          for (int j = 0; ok && j < rounds; ++j, ++round) {
+            if (x == 1 && !wait(&bars->turn[round & 1], (round >> 1) & 1)) break;
+            if (j < cnt) {
+              const uint32_t t = tile0 + (pair ? j : 2 * j + x);
+              pass_v(t);
+              if (!wait(&bars->vh_full[t & 1], (t >> 1) & 1)) break;
+              ++vn;
+              // O += P V: a page per MMA (two halves of eight tokens, D * 16 bytes apart)
+              const uint64_t vd = v_desc + (t & 1) * (2 * G::TILE >> 4);
+              // the first half of the keys while the softmax works on the second
 #pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk)  // a page per MMA: two halves of eight tokens, D * 16 bytes apart
-              umma_f16_ta(tmem + 2 * TK + x * D, tmem + x * TK + kk * 8, desc_interleave(v_s + kk * 2 * G::PAGE, D * 16, 128),
-                          IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
-            if (!pair || x == 1) umma_commit(&bars->vh_empty[t & 1]);
-            if (j == cnt[x] - 1) umma_commit(&bars->o_full[x]);
-          }
-          __syncwarp();
-        };
+              for (int h = 0; h < 2; ++h) {
+                if (!wait(&bars->p_full[x][h], np & 1)) break;
+                tc_fence_after();
 #pragma unroll
-        for (int x = 0; x < 2; ++x)
-          if (cnt[x] > 0 && wait_all(&bars->q_full[x], nseg & 1)) qk(x, 0);
-        for (int j = 0; ok && j < cnt[0]; ++j) {
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (!ok || j >= cnt[x]) continue;
-            pv(x, j);
-            if (ok && j + 1 < cnt[x]) qk(x, j + 1);
+                for (int kk = h * 4; kk < h * 4 + 4; ++kk)
+                  umma_f16_ta(o_t, s_t + kk * 8, vd + ((kk * 2 * G::PAGE) >> 4), IDESC_O, (j > 0 || kk > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              ++np;
+              umma_commit(&bars->vh_empty[t & 1]);
+              if (j == cnt - 1) umma_commit(&bars->o_full[x]);
+              if (j + 1 < cnt) qk(j + 1);
+            }
+            if (x == 0) mbar_arrive(&bars->turn[round & 1]);
           }
+          pass_k(tile0 + n);
+          pass_v(tile0 + n);
         }
         tile0 += n;
+        ok = __all_sync(0xffffffffu, ok);
       }
       // every MMA has completed before the tensor memory is released
-      if (lane == 0) umma_commit(&bars->done);
+      if (elect_one()) umma_commit(&bars->done[x]);
       __syncwarp();
-      mbar_wait(&bars->done, 0);
+      mbar_wait(&bars->done[x], 0);
     }
   } else if (warp >= kSoftWarps) {
     setmaxnreg_dec<REG_CONV>();
@@ -448,30 +489,43 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         const int valid = s.L - kt * TK;  // tokens of the tile, if less than TK
         const uint8_t* src = smem + G::OFF_V + st * G::TILE;
         uint8_t* dst = smem + G::OFF_VH + (it & 1) * 2 * G::TILE;
-#pragma unroll 4
-        for (int i = t; i < TK / kPage * D; i += kConvWarps * 32) {
-          const int pg = i / D, d = i % D;
-          uint4 c = *reinterpret_cast<const uint4*>(src + i * 16);
-          const int left = valid - pg * kPage;
-          if ((dead >> pg) & 1) {
-            c = make_uint4(0, 0, 0, 0);
-          } else if (left < kPage) {
-            uint32_t w[4] = {c.x, c.y, c.z, c.w};
+        constexpr int IT = TK / kPage * D / (kConvWarps * 32), CHUNK = 4;
+        const bool edge = dead != 0 || valid < TK;
+#pragma unroll 1
+        for (int i0 = 0; i0 < IT; i0 += CHUNK) {
+          uint4 c[CHUNK];
 #pragma unroll
-            for (int tok = 0; tok < kPage; ++tok) {
-              const int sl = fp8_v_slot(tok);
-              if (tok >= left) w[sl >> 2] &= ~(0xFFu << (8 * (sl & 3)));
+          for (int u = 0; u < CHUNK; ++u)
+            c[u] = *reinterpret_cast<const uint4*>(src + (t + (i0 + u) * kConvWarps * 32) * 16);
+          if (edge) {
+#pragma unroll 1
+            for (int u = 0; u < CHUNK; ++u) {
+              const int pg = (t + (i0 + u) * kConvWarps * 32) / D, left = valid - pg * kPage;
+              uint32_t m[4] = {0, 0, 0, 0};
+              if (!((dead >> pg) & 1)) {
+#pragma unroll
+                for (int tok = 0; tok < kPage; ++tok) {
+                  const int sl = fp8_v_slot(tok);
+                  if (tok < left) m[sl >> 2] |= 0xFFu << (8 * (sl & 3));
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < CHUNK; ++k)
+                if (k == u) c[k] = make_uint4(c[k].x & m[0], c[k].y & m[1], c[k].z & m[2], c[k].w & m[3]);
             }
-            c = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          uint4 lo, hi;
-          fp8x4_to_f16x2x2<E5>(c.x, lo.x, lo.y);
-          fp8x4_to_f16x2x2<E5>(c.y, lo.z, lo.w);
-          fp8x4_to_f16x2x2<E5>(c.z, hi.x, hi.y);
-          fp8x4_to_f16x2x2<E5>(c.w, hi.z, hi.w);
-          uint8_t* o = dst + pg * 2 * G::PAGE + d * 16;
-          *reinterpret_cast<uint4*>(o) = lo;
-          *reinterpret_cast<uint4*>(o + D * 16) = hi;
+#pragma unroll
+          for (int u = 0; u < CHUNK; ++u) {
+            const int i = t + (i0 + u) * kConvWarps * 32, pg = i / D, d = i % D;
+            uint4 lo, hi;
+            fp8x4_to_f16x2x2<E5>(c[u].x, lo.x, lo.y);
+            fp8x4_to_f16x2x2<E5>(c[u].y, lo.z, lo.w);
+            fp8x4_to_f16x2x2<E5>(c[u].z, hi.x, hi.y);
+            fp8x4_to_f16x2x2<E5>(c[u].w, hi.z, hi.w);
+            uint8_t* o = dst + pg * 2 * G::PAGE + d * 16;
+            *reinterpret_cast<uint4*>(o) = lo;
+            *reinterpret_cast<uint4*>(o + D * 16) = hi;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -506,49 +560,65 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       const int r = (pair ? x * TR : 0) + row;  // row of the unit
       const bool live = r < s.rows;
       const bool warp_live = __any_sync(0xffffffffu, live);
-      // ---- the query row as two E4M3 terms, swizzled K-major ----
+      // ---- the query rows as two E4M3 terms, swizzled K-major: D / 8 lanes per
+      // row, eight dimensions each ----
       float coef = 0.f;
-      if (live) {
-        const int rr = s.row0 + r;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const __nv_bfloat16*>(p.q) +
-            (static_cast<size_t>(s.a + rr / p.g) * p.Hq + static_cast<size_t>(kvh) * p.g + rr % p.g) * D);
-        float mx = 0.f;
+      {
+        constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
+        const int sub = lane / LPR, c8 = lane % LPR;
+        // q row of this lane's own row, then of the row that each lane loads a part of
+        const int own = live ? (s.a + (s.row0 + r) / p.g) * p.Hq + kvh * p.g + (s.row0 + r) % p.g : -1;
+        auto load = [&](int i) {
+          const int qr = i < NI ? __shfl_sync(0xffffffffu, own, i * RPI + sub) : -1;
+          uint4 u = make_uint4(0, 0, 0, 0);
+          if (qr >= 0) u = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<size_t>(qr) * D) + c8);
+          return u;
+        };
+        // a loop kept small: the first segment pays for fetching its code
+        uint4 ahead[4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 u = __ldcg(src + i);
+        for (int i = 0; i < 4; ++i) ahead[i] = load(i);
+#pragma unroll 2
+        for (int i = 0; i < NI; ++i) {
+          const int rq = quarter * 32 + i * RPI + sub;  // row of the tile
+          const uint4 u = ahead[0];
+          ahead[0] = ahead[1];
+          ahead[1] = ahead[2];
+          ahead[2] = ahead[3];
+          ahead[3] = load(i + 4);
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          float v[8], mx = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx = fmax3(mx, fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
-        }
-        int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127 : 0;
-        e2 = e2 < -100 ? -100 : e2;
-        const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
-        coef = kscale * __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
-        uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + row * D;
-#pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int hw = 0; hw < 2; ++hw) {
-            const uint4 u = __ldcg(src + 2 * c + hw);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              float v[4] = {__uint_as_float(w[e] << 16) * sigma, __uint_as_float(w[e] & 0xFFFF0000u) * sigma,
-                            __uint_as_float(w[e + 1] << 16) * sigma, __uint_as_float(w[e + 1] & 0xFFFF0000u) * sigma};
-              const uint32_t h = f32x2_to_e4m3x2(v[0], v[1]) | (f32x2_to_e4m3x2(v[2], v[3]) << 16);
-              uint32_t f0, f1;
-              e4m3x4_to_f16x2x2(h, f0, f1);
-              const float2 a = __half22float2(*reinterpret_cast<__half2*>(&f0)), b = __half22float2(*reinterpret_cast<__half2*>(&f1));
-              hi[2 * hw + e / 2] = h;
-              lo[2 * hw + e / 2] = f32x2_to_e4m3x2(v[0] - a.x, v[1] - a.y) | (f32x2_to_e4m3x2(v[2] - b.x, v[3] - b.y) << 16);
-            }
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+            mx = fmax3(mx, fabsf(v[2 * e]), fabsf(v[2 * e + 1]));
           }
-          const int pc = (D == 128 ? c ^ (row & 7) : c ^ ((row >> 1) & 3)) << 4;
-          *reinterpret_cast<uint4*>(qs + pc) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(qs + G::QT + pc) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127 : 0;
+          e2 = e2 < -100 ? -100 : e2;
+          const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+          const float inv = __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+#pragma unroll
+          for (int h = 0; h < RPI; ++h) {
+            const float ih = __shfl_sync(0xffffffffu, inv, h * LPR);
+            if (lane == i * RPI + h) coef = kscale * ih;
+          }
+          uint32_t hi[2], lo[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float a0 = v[4 * e] * sigma, a1 = v[4 * e + 1] * sigma, a2 = v[4 * e + 2] * sigma, a3 = v[4 * e + 3] * sigma;
+            hi[e] = f32x2_to_e4m3x2(a0, a1) | (f32x2_to_e4m3x2(a2, a3) << 16);
+            uint32_t f0, f1;
+            e4m3x4_to_f16x2x2(hi[e], f0, f1);
+            const float2 b0 = __half22float2(*reinterpret_cast<__half2*>(&f0)), b1 = __half22float2(*reinterpret_cast<__half2*>(&f1));
+            lo[e] = f32x2_to_e4m3x2(a0 - b0.x, a1 - b0.y) | (f32x2_to_e4m3x2(a2 - b1.x, a3 - b1.y) << 16);
+          }
+          const int c = c8 >> 1;  // 16-byte chunk of the row
+          uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + rq * D + ((D == 128 ? c ^ (rq & 7) : c ^ ((rq >> 1) & 3)) << 4) + (c8 & 1) * 8;
+          *reinterpret_cast<uint2*>(qs) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(qs + G::QT) = make_uint2(lo[0], lo[1]);
         }
       }
       fence_proxy_async_smem();
@@ -562,39 +632,30 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           const uint32_t t = tile0 + (pair ? j : 2 * j + x);
           const int kt = s.k0 + (pair ? j : 2 * j + x);
           const uint32_t bad = reinterpret_cast<volatile uint32_t*>(bars->k_bad)[t % kInfo];
-          float sv[TK];
-          {
-            uint32_t v[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_t + 32 * c, v[c]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_pin32(v[c]);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) sv[32 * c + i] = __uint_as_float(v[c][i]);
-            }
-          }
           const int valid = s.L - kt * TK;
-          if (bad != 0 || valid < TK) {
+          const bool edge = bad != 0 || valid < TK;
+          uint32_t v[4][32];
 #pragma unroll
-            for (int k = 0; k < TK; ++k) sv[k] = (k >= valid || ((bad >> (k / kPage)) & 1)) ? -INFINITY : sv[k];
+          for (int c = 0; c < 4; ++c) tmem_ld32_nowait(s_t + 32 * c, v[c]);
+          tmem_wait_ld();
+          float mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_pin32(v[c]);
+            if (edge) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i >= valid || ((bad >> (2 * c + i / kPage)) & 1)) v[c][i] = __float_as_uint(-INFINITY);
+            }
+            float m1[11];
+#pragma unroll
+            for (int i = 0; i < 10; ++i)
+              m1[i] = fmax3(__uint_as_float(v[c][3 * i]), __uint_as_float(v[c][3 * i + 1]), __uint_as_float(v[c][3 * i + 2]));
+            m1[10] = fmaxf(__uint_as_float(v[c][30]), __uint_as_float(v[c][31]));
+            mx = fmax3(mx, fmax3(fmax3(m1[0], m1[1], m1[2]), fmax3(m1[3], m1[4], m1[5]), fmax3(m1[6], m1[7], m1[8])),
+                       fmaxf(m1[9], m1[10]));
           }
-          float mx;
-          {
-            float m1[43];
-#pragma unroll
-            for (int i = 0; i < 42; ++i) m1[i] = fmax3(sv[3 * i], sv[3 * i + 1], sv[3 * i + 2]);
-            m1[42] = fmaxf(sv[126], sv[127]);
-            float m2[15];
-#pragma unroll
-            for (int i = 0; i < 14; ++i) m2[i] = fmax3(m1[3 * i], m1[3 * i + 1], m1[3 * i + 2]);
-            m2[14] = m1[42];
-            float m3[5];
-#pragma unroll
-            for (int i = 0; i < 5; ++i) m3[i] = fmax3(m2[3 * i], m2[3 * i + 1], m2[3 * i + 2]);
-            mx = fmax3(fmaxf(m3[0], m3[1]), fmaxf(m3[2], m3[3]), m3[4]) * coef;
-          }
+          mx *= coef;
           const bool move = live && mx > M + kSlack;  // M = -inf: the first tile with a live key
           if (j > 0 && __any_sync(0xffffffffu, move)) {
             const float a = move ? ex2(M - mx) : 1.f;
@@ -614,24 +675,29 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           const float2 coef2 = make_float2(coef, coef), nb2 = make_float2(nb, nb);
           float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // 32 keys: two pages, 16 words of two slots
+          for (int c = 0; c < 4; ++c) {  // 32 keys (two pages), 16 words of two slots
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const int k = 32 * c + (i >> 3) * 16 + (i & 1) * 8 + ((i & 7) >> 1) * 2;  // tokens of slots 2i, 2i + 1
-              float2 e = ffma2(make_float2(sv[k], sv[k + 1]), coef2, nb2);
+              const int k = (i >> 3) * 16 + (i & 1) * 8 + ((i & 7) >> 1) * 2;  // tokens of slots 2i, 2i + 1
+              float2 e = ffma2(make_float2(__uint_as_float(v[c][k]), __uint_as_float(v[c][k + 1])), coef2, nb2);
               e.x = ex2(e.x);
               e.y = ex2(e.y);
               sum = fadd2(sum, e);
               w[i] = pack_f16x2(e.x, e.y);
             }
-            tmem_st16(s_t + 16 * c, w);
+            tmem_st16(s_t + 16 * c, w);  // over S, which the registers hold
+            if (c & 1) {
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&bars->p_full[x][c >> 1]);
+            }
           }
           l += sum.x + sum.y;
-          tmem_wait_st();
+        } else {
+          mbar_arrive(&bars->p_full[x][0]);
+          mbar_arrive(&bars->p_full[x][1]);
         }
-        tc_fence_before();
-        mbar_arrive(&bars->p_full[x]);
       }
       tile0 += n;
       if (!ok) break;
@@ -641,18 +707,31 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         ++nseg;
         tc_fence_after();
         const float f = l > 0.f ? vscale / l : 0.f;
-        float4* dst = reinterpret_cast<float4*>(p.o_part + idx * D);
+        // A lane holds a row; through shared memory the rows leave as 128-byte
+        // runs instead of 16-byte ones (which cost 9,000 cycles per segment).
+        constexpr int PITCH = G::PITCH;
+        float* stage = reinterpret_cast<float*>(smem + G::OFF_STAGE + warp * G::STAGE_WARP);
+        const int nrow = min(32, s.rows - (pair ? x * TR : 0) - quarter * 32);  // live rows of the warp
+        float* dst = p.o_part + (idx - lane) * D;
         if (warp_live) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t o[32];
             tmem_ld32(o_t + 32 * c, o);
-            if (live) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[8 * c + i] = make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
-                                             __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float4*>(stage + lane * PITCH + 4 * i) =
+                  make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
+                              __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int rr = 4 * i + (lane >> 3);
+              if (rr < nrow)
+                *reinterpret_cast<float4*>(dst + rr * D + 32 * c + 4 * (lane & 7)) =
+                    *reinterpret_cast<const float4*>(stage + rr * PITCH + 4 * (lane & 7));
             }
+            __syncwarp();
           }
         }
         tc_fence_before();
@@ -695,17 +774,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
   int ns = 0, halves = 1;
   size_t first = 0;
   {
-    const int64_t W = total_cost(p, lane, false), N = used_slots(p, W);
-    int64_t gstart = 0;
-    int ubase = 0;
+    int W = 0, gstart = 0, ubase = 0, c0 = 0, c1 = 0;
+    bool found = false;
+#pragma unroll 1
     for (int base = 0; base < p.G; base += 32) {
       Group r = {};
       if (base + lane < p.G) r = group_of(p, base + lane, false);
-      int64_t c = r.cost();
-      int u = r.units();
+      int c = r.cost(), u = r.units();
       scan_groups(c, u, lane);
       const uint32_t hit = __ballot_sync(0xffffffffu, base + lane < p.G && b >= r.a && b < r.a + r.nb);
-      if (hit) {
+      if (hit && !found) {
+        found = true;
         const int at = __ffs(hit) - 1;
         const int a = __shfl_sync(0xffffffffu, r.a, at), K = __shfl_sync(0xffffffffu, r.K, at);
         const int tiles = __shfl_sync(0xffffffffu, r.tiles, at);
@@ -713,46 +792,87 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
         ubase += __shfl_sync(0xffffffffu, u - r.units(), at);
         const int row = (b - a) * p.g + hq % p.g, un = row / UNIT;
         const int nq = min(2, tiles - 2 * un);
-        if (K > 0 && ubase + un < p.max_units) {
-          const int64_t c0 = gstart + static_cast<int64_t>(un) * 2 * K, c1 = c0 + static_cast<int64_t>(nq) * K;
-          const int s0 = static_cast<int>(((c0 + 1) * N + W - 1) / W) - 1;
-          const int s1 = static_cast<int>((c1 * N + W - 1) / W) - 1;
-          ns = s1 - s0 + 1;
-          halves = nq == 1 ? 2 : 1;
-          first = (static_cast<size_t>(hq / p.g) * p.kseg + s0 + ubase + un) * UNIT + row % UNIT;
-        }
-        break;
+        c0 = gstart + un * 2 * K;
+        c1 = ubase + un < p.max_units ? c0 + nq * K : c0;
+        halves = nq == 1 ? 2 : 1;
+        first = (static_cast<size_t>(hq / p.g) * p.kseg + ubase + un) * UNIT + row % UNIT;
       }
-      gstart += __shfl_sync(0xffffffffu, c, 31);
-      ubase += __shfl_sync(0xffffffffu, u, 31);
+      const int ct = __shfl_sync(0xffffffffu, c, 31);
+      W += ct;
+      if (!found) {
+        gstart += ct;
+        ubase += __shfl_sync(0xffffffffu, u, 31);
+      }
+    }
+    if (c1 > c0) {
+      const Cut cut(p, W);
+      const int s0 = cut.slot_of(c0);
+      ns = cut.slot_of(c1 - 1) - s0 + 1;
+      first += static_cast<size_t>(s0) * UNIT;
     }
   }
   grid_dependency_wait();
+  // Partial i of the row: prefix partials first, then the own tokens'.  A warp
+  // takes 32 of them at a time: a lane per log-sum-exp, then the outputs of
+  // those that carry weight, eight loads in flight.
   const int np = ns * halves, total = np + mp.per_row;
-  auto at = [&](int i, const float*& o, const float*& l) {
-    if (i < np) {
-      const size_t idx = first + static_cast<size_t>(i / halves) * UNIT + (i % halves) * TR;
-      o = p.o_part + idx * D;
-      l = p.lse_part + idx;
-    } else {
-      const size_t idx = static_cast<size_t>(blockIdx.x) * mp.per_row + (i - np);
-      o = mp.o_own + idx * D;
-      l = mp.lse_own + idx;
-    }
-  };
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  for (int i = wid; i < total; i += kMergeWarps) {
-    const float *op, *lp;
-    at(i, op, lp);
-    const float x = *lp;
-    if (x == -INFINITY) continue;
-    const float mn = fmaxf(m, x), a = ex2(m - mn), w = ex2(x - mn);
-    l = l * a + w;
+  for (int i0 = wid; i0 < total; i0 += 32 * kMergeWarps) {
+    const int i = i0 + lane * kMergeWarps;
+    const float* op = nullptr;
+    float x = -INFINITY;
+    if (i < np) {
+      const size_t idx = first + static_cast<size_t>(halves == 2 ? i >> 1 : i) * UNIT + (halves == 2 ? (i & 1) * TR : 0);
+      x = __ldcg(p.lse_part + idx);
+      op = p.o_part + idx * D;
+    } else if (i < total) {
+      const size_t idx = static_cast<size_t>(blockIdx.x) * mp.per_row + (i - np);
+      x = __ldcg(mp.lse_own + idx);
+      op = mp.o_own + idx * D;
+    }
+    float mn = x;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(w, op[lane * E + e], acc[e] * a);
+    for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mn = fmaxf(mn, m);
+    if (mn == -INFINITY) continue;  // uniform
+    const float w = ex2(x - mn), a = ex2(m - mn);
     m = mn;
+    l *= a;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= a;
+    uint32_t todo = __ballot_sync(0xffffffffu, w > 0.f);
+    while (todo) {
+      float wk[8];
+      float o[8][E];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int src = todo ? __ffs(todo) - 1 : 0;
+        const bool on = todo != 0;
+        todo &= todo - 1;
+        const float* ok_ = reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(op), src));
+        const float ws = __shfl_sync(0xffffffffu, w, src);
+        wk[k] = on ? ws : 0.f;
+        if constexpr (E == 4) {
+          const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(ok_) + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+          o[k][0] = t.x;
+          o[k][1] = t.y;
+          o[k][2] = t.z;
+          o[k][3] = t.w;
+        } else {
+          const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(ok_) + lane) : make_float2(0.f, 0.f);
+          o[k][0] = t.x;
+          o[k][1] = t.y;
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        l += wk[k];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(wk[k], o[k][e], acc[e]);
+      }
+    }
   }
   if (lane == 0) {
     m_s[wid] = m;
@@ -871,7 +991,8 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
     return fail(KVQ_ERR_INVALID_ARG, "shared_prefix: misaligned pointer");
   const int64_t g = Hq / Hkv;
   if (static_cast<int64_t>(max_prefix_blocks) * P > 0x7FFFFFFFll - TK || static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFFll - TK ||
-      static_cast<int64_t>(B) * Hq > 0x7FFFFFFFll || B * g > 0x7FFFFFFFll - TR || prefix_units(B, G, g) > 0x3FFFFFFF)
+      static_cast<int64_t>(B) * Hq > 0x7FFFFFFFll || B * g > 0x7FFFFFFFll - TR || prefix_units(B, G, g) > 0x3FFFFFFF ||
+      2 * prefix_units(B, G, g) * ((static_cast<int64_t>(max_prefix_blocks) * P + TK - 1) / TK) > 0x7FFFFFFFll)
     return fail(KVQ_ERR_UNSUPPORTED, "shared_prefix: problem too large");
   const DecodePartialPlan own = decode_partial_plan(B, Hq, Hkv, D, max_blocks);
   if (static_cast<int64_t>(B) * Hkv * own.splits > 0x7FFFFFFFll)
