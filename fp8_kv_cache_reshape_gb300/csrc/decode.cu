@@ -32,12 +32,15 @@
 // ordered so that consecutive CTAs serve different (sequence, KV head)
 // pairs.  A combine kernel, launched as a programmatic dependent of the
 // partial kernel, merges the S x NW partials of each query head in one pass.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <mutex>
+#include <type_traits>
 
 #include "kvq_device.cuh"
 #include "kvq_host.h"
+#include "kvq_plan.cuh"
 
 namespace kvq {
 
@@ -109,6 +112,7 @@ struct Geo {
 };
 
 constexpr int kNW = 4;     // consumer warps per CTA
+static_assert(kNW == kPartialWarps, "partials per segment");
 // Resident CTAs per SM: 3, and 4 at head dim 64, whose stages carry half the
 // bytes for the same per-stage work (the softmax of 32 tokens), so more
 // consumer warps per SM keep the pages streaming.
@@ -274,12 +278,30 @@ struct SegCursor {
   int item;
   int pos, end;  // balanced: the slot's remaining stream pages [pos, end)
   int b;         // balanced: the next sequence to look at; per-sequence: 1 once returned
+  int start;     // BAL 2: that sequence's first stream page
 };
-template <bool BAL>
+// BAL 2, batches of up to kWideBatch sequences (partials only): the same cut of
+// the batch's page stream into p.num_slots slots per KV head, at least
+// kWidePages pages each.  The first sequence of a slot is found by one scan of
+// the lengths; the cursor then walks them one by one.
+template <int BAL>
 KVQ_DEVINL SegCursor seg_begin(const DecodeParams& p, int item, int lane, bool spec) {
   SegCursor c;
   c.item = item;
   c.pos = c.end = c.b = 0;
+  if constexpr (BAL == 2) {
+    const WideScan ws = wide_scan(p.seq_lens, p.B, p.max_blocks, lane, spec);
+    const int64_t T = ws.total;
+    const int64_t N = wide_slots(p.num_slots, p.B, ws.total);
+    const int slot = item / p.Hkv;
+    c.start = 0;
+    if (slot < N) {
+      c.pos = static_cast<int>(slot * T / N);
+      c.end = static_cast<int>((slot + 1) * T / N);
+      wide_find(p.seq_lens, p.B, p.max_blocks, ws, c.pos, lane, spec, c.b, c.start);
+    }
+    return c;
+  }
   if constexpr (BAL) {
     const BatchScan bs = batch_scan(p, lane, spec, false);
     const int64_t T = bs.total;
@@ -294,8 +316,30 @@ KVQ_DEVINL SegCursor seg_begin(const DecodeParams& p, int item, int lane, bool s
   }
   return c;
 }
-template <bool BAL>
+template <int BAL>
 KVQ_DEVINL bool seg_next(const DecodeParams& p, SegCursor& c, ItemRange& r, int lane, bool spec, bool report) {
+  if constexpr (BAL == 2) {
+    while (c.pos < c.end && c.b < p.B) {
+      const int L = wide_len(p.seq_lens, c.b, p.max_blocks, spec);
+      const int pages = (L + kPage - 1) / kPage;
+      if (c.start + pages <= c.pos) {  // sequence b ends before pos (or is empty)
+        c.start += pages;
+        ++c.b;
+        continue;
+      }
+      const int stop = min(c.end, c.start + pages);
+      r.b = c.b;
+      r.kvh = c.item % p.Hkv;
+      r.split = c.item / p.Hkv;
+      r.lo = 0;
+      r.hi = L;
+      r.pg0 = c.pos - c.start;
+      r.n = stop - c.pos;
+      c.pos = stop;
+      return true;
+    }
+    return false;
+  }
   if constexpr (!BAL) {
     if (c.b) return false;
     r = item_range(p, c.item, report);
@@ -330,7 +374,7 @@ KVQ_DEVINL bool seg_next(const DecodeParams& p, SegCursor& c, ItemRange& r, int 
 }
 
 // Every segment of this CTA's items (item = blockIdx.x, + gridDim.x, ...).
-template <bool BAL>
+template <int BAL>
 struct SegWalk {
   SegCursor c;
   KVQ_DEVINL SegWalk(const DecodeParams& p, int lane) {
@@ -350,7 +394,7 @@ struct SegWalk {
 };
 // The per-sequence plan: one segment per item.
 template <>
-struct SegWalk<false> {
+struct SegWalk<0> {
   int item;
   bool started;
   KVQ_DEVINL SegWalk(const DecodeParams&, int) : item(blockIdx.x), started(false) {}
@@ -370,15 +414,15 @@ struct SegWalk<false> {
 // the wait; loads cached in L2 only leave no stale L1 line), clamped so that
 // every address stays inside the block table and the caches.  A page the
 // preceding kernel writes after the hint is updated in L2 like any other.
-template <int D, bool FP8, bool PT, bool BAL>
+template <int D, bool FP8, bool PT, int BAL>
 KVQ_DEVINL void prefetch_first_pages(const DecodeParams& p, int lane, int max_pages) {
   using G = Geo<D, FP8>;
   constexpr int VS = v_stride<D, FP8, PT>();
   int b, kvh, pg0, n;
   if constexpr (BAL) {
-    SegCursor cur = seg_begin<true>(p, blockIdx.x, lane, true);
+    SegCursor cur = seg_begin<BAL>(p, blockIdx.x, lane, true);
     ItemRange r;
-    if (!seg_next<true>(p, cur, r, lane, true, false)) return;
+    if (!seg_next<BAL>(p, cur, r, lane, true, false)) return;
     b = r.b;
     kvh = r.kvh;
     pg0 = r.pg0;
@@ -421,14 +465,14 @@ constexpr int kPresent0 = 1, kPresent1 = 2, kBad0 = 4, kBad1 = 8;
 // AP: the append entry point's instantiation (the new token's cache write);
 // the plain decode is compiled without it.
 // SC: the weights entry point's instantiation (p.scores is written).
-template <int D, bool FP8, int NW, int NST, bool E5, bool PT, bool SL, bool AP = false, bool BAL = false,
+template <int D, bool FP8, int NW, int NST, bool E5, bool PT, bool SL, bool AP = false, int BAL = 0,
           bool SC = false>
 __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partial_kernel(const __grid_constant__ DecodeParams p) {
   using G = Geo<D, FP8>;
   static_assert(NST % NW == 0 && NST >= NW, "each ring slot must belong to one consumer warp");
   static_assert(FP8 || !PT, "per-token scales apply to FP8 caches");
   static_assert(!SL || (FP8 && !PT), "the single-level ablation covers the per-head FP8 path");
-  static_assert(!BAL || (D == 128 && FP8 && !E5 && !PT && !SL), "the balanced plan covers the E4M3 per-head path");
+  static_assert(BAL != 1 || (D == 128 && FP8 && !E5 && !PT && !SL), "the balanced plan covers the E4M3 per-head path");
   constexpr int STRIDE = stage_stride<D, FP8, PT>();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* stages = smem;
@@ -474,6 +518,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
     // faults in the lengths: reported by lane 0 per item, or (balanced) by the
     // lane of each sequence in CTA 0
     const bool report = BAL ? blockIdx.x == 0 : lane == 0;
+    if constexpr (BAL == 2) {
+      if (blockIdx.x == 0)
+        for (int b = lane; b < p.B; b += 32) seq_len_of(p.seq_lens, b, p.max_blocks, p.dev_status, true);
+    }
     for (ItemRange r; !aborted && walk.next(p, lane, r, report);) {
       const int32_t* bt = p.block_table + static_cast<size_t>(r.b) * p.max_blocks + r.pg0;
       // append: this item holds the page of the sequence's last token
@@ -1334,7 +1382,7 @@ size_t partial_count(int B, int Hq, int S) {
   return static_cast<size_t>(B) * Hq * S * kNW;
 }
 
-template <int D, bool FP8, bool E5 = false, bool PT = false, bool SL = false, bool AP = false, bool BAL = false,
+template <int D, bool FP8, bool E5 = false, bool PT = false, bool SL = false, bool AP = false, int BAL = 0,
           bool SC = false>
 kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream_t s,
                            WeightsParams* weights = nullptr, bool partials_only = false) {
@@ -1428,19 +1476,30 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
 
 using namespace kvq;
 
-// The per-sequence plan's partials without the combine (a caller with further
-// partials of the same rows merges them itself).
+// The wide balanced plan's partials without the combine (a caller with further
+// partials of the same rows merges them itself).  Batches beyond kWideBatch
+// keep one range per (sequence, KV head): with that many, several to a CTA,
+// their lengths average out.
 DecodePartialPlan kvq::decode_partial_plan(int B, int Hq, int Hkv, int D, int max_blocks) {
-  int S, pps;
-  split_plan(B, Hkv, D, kPage, max_blocks, -1, 0, &S, &pps);
-  DecodePartialPlan d;
-  d.splits = S;
-  d.per_row = S * kNW;
-  d.rows = static_cast<size_t>(B) * Hq * S * kNW;
+  DecodePartialPlan d = {};
+  if (B > kWideBatch) {
+    int S, pps;
+    split_plan(B, Hkv, D, kPage, max_blocks, -1, 0, &S, &pps);
+    d.splits = S;
+    d.rows = static_cast<size_t>(B) * Hq * S * kNW;
+    d.items = static_cast<int64_t>(B) * Hkv * S;
+    return d;
+  }
+  const int64_t pages = static_cast<int64_t>(B) * max_blocks;
+  int64_t slots = ctas_per_sm_of(D) * sm_count() / Hkv;
+  slots = wide_slots(static_cast<int>(slots), B, static_cast<int>(std::min<int64_t>(pages, 0x7FFFFFFF)));
+  d.slots = static_cast<int>(std::max<int64_t>(slots, 1));
+  d.rows = static_cast<size_t>(Hq) * (d.slots + B - 1) * kNW;
+  d.items = static_cast<int64_t>(d.slots) * Hkv;
   return d;
 }
 
-kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, cudaStream_t s) {
+kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, const DecodePartialPlan& plan, cudaStream_t s) {
   DecodeParams prm = {};
   prm.q = a.q;
   prm.k_cache = a.k_cache;
@@ -1459,8 +1518,10 @@ kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, cudaStream_t s) {
   prm.num_blocks = a.num_blocks;
   prm.sm_scale = a.sm_scale;
   prm.window = -1;
-  prm.num_splits = a.splits;
-  prm.num_items = a.B * a.Hkv * a.splits;
+  prm.num_splits = plan.splits;
+  prm.num_items = static_cast<int>(plan.items);
+  prm.num_slots = plan.slots;
+  prm.kseg = plan.slots + a.B - 1;
   prm.dev_status = a.dev_status;
   prm.stall_ns = stall_ns();
   const int64_t page_b = static_cast<int64_t>(kPage) * a.D;
@@ -1468,11 +1529,15 @@ kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, cudaStream_t s) {
   prm.k_str = ps.k;
   prm.v_str = ps.v;
   prm.paired = ps.paired ? 1 : 0;
-  if (a.e5m2)
-    return a.D == 128 ? launch_decode<128, true, true>(prm, nullptr, s, nullptr, true)
-                      : launch_decode<64, true, true>(prm, nullptr, s, nullptr, true);
-  return a.D == 128 ? launch_decode<128, true>(prm, nullptr, s, nullptr, true)
-                    : launch_decode<64, true>(prm, nullptr, s, nullptr, true);
+  auto run = [&](auto dim) {
+    constexpr int D = decltype(dim)::value;
+    if (plan.slots)
+      return a.e5m2 ? launch_decode<D, true, true, false, false, false, 2>(prm, nullptr, s, nullptr, true)
+                    : launch_decode<D, true, false, false, false, false, 2>(prm, nullptr, s, nullptr, true);
+    return a.e5m2 ? launch_decode<D, true, true>(prm, nullptr, s, nullptr, true)
+                  : launch_decode<D, true>(prm, nullptr, s, nullptr, true);
+  };
+  return a.D == 128 ? run(std::integral_constant<int, 128>()) : run(std::integral_constant<int, 64>());
 }
 
 extern "C" int kvq_decode_num_splits(int B, int Hkv, int D, int P, int max_blocks, int window, int num_splits) {
@@ -1625,21 +1690,21 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
     wp.gp = prm.gp;
     if (per_token) {
       if (D == 128)
-        return e5 ? launch_decode<128, true, true, true, false, false, false, true>(prm, o, s, &wp)
-                  : launch_decode<128, true, false, true, false, false, false, true>(prm, o, s, &wp);
-      return e5 ? launch_decode<64, true, true, true, false, false, false, true>(prm, o, s, &wp)
-                : launch_decode<64, true, false, true, false, false, false, true>(prm, o, s, &wp);
+        return e5 ? launch_decode<128, true, true, true, false, false, 0, true>(prm, o, s, &wp)
+                  : launch_decode<128, true, false, true, false, false, 0, true>(prm, o, s, &wp);
+      return e5 ? launch_decode<64, true, true, true, false, false, 0, true>(prm, o, s, &wp)
+                : launch_decode<64, true, false, true, false, false, 0, true>(prm, o, s, &wp);
     }
     if (e5)
-      return D == 128 ? launch_decode<128, true, true, false, false, false, false, true>(prm, o, s, &wp)
-                      : launch_decode<64, true, true, false, false, false, false, true>(prm, o, s, &wp);
+      return D == 128 ? launch_decode<128, true, true, false, false, false, 0, true>(prm, o, s, &wp)
+                      : launch_decode<64, true, true, false, false, false, 0, true>(prm, o, s, &wp);
     if (D == 128) {
-      if (prm.balanced) return launch_decode<128, true, false, false, false, false, true, true>(prm, o, s, &wp);
-      return fp8 ? launch_decode<128, true, false, false, false, false, false, true>(prm, o, s, &wp)
-                 : launch_decode<128, false, false, false, false, false, false, true>(prm, o, s, &wp);
+      if (prm.balanced) return launch_decode<128, true, false, false, false, false, 1, true>(prm, o, s, &wp);
+      return fp8 ? launch_decode<128, true, false, false, false, false, 0, true>(prm, o, s, &wp)
+                 : launch_decode<128, false, false, false, false, false, 0, true>(prm, o, s, &wp);
     }
-    return fp8 ? launch_decode<64, true, false, false, false, false, false, true>(prm, o, s, &wp)
-               : launch_decode<64, false, false, false, false, false, false, true>(prm, o, s, &wp);
+    return fp8 ? launch_decode<64, true, false, false, false, false, 0, true>(prm, o, s, &wp)
+               : launch_decode<64, false, false, false, false, false, 0, true>(prm, o, s, &wp);
   }
   if (single_level) {
     if (cache_dtype != KVQ_DTYPE_FP8_E4M3 || per_token)
@@ -1657,7 +1722,7 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
       return D == 128 ? launch_decode<128, true, true, false, false, true>(prm, o, s)
                       : launch_decode<64, true, true, false, false, true>(prm, o, s);
     if (D == 128) {
-      if (prm.balanced) return launch_decode<128, true, false, false, false, true, true>(prm, o, s);
+      if (prm.balanced) return launch_decode<128, true, false, false, false, true, 1>(prm, o, s);
       return fp8 ? launch_decode<128, true, false, false, false, true>(prm, o, s)
                  : launch_decode<128, false, false, false, false, true>(prm, o, s);
     }
@@ -1666,7 +1731,7 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   }
   if (e5) return D == 128 ? launch_decode<128, true, true>(prm, o, s) : launch_decode<64, true, true>(prm, o, s);
   if (D == 128) {
-    if (prm.balanced) return launch_decode<128, true, false, false, false, false, true>(prm, o, s);
+    if (prm.balanced) return launch_decode<128, true, false, false, false, false, 1>(prm, o, s);
     return fp8 ? launch_decode<128, true>(prm, o, s) : launch_decode<128, false>(prm, o, s);
   }
   return fp8 ? launch_decode<64, true>(prm, o, s) : launch_decode<64, false>(prm, o, s);

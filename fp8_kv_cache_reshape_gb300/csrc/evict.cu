@@ -100,10 +100,10 @@ KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint32_t dyn[];
   uint32_t* keys = dyn;  // [seg_cap]
-  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t hist[3][kBins];  // one per pass; the leader's collect the cluster's
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ int totals[2];  // this CTA's counts above and at the threshold, read by the cluster
-  __shared__ uint32_t found[2];  // chosen bin, keys still needed inside it
+  __shared__ uint32_t found[3][2];  // per pass: chosen bin, keys still needed inside it
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
@@ -138,55 +138,70 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     }
     return;
   }
+  auto sync_all = [&]() {
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+  };
   const int seg = (N + C - 1) / C;
   const int i0 = min(N, rank * seg), i1 = min(N, i0 + seg), len = i1 - i0;
   const float* wseg = w + cut.s + i0;
   const bool held = len <= p.seg_cap;
-  if (held)
+  for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
+  if (held) {
+#pragma unroll 4
     for (int i = tid; i < len; i += kSelThreads) keys[i] = weight_key(wseg[i]);
+  }
   auto key_at = [&](int i) { return held ? keys[i] : weight_key(wseg[i]); };
+  sync_all();  // every histogram is zero
 
-  // threshold: the m-th largest key, digit by digit from the top
+  // threshold: the m-th largest key, digit by digit from the top.  The CTAs add
+  // their counts to the leader's histogram (bins that hold any: few), which
+  // finds the digit and hands it out.
   uint32_t prefix = 0, mask = 0;
   int need = m;
   constexpr int kShift[3] = {21, 10, 0};
-#pragma unroll
+#pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = kShift[pass], bins = pass < 2 ? 2048 : 1024;
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
+#pragma unroll 4
     for (int i = tid; i < len; i += kSelThreads) {
       const uint32_t k = key_at(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+      if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
     }
-    cluster.sync();
-    // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
-    uint32_t c0 = 0, c1 = 0;
-    const int hi = kBins - 1 - 2 * tid;
-    for (int k = 0; k < C; ++k) {
-      const uint32_t* other = cluster.map_shared_rank(hist, k);
-      c0 += other[hi];
-      c1 += other[hi - 1];
+    if (rank != 0) {
+      __syncthreads();
+      uint32_t* lead = cluster.map_shared_rank(&hist[pass][0], 0);
+      for (int i = tid; i < bins; i += kSelThreads) {
+        const uint32_t c = hist[pass][i];
+        if (c) atomicAdd(lead + i, c);
+      }
     }
-    int tot;
-    const int excl = warp_scan_excl(static_cast<int>(c0 + c1), lane, tot);
-    if (lane == 0) warp_gt[wid] = tot;
-    __syncthreads();
-    int before = excl;
-    {
+    sync_all();
+    if (rank == 0) {
+      // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
+      const int hi = kBins - 1 - 2 * tid;
+      const uint32_t c0 = hist[pass][hi], c1 = hist[pass][hi - 1];
+      int tot;
+      const int excl = warp_scan_excl(static_cast<int>(c0 + c1), lane, tot);
+      if (lane == 0) warp_gt[wid] = tot;
+      __syncthreads();
       int all;
       const int wx = warp_scan_excl(warp_gt[lane], lane, all);
-      before += __shfl_sync(0xffffffffu, wx, wid);
+      const int before = excl + __shfl_sync(0xffffffffu, wx, wid);
+      if (before < need && before + static_cast<int>(c0 + c1) >= need) {  // exactly one thread
+        const bool first = before + static_cast<int>(c0) >= need;
+        const uint32_t bin = first ? hi : hi - 1, left = need - (first ? before : before + static_cast<int>(c0));
+        for (int k = 0; k < C; ++k) {
+          uint32_t* f = cluster.map_shared_rank(&found[pass][0], k);
+          f[0] = bin;
+          f[1] = left;
+        }
+      }
     }
-    if (before < need && before + static_cast<int>(c0 + c1) >= need) {  // exactly one thread
-      const bool first = before + static_cast<int>(c0) >= need;
-      found[0] = first ? hi : hi - 1;
-      found[1] = need - (first ? before : before + static_cast<int>(c0));
-    }
-    cluster.sync();  // every CTA has read this histogram; found is set
-    prefix |= found[0] << shift;
+    sync_all();
+    prefix |= found[pass][0] << shift;
     mask |= static_cast<uint32_t>(bins - 1) << shift;
-    need = static_cast<int>(found[1]);
+    need = static_cast<int>(found[pass][1]);
   }
   // prefix is the threshold; of the keys equal to it the first `need` are taken
   const int sub = (((len + kSelWarps - 1) / kSelWarps) + 31) / 32 * 32;
@@ -209,14 +224,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     totals[0] = gt_all;
     totals[1] = eq_all;
   }
-  cluster.sync();
+  sync_all();
   int gt_before = __shfl_sync(0xffffffffu, gx, wid), eq_before = __shfl_sync(0xffffffffu, ex, wid);
   for (int k = 0; k < rank; ++k) {
     const int* other = cluster.map_shared_rank(totals, k);
     gt_before += other[0];
     eq_before += other[1];
   }
-  cluster.sync();  // no CTA leaves while its totals may be read
+  if (C > 1) cluster.sync();  // no CTA leaves while its totals may be read
   const uint32_t below = (1u << lane) - 1u;
   for (int j = j0; j < j1; j += 32) {
     const int i = j + lane;
@@ -237,11 +252,20 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
 
 // ------------------------------------------------------------------ move ---
 constexpr int kMoveWarps = 4;
+KVQ_DEVINL void load16(const uint8_t* src, uint32_t* w) {
+  const uint4 v = __ldcg(reinterpret_cast<const uint4*>(src));
+  w[0] = v.x;
+  w[1] = v.y;
+  w[2] = v.z;
+  w[3] = v.w;
+}
 
 // One warp per (sequence, KV head, destination page).  K: 16-byte chunks, row
-// by row, each swizzled for its source and its destination row.  V: a lane per
-// dimension row; the row's 16 tokens come from up to 16 source pages, one
-// 32-bit word each, and are put together with byte permutes.
+// by row, each swizzled for its source and its destination row.  V: the lanes
+// hold the rows (dimensions) of one source page at a time, read whole, and put
+// the kept tokens' bytes into their destination rows with byte permutes.
+// (Reading one 32-bit word per row and token instead touches every sector as
+// often as the page holds kept tokens: 80 against XX us for 8 x 20K to 8K.)
 template <int D, int ESZ, bool PT>
 __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int ROWB = D * ESZ;
@@ -283,44 +307,67 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
     const int so = __shfl_sync(0xffffffffu, src_off, t);
     if (sp >= 0)
       *reinterpret_cast<uint4*>(kd + k_off(t, j)) =
-          *reinterpret_cast<const uint4*>(p.k_cache + sp * p.k_str + k_off(so, j));
+          __ldcg(reinterpret_cast<const uint4*>(p.k_cache + sp * p.k_str + k_off(so, j)));
   }
   constexpr int WORDS = kPage * ESZ / 4;  // 32-bit words of a V row
-  for (int d = lane; d < D; d += 32) {
-    uint32_t row[WORDS];
-    uint32_t* dst = reinterpret_cast<uint32_t*>(vd + d * kPage * ESZ);
-    if (live != 0xFFFFu) {
+  constexpr int VEC = WORDS / 4;          // 16-byte pieces of a V row
+  constexpr int RPL = D / 32 < 4 / VEC ? D / 32 : 4 / VEC;  // rows per lane at a time
+#pragma unroll 1
+  for (int d0 = lane; d0 < D; d0 += 32 * RPL) {
+    uint32_t row[RPL][WORDS], cur[RPL][WORDS];
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) row[i] = dst[i];
-    } else {
+    for (int i = 0; i < RPL; ++i) {
+      if (live != 0xFFFFu) {  // slots of other tokens stay
 #pragma unroll
-      for (int i = 0; i < WORDS; ++i) row[i] = 0u;
+        for (int v = 0; v < VEC; ++v) load16(vd + (d0 + 32 * i) * kPage * ESZ + 16 * v, &row[i][4 * v]);
+      } else {
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w) row[i][w] = 0u;
+      }
     }
+    int64_t at = -1;  // the source page held
 #pragma unroll
     for (int t = 0; t < kPage; ++t) {
       const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
       const int so = __shfl_sync(0xffffffffu, src_off, t);
       if (sp < 0) continue;  // uniform
-      const int from = ESZ == 1 ? d * kPage + fp8_v_slot(so) : bf16_v_offset(d, so);
-      const uint32_t word = *reinterpret_cast<const uint32_t*>(p.v_cache + sp * p.v_str + (from & ~3));
-      const uint32_t at = from & 3;
-      if constexpr (ESZ == 1) {
-        const int slot = fp8_v_slot(t);  // compile time
-        const uint32_t sel = (0x3210u & ~(0xFu << (4 * (slot & 3)))) | ((4u + at) << (4 * (slot & 3)));
-        row[slot >> 2] = __byte_perm(row[slot >> 2], word, sel);
-      } else {
-        // the halves of the row swap with d: the word index depends on the lane
-        const uint32_t pair_sel = at ? 0x76u : 0x54u;
-        const uint32_t sel = (t & 1) ? (0x0010u | (pair_sel << 8)) : (0x3200u | pair_sel);
-        const bool swap = (d >> 2) & 1;
-        const int w0 = (t >> 1), w1 = (t >> 1) ^ 4;
-        if (!swap) row[w0] = __byte_perm(row[w0], word, sel);
-        else row[w1] = __byte_perm(row[w1], word, sel);
+      if (sp != at) {
+        at = sp;
+        const uint8_t* src = p.v_cache + sp * p.v_str;
+#pragma unroll
+        for (int i = 0; i < RPL; ++i)
+#pragma unroll
+          for (int v = 0; v < VEC; ++v) load16(src + (d0 + 32 * i) * kPage * ESZ + 16 * v, &cur[i][4 * v]);
+      }
+#pragma unroll
+      for (int i = 0; i < RPL; ++i) {
+        if constexpr (ESZ == 1) {
+          const int from = fp8_v_slot(so), to = fp8_v_slot(t);  // `to` at compile time
+          const uint32_t a = (from & 4) ? cur[i][1] : cur[i][0], b2 = (from & 4) ? cur[i][3] : cur[i][2];
+          const uint32_t word = (from & 8) ? b2 : a;
+          const uint32_t sel = (0x3210u & ~(0xFu << (4 * (to & 3)))) | ((4u + (from & 3)) << (4 * (to & 3)));
+          row[i][to >> 2] = __byte_perm(row[i][to >> 2], word, sel);
+        } else {
+          // the halves of a row swap with its dimension, alike in source and destination
+          const bool swap = ((d0 + 32 * i) >> 2) & 1;
+          const int wf = (so >> 1) & 3;
+          const bool upper = (so >= 8) != swap;
+          const uint32_t lo = (wf & 2) ? ((wf & 1) ? cur[i][3] : cur[i][2]) : ((wf & 1) ? cur[i][1] : cur[i][0]);
+          const uint32_t hi = (wf & 2) ? ((wf & 1) ? cur[i][7] : cur[i][6]) : ((wf & 1) ? cur[i][5] : cur[i][4]);
+          const uint32_t word = upper ? hi : lo;
+          const uint32_t pair_sel = (so & 1) ? 0x76u : 0x54u;
+          const uint32_t sel = (t & 1) ? (0x0010u | (pair_sel << 8)) : (0x3200u | pair_sel);
+          if (swap) row[i][(t >> 1) ^ 4] = __byte_perm(row[i][(t >> 1) ^ 4], word, sel);
+          else row[i][t >> 1] = __byte_perm(row[i][t >> 1], word, sel);
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < WORDS; i += 4)
-      *reinterpret_cast<uint4*>(dst + i) = make_uint4(row[i], row[i + 1], row[i + 2], row[i + 3]);
+    for (int i = 0; i < RPL; ++i)
+#pragma unroll
+      for (int v = 0; v < VEC; ++v)
+        *reinterpret_cast<uint4*>(vd + (d0 + 32 * i) * kPage * ESZ + 16 * v) =
+            make_uint4(row[i][4 * v], row[i][4 * v + 1], row[i][4 * v + 2], row[i][4 * v + 3]);
   }
   if constexpr (PT) {
     if (src_page >= 0) {
@@ -335,11 +382,12 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
 constexpr int kMaxCluster = 8;
 constexpr int kKeysMax = 48 * 1024;  // keys a CTA holds in shared memory (192 KiB)
 
-// CTAs per (sequence, KV head): a cluster large enough that a CTA's segment is
-// at most 4,096 candidates.
-int select_cluster(int64_t tokens) {
+// CTAs per (sequence, KV head): clusters as large as the GPU holds at once (a
+// CTA fills an SM; further waves cost a whole selection each), with at least
+// 2,048 candidates per CTA.
+int select_cluster(int64_t tokens, int64_t pairs) {
   int c = 1;
-  while (c < kMaxCluster && tokens > 4096ll * c) c *= 2;
+  while (c < kMaxCluster && 2 * c * pairs <= sm_count() && tokens >= 4096ll * c) c *= 2;
   return c;
 }
 
@@ -419,7 +467,7 @@ extern "C" kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_s
   p.sink = sink;
   p.recent = recent;
   p.dev_status = dev_status;
-  const int C = select_cluster(cap);
+  const int C = select_cluster(cap, static_cast<int64_t>(B) * Hkv);
   const int64_t seg = (cap + C - 1) / C;
   p.seg_cap = seg <= kKeysMax ? static_cast<int>(seg) : 0;
   static int configured_mask = 0;  // devices whose attribute is set

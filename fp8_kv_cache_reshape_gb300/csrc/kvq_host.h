@@ -34,11 +34,14 @@ inline PageStrides page_strides(const void* k_cache, const void* v_cache, int64_
 }
 
 // The split-KV partials of an FP8 decode (per-head scales, no window) without
-// their combine: float32 [B][Hq][per_row][D] outputs and [B][Hq][per_row]
-// base-2 log-sum-exps.
+// their combine: float32 outputs [rows][D] and base-2 log-sum-exps [rows].
+// slots > 0: the wide balanced plan (kvq_plan.cuh), a segment (slot, sequence)
+// of query head h at ((h * (slots + B - 1) + slot + b) * 4 + warp); slots 0:
+// (b * Hq + h) * splits * 4 + i.
 struct DecodePartialPlan {
-  int splits, per_row;
+  int slots, splits;
   size_t rows;
+  int64_t items;
 };
 DecodePartialPlan decode_partial_plan(int B, int Hq, int Hkv, int D, int max_blocks);
 struct DecodePartialArgs {
@@ -47,12 +50,12 @@ struct DecodePartialArgs {
   const float *k_scale, *v_scale;
   const int32_t *block_table, *seq_lens;
   float *o_part, *lse_part;
-  int B, Hq, Hkv, D, max_blocks, splits;
+  int B, Hq, Hkv, D, max_blocks;
   int64_t num_blocks;
   float sm_scale;
   bool e5m2;
   int* dev_status;
 };
-kvq_status_t decode_partials(const DecodePartialArgs& a, cudaStream_t s);
+kvq_status_t decode_partials(const DecodePartialArgs& a, const DecodePartialPlan& plan, cudaStream_t s);
 
 }  // namespace kvq

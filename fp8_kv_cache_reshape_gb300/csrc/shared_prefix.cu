@@ -10,6 +10,7 @@
 
 #include "kvq_device.cuh"
 #include "kvq_host.h"
+#include "kvq_plan.cuh"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
@@ -40,6 +41,10 @@ struct SharedParams {
   int max_units;  // bound of the batch's units
   int kseg;       // slots + max_units
   int* dev_status;
+  // merge table, written by the prefix kernel: [B][g], see RowParts
+  int4* parts;
+  const int32_t* seq_lens;
+  int max_blocks, own_slots;
   // failure-path test hook (kvq_debug_set_stall_ns): > 0 makes the softmax
   // warps wait up to this long on a barrier nothing arrives on
   uint64_t stall_ns;
@@ -48,14 +53,17 @@ struct SharedParams {
 // ------------------------------------------------------------------ plan ---
 // Rows of group i: its sequences x the query heads of a KV head, in tiles of
 // 128; a unit is two tiles (the last of a group maybe one) over the prefix's
-// key tiles.  The cost of a unit is tiles x key tiles.  Per KV head the
-// batch's units are laid end to end and cut into equal slots, one per CTA; a
-// slot's part inside a unit is a segment.
+// key tiles.  The cost of a unit is tiles x key tiles, after kUnitCost for
+// starting it (its queries, its first scores, its output: measured as about
+// twelve tiles' time).  Per KV head the batch's units are laid end to end and,
+// less the first unit's start, which every CTA pays, cut into equal slots, one
+// per CTA; a slot's part inside a unit is a segment.
+constexpr int kUnitCost = 12;
 struct Group {
   int a, nb;        // first sequence, sequences
   int L, tiles, K;  // prefix tokens, row tiles, key tiles
   KVQ_DEVINL int units() const { return (tiles + 1) / 2; }
-  KVQ_DEVINL int cost() const { return tiles * K; }
+  KVQ_DEVINL int cost() const { return tiles * K > 0 ? tiles * K + units() * kUnitCost : 0; }
 };
 KVQ_DEVINL Group group_of(const SharedParams& p, int i, bool report) {
   Group r;
@@ -91,18 +99,20 @@ KVQ_DEVINL void scan_groups(int& cost, int& units, int lane) {
     }
   }
 }
-// The cut of a total cost W (below 2^31, checked on the host; with faulty
-// groups it may wrap, which the clamps keep in bounds) into used slots: the
-// first `rem` slots hold q + 1, the others q.
+// The cut of the stream [kUnitCost, W) of cost (below 2^31, checked on the
+// host; with faulty groups it may wrap, which the clamps keep in bounds) into
+// used slots: the first `rem` slots hold q + 1, the others q.
 struct Cut {
   int q, rem, used;
   KVQ_DEVINL Cut(const SharedParams& p, int W) {
+    W -= kUnitCost;
     used = max(0, min(W, p.slots));
     q = used ? W / used : 0;
     rem = used ? W - q * used : 0;
   }
-  KVQ_DEVINL int start(int slot) const { return slot * q + min(slot, rem); }
+  KVQ_DEVINL int start(int slot) const { return kUnitCost + slot * q + min(slot, rem); }
   KVQ_DEVINL int slot_of(int x) const {
+    x -= kUnitCost;
     const int y = x - rem * (q + 1);
     return min(used - 1, y < 0 ? x / (q + 1) : rem + y / q);
   }
@@ -167,17 +177,20 @@ struct SegWalk {
       if (gi >= base + 32 || gi < base) load(p, gi & ~31, lane, false);
       const int at = gi - base;
       const int tiles = __shfl_sync(0xffffffffu, mine.tiles, at), K = __shfl_sync(0xffffffffu, mine.K, at);
-      if (pos >= gstart + tiles * K) {
-        gstart += tiles * K;
+      const int cost = tiles * K > 0 ? tiles * K + (tiles + 1) / 2 * kUnitCost : 0;
+      if (pos >= gstart + cost) {
+        gstart += cost;
         ubase += (tiles + 1) / 2;
         ++gi;
         continue;
       }
-      const int u = (pos - gstart) / (2 * K);
-      const int ustart = gstart + u * 2 * K;
+      const int u = (pos - gstart) / (2 * K + kUnitCost);
+      const int ustart = gstart + u * (2 * K + kUnitCost) + kUnitCost;  // past its starting cost
       s.once = tiles <= 2;
       s.nq = min(2, tiles - 2 * u);
       const int stop = min(end, ustart + s.nq * K);
+      if (stop <= ustart) break;  // the slot ends before the unit's first tile
+      pos = max(pos, ustart);
       s.k0 = s.nq == 2 ? (pos - ustart + 1) >> 1 : pos - ustart;
       s.k1 = s.nq == 2 ? (stop - ustart + 1) >> 1 : stop - ustart;
       s.a = __shfl_sync(0xffffffffu, mine.a, at);
@@ -192,6 +205,66 @@ struct SegWalk {
     return false;
   }
 };
+
+// Where the partials of row (b, head hi of a KV head's group) are, for every KV
+// head alike.  x: index of the first prefix partial (its segment * UNIT + the
+// row in its unit); y: their count, and 2 << 24 where a segment holds two
+// (alternate key tiles), else 1 << 24; z, w: first segment of the own tokens'
+// partials (slot + b) and their count.
+KVQ_DEVINL void write_parts(const SharedParams& p, int lane) {
+  WideScan ws = {};
+  if (p.own_slots) ws = wide_scan(p.seq_lens, p.B, p.max_blocks, lane, true);
+#pragma unroll 1
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+    int W = 0, gstart = 0, ubase = 0, a = 0, K = 0, tiles = 0;
+    bool found = false;
+#pragma unroll 1
+    for (int base = 0; base < p.G; base += 32) {
+      Group r = {};
+      if (base + lane < p.G) r = group_of(p, base + lane, false);
+      int c = r.cost(), u = r.units();
+      scan_groups(c, u, lane);
+      const uint32_t hit = __ballot_sync(0xffffffffu, base + lane < p.G && b >= r.a && b < r.a + r.nb);
+      if (hit && !found) {
+        found = true;
+        const int at = __ffs(hit) - 1;
+        a = __shfl_sync(0xffffffffu, r.a, at);
+        K = __shfl_sync(0xffffffffu, r.K, at);
+        tiles = __shfl_sync(0xffffffffu, r.tiles, at);
+        gstart += __shfl_sync(0xffffffffu, c - r.cost(), at);
+        ubase += __shfl_sync(0xffffffffu, u - r.units(), at);
+      }
+      const int ct = __shfl_sync(0xffffffffu, c, 31);
+      W += ct;
+      if (!found) {
+        gstart += ct;
+        ubase += __shfl_sync(0xffffffffu, u, 31);
+      }
+    }
+    int4 e = make_int4(0, 1 << 24, 0, 0);
+    const int row = (b - a) * p.g + lane, un = row / UNIT;
+    if (found && K > 0 && lane < p.g && ubase + un < p.max_units) {
+      const int nq = min(2, tiles - 2 * un), c0 = gstart + un * (2 * K + kUnitCost) + kUnitCost;
+      const Cut cut(p, W);
+      const int s0 = cut.slot_of(c0), ns = cut.slot_of(c0 + nq * K - 1) - s0 + 1;
+      e.x = (s0 + ubase + un) * UNIT + row % UNIT;
+      e.y = nq == 1 ? (2 * ns) | (2 << 24) : ns | (1 << 24);
+    }
+    if (p.own_slots) {
+      int start, pages;
+      wide_locate(p.seq_lens, p.B, p.max_blocks, ws, b, lane, start, pages);
+      if (pages > 0) {
+        const int64_t T = ws.total, N = wide_slots(p.own_slots, p.B, ws.total);
+        // the slot of a stream page x: the largest s with s * T / N <= x
+        const int s0 = static_cast<int>(((start + 1ll) * N + T - 1) / T) - 1;
+        const int s1 = static_cast<int>(((start + static_cast<int64_t>(pages)) * N + T - 1) / T) - 1;
+        e.z = s0 + b;
+        e.w = (s1 - s0 + 1) * kPartialWarps;
+      }
+    }
+    if (lane < p.g) p.parts[static_cast<size_t>(b) * p.g + lane] = e;
+  }
+}
 
 // ---------------------------------------------------------------- prefix ---
 // One CTA per (KV head, slot).  Two streams, each with its own 128 query rows,
@@ -388,9 +461,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       const uint64_t v_desc = desc_interleave(sbase + G::OFF_VH, D * 16, 128);
       const uint32_t s_t = tmem + x * TK, o_t = tmem + 2 * TK + x * D;
       SegWalk walk(p, slot, lane, false);
-      uint32_t tile0 = 0, np = 0, nseg = 0, round = 0;  // tiles of earlier segments, P tiles seen, segments, turns
+      uint32_t tile0 = 0, np = 0, nseg = 0, round = 0;  // tiles of earlier segments, P tiles and queries seen, turns
       uint32_t kn = 0, vn = 0;                          // next K and V tile to pass
-      for (Segment s; ok && walk.next(p, s, lane); ++nseg) {
+      for (Segment s; ok && walk.next(p, s, lane);) {
         const int n = s.k1 - s.k0;
         if (elect_one()) {
           const bool pair = s.nq == 2;
@@ -427,7 +500,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             umma_commit(&bars->s_full[x]);
             umma_commit(&bars->k_empty[st]);
           };
-          if (cnt > 0 && wait(&bars->q_full[x], nseg & 1)) qk(0);
+          if (cnt > 0 && wait(&bars->q_full[x], nseg++ & 1)) qk(0);
           // Stream 1 issues a tile's P.V only after stream 0 has issued its own
           // and its next S: left alone the streams fall into step, and the
           // tensor cores idle while both softmaxes run.  Stream 0 is at most a
@@ -477,6 +550,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     // A thread per dimension row: 16 codes -> two 16-byte chunks of f16, the
     // no-swizzle K-major operand (token slots 0-7, then 8-15).  Slots of tokens
     // that are not there are zeroed: P is 0 for them, and 0 x NaN is NaN.
+    if (warp == kSoftWarps) write_parts(p, lane);  // V is not needed before the first softmax is done
     SegWalk walk(p, slot, lane, false);
     const int t = threadIdx.x - kSoftWarps * 32;
     uint32_t it = 0;
@@ -544,9 +618,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const int row = quarter * 32 + lane;     // of the stream's tile
     const uint32_t s_t = tmem + t_lane + x * TK, o_t = tmem + t_lane + 2 * TK + x * D;
-    const float kscale = __fmul_rn(__fmul_rn(p.k_scale[kvh], p.sm_scale), kLog2e);
-    const float vscale = p.v_scale[kvh];
+    const float kscale_raw = __ldg(p.k_scale + kvh), vscale = __ldg(p.v_scale + kvh);  // used after the walk's loads
     SegWalk walk(p, slot, lane, false);
+    const float kscale = __fmul_rn(__fmul_rn(kscale_raw, p.sm_scale), kLog2e);
     uint32_t tile0 = 0, ns = 0, nseg = 0;  // tiles of earlier segments; S tiles seen; O sums taken
     if (!__all_sync(0xffffffffu, stall_wait(&bars->stall, p.stall_ns, abort_flag))) {
       ok = false;
@@ -560,65 +634,68 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       const int r = (pair ? x * TR : 0) + row;  // row of the unit
       const bool live = r < s.rows;
       const bool warp_live = __any_sync(0xffffffffu, live);
+      const size_t idx = (static_cast<size_t>(kvh) * p.kseg + slot + s.unit) * UNIT + x * TR + row;
+      if (cnt == 0) {  // nothing for this stream: no queries, no barriers
+        if (live) p.lse_part[idx] = -INFINITY;
+        tile0 += n;
+        continue;
+      }
       // ---- the query rows as two E4M3 terms, swizzled K-major: D / 8 lanes per
       // row, eight dimensions each ----
       float coef = 0.f;
       {
-        constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;
-        const int sub = lane / LPR, c8 = lane % LPR;
-        // q row of this lane's own row, then of the row that each lane loads a part of
-        const int own = live ? (s.a + (s.row0 + r) / p.g) * p.Hq + kvh * p.g + (s.row0 + r) % p.g : -1;
-        auto load = [&](int i) {
-          const int qr = i < NI ? __shfl_sync(0xffffffffu, own, i * RPI + sub) : -1;
-          uint4 u = make_uint4(0, 0, 0, 0);
-          if (qr >= 0) u = __ldcg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<size_t>(qr) * D) + c8);
-          return u;
-        };
-        // a loop kept small: the first segment pays for fetching its code
-        uint4 ahead[4];
+        // 16-byte pieces c4, c4 + 4, ... of eight dimensions each: lanes of a row
+        // read 64-byte runs, and a lane's pieces convert side by side.  A loop
+        // kept small: the first segment pays for fetching its code.
+        constexpr int NP = D / 32, NI = 4;  // pieces per lane, steps of eight rows
+        const int sub = lane >> 2, c4 = lane & 3;
+        const int own = live ? (s.a + (s.row0 + r) / p.g) * p.Hq + kvh * p.g + (s.row0 + r) % p.g : -1;  // q row
+        uint4 u[NI][NP];  // every load in flight at once
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ahead[i] = load(i);
-#pragma unroll 2
         for (int i = 0; i < NI; ++i) {
-          const int rq = quarter * 32 + i * RPI + sub;  // row of the tile
-          const uint4 u = ahead[0];
-          ahead[0] = ahead[1];
-          ahead[1] = ahead[2];
-          ahead[2] = ahead[3];
-          ahead[3] = load(i + 4);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-          float v[8], mx = 0.f;
+          const int qr = __shfl_sync(0xffffffffu, own, i * 8 + sub);
+          const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + static_cast<size_t>(max(qr, 0)) * D);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-            mx = fmax3(mx, fabsf(v[2 * e]), fabsf(v[2 * e + 1]));
-          }
+          for (int k = 0; k < NP; ++k) u[i][k] = qr >= 0 ? __ldcg(src + c4 + 4 * k) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll 1
+        for (int i = 0; i < NI; ++i) {
+          const int rq = quarter * 32 + i * 8 + sub;  // row of the tile
+          uint32_t mb = 0;  // the largest magnitude, as bf16 bits in either half
 #pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127 : 0;
-          e2 = e2 < -100 ? -100 : e2;
+          for (int k = 0; k < NP; ++k)
+            mb = __vmaxu2(mb, __vmaxu2(__vmaxu2(u[0][k].x & 0x7FFF7FFFu, u[0][k].y & 0x7FFF7FFFu),
+                                       __vmaxu2(u[0][k].z & 0x7FFF7FFFu, u[0][k].w & 0x7FFF7FFFu)));
+          mb = __vmaxu2(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+          mb = __vmaxu2(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+          const uint32_t top = max(mb & 0xFFFFu, mb >> 16);
+          int e2 = top ? static_cast<int>(top >> 7) - 127 : 0;
+          e2 = e2 < -100 ? -100 : (e2 > 127 ? 127 : e2);
           const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+          const float mine = __shfl_sync(0xffffffffu, inv, (lane & 7) * 4);
+          if ((lane >> 3) == i) coef = kscale * mine;
 #pragma unroll
-          for (int h = 0; h < RPI; ++h) {
-            const float ih = __shfl_sync(0xffffffffu, inv, h * LPR);
-            if (lane == i * RPI + h) coef = kscale * ih;
-          }
-          uint32_t hi[2], lo[2];
+          for (int k = 0; k < NP; ++k) {
+            const uint32_t w[4] = {u[0][k].x, u[0][k].y, u[0][k].z, u[0][k].w};
+            uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float a0 = v[4 * e] * sigma, a1 = v[4 * e + 1] * sigma, a2 = v[4 * e + 2] * sigma, a3 = v[4 * e + 3] * sigma;
-            hi[e] = f32x2_to_e4m3x2(a0, a1) | (f32x2_to_e4m3x2(a2, a3) << 16);
-            uint32_t f0, f1;
-            e4m3x4_to_f16x2x2(hi[e], f0, f1);
-            const float2 b0 = __half22float2(*reinterpret_cast<__half2*>(&f0)), b1 = __half22float2(*reinterpret_cast<__half2*>(&f1));
-            lo[e] = f32x2_to_e4m3x2(a0 - b0.x, a1 - b0.y) | (f32x2_to_e4m3x2(a2 - b1.x, a3 - b1.y) << 16);
+            for (int e = 0; e < 2; ++e) {
+              const float a0 = __uint_as_float(w[2 * e] << 16) * sigma, a1 = __uint_as_float(w[2 * e] & 0xFFFF0000u) * sigma;
+              const float a2 = __uint_as_float(w[2 * e + 1] << 16) * sigma, a3 = __uint_as_float(w[2 * e + 1] & 0xFFFF0000u) * sigma;
+              hi[e] = f32x2_to_e4m3x2(a0, a1) | (f32x2_to_e4m3x2(a2, a3) << 16);
+              uint32_t f0, f1;
+              e4m3x4_to_f16x2x2(hi[e], f0, f1);
+              const float2 b0 = __half22float2(*reinterpret_cast<__half2*>(&f0)), b1 = __half22float2(*reinterpret_cast<__half2*>(&f1));
+              lo[e] = f32x2_to_e4m3x2(a0 - b0.x, a1 - b0.y) | (f32x2_to_e4m3x2(a2 - b1.x, a3 - b1.y) << 16);
+            }
+            const int c8 = c4 + 4 * k, c = c8 >> 1;  // piece, 16-byte chunk of the row
+            uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + rq * D + ((D == 128 ? c ^ (rq & 7) : c ^ ((rq >> 1) & 3)) << 4) + (c8 & 1) * 8;
+            *reinterpret_cast<uint2*>(qs) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(qs + G::QT) = make_uint2(lo[0], lo[1]);
+#pragma unroll
+            for (int n = 0; n + 1 < NI; ++n) u[n][k] = u[n + 1][k];
           }
-          const int c = c8 >> 1;  // 16-byte chunk of the row
-          uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + rq * D + ((D == 128 ? c ^ (rq & 7) : c ^ ((rq >> 1) & 3)) << 4) + (c8 & 1) * 8;
-          *reinterpret_cast<uint2*>(qs) = make_uint2(hi[0], hi[1]);
-          *reinterpret_cast<uint2*>(qs + G::QT) = make_uint2(lo[0], lo[1]);
         }
       }
       fence_proxy_async_smem();
@@ -701,8 +778,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
       }
       tile0 += n;
       if (!ok) break;
-      const size_t idx = (static_cast<size_t>(kvh) * p.kseg + slot + s.unit) * UNIT + x * TR + row;
-      if (cnt > 0) {
+      {
         if (!wait_all(&bars->o_full[x], nseg & 1)) break;
         ++nseg;
         tc_fence_after();
@@ -754,9 +830,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
 // --------------------------------------------------------------- combine ---
 struct MergeParams {
   SharedParams sp;
-  const float* o_own;    // [B][Hq][per_row][D]
-  const float* lse_own;  // [B][Hq][per_row]
-  int per_row;
+  const float* o_own;    // the own tokens' partials (DecodePartialPlan)
+  const float* lse_own;
+  int own_splits;
   __nv_bfloat16* out;
 };
 constexpr int kMergeWarps = 4;
@@ -770,52 +846,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
   const SharedParams& p = mp.sp;
   const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  // the row's prefix partials: slots s0 .. s0 + ns - 1, `halves` of each
-  int ns = 0, halves = 1;
-  size_t first = 0;
-  {
-    int W = 0, gstart = 0, ubase = 0, c0 = 0, c1 = 0;
-    bool found = false;
-#pragma unroll 1
-    for (int base = 0; base < p.G; base += 32) {
-      Group r = {};
-      if (base + lane < p.G) r = group_of(p, base + lane, false);
-      int c = r.cost(), u = r.units();
-      scan_groups(c, u, lane);
-      const uint32_t hit = __ballot_sync(0xffffffffu, base + lane < p.G && b >= r.a && b < r.a + r.nb);
-      if (hit && !found) {
-        found = true;
-        const int at = __ffs(hit) - 1;
-        const int a = __shfl_sync(0xffffffffu, r.a, at), K = __shfl_sync(0xffffffffu, r.K, at);
-        const int tiles = __shfl_sync(0xffffffffu, r.tiles, at);
-        gstart += __shfl_sync(0xffffffffu, c - r.cost(), at);
-        ubase += __shfl_sync(0xffffffffu, u - r.units(), at);
-        const int row = (b - a) * p.g + hq % p.g, un = row / UNIT;
-        const int nq = min(2, tiles - 2 * un);
-        c0 = gstart + un * 2 * K;
-        c1 = ubase + un < p.max_units ? c0 + nq * K : c0;
-        halves = nq == 1 ? 2 : 1;
-        first = (static_cast<size_t>(hq / p.g) * p.kseg + ubase + un) * UNIT + row % UNIT;
-      }
-      const int ct = __shfl_sync(0xffffffffu, c, 31);
-      W += ct;
-      if (!found) {
-        gstart += ct;
-        ubase += __shfl_sync(0xffffffffu, u, 31);
-      }
-    }
-    if (c1 > c0) {
-      const Cut cut(p, W);
-      const int s0 = cut.slot_of(c0);
-      ns = cut.slot_of(c1 - 1) - s0 + 1;
-      first += static_cast<size_t>(s0) * UNIT;
-    }
-  }
   grid_dependency_wait();
+  const int4 rp = __ldcg(p.parts + static_cast<size_t>(b) * p.g + hq % p.g);
+  const int np = rp.y & 0xFFFFFF, halves = rp.y >> 24;
+  const size_t first = (static_cast<size_t>(hq / p.g) * p.kseg * UNIT + rp.x);
+  const size_t own_first = p.own_slots ? (static_cast<size_t>(hq) * (p.own_slots + p.B - 1) + rp.z) * kPartialWarps
+                                       : static_cast<size_t>(blockIdx.x) * mp.own_splits * kPartialWarps;
+  const int n_own = p.own_slots ? rp.w : mp.own_splits * kPartialWarps;
   // Partial i of the row: prefix partials first, then the own tokens'.  A warp
   // takes 32 of them at a time: a lane per log-sum-exp, then the outputs of
   // those that carry weight, eight loads in flight.
-  const int np = ns * halves, total = np + mp.per_row;
+  const int total = np + n_own;
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -828,7 +869,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) merge_kernel(const __grid_co
       x = __ldcg(p.lse_part + idx);
       op = p.o_part + idx * D;
     } else if (i < total) {
-      const size_t idx = static_cast<size_t>(blockIdx.x) * mp.per_row + (i - np);
+      const size_t idx = own_first + (i - np);
       x = __ldcg(mp.lse_own + idx);
       op = mp.o_own + idx * D;
     }
@@ -908,7 +949,7 @@ int prefix_slots(int Hkv) {
 int64_t prefix_units(int B, int G, int g) { return static_cast<int64_t>(B) * g / UNIT + G; }
 
 struct Layout {
-  size_t o_part, lse_part, o_own, lse_own, total;  // byte offsets
+  size_t o_part, lse_part, o_own, lse_own, parts, total;  // byte offsets
 };
 Layout layout_of(int B, int G, int Hq, int Hkv, int D, int max_blocks) {
   const size_t rows = static_cast<size_t>(Hkv) * (prefix_slots(Hkv) + prefix_units(B, G, Hq / Hkv)) * UNIT;
@@ -918,7 +959,8 @@ Layout layout_of(int B, int G, int Hq, int Hkv, int D, int max_blocks) {
   l.lse_part = rows * D * 4;
   l.o_own = l.lse_part + rows * 4;
   l.lse_own = l.o_own + own.rows * D * 4;
-  l.total = l.lse_own + (own.rows * 4 + 15) / 16 * 16;
+  l.parts = l.lse_own + (own.rows * 4 + 15) / 16 * 16;
+  l.total = l.parts + static_cast<size_t>(B) * (Hq / Hkv) * sizeof(int4);
   return l;
 }
 
@@ -991,11 +1033,11 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
     return fail(KVQ_ERR_INVALID_ARG, "shared_prefix: misaligned pointer");
   const int64_t g = Hq / Hkv;
   if (static_cast<int64_t>(max_prefix_blocks) * P > 0x7FFFFFFFll - TK || static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFFll - TK ||
-      static_cast<int64_t>(B) * Hq > 0x7FFFFFFFll || B * g > 0x7FFFFFFFll - TR || prefix_units(B, G, g) > 0x3FFFFFFF ||
-      2 * prefix_units(B, G, g) * ((static_cast<int64_t>(max_prefix_blocks) * P + TK - 1) / TK) > 0x7FFFFFFFll)
+      static_cast<int64_t>(B) * Hq > 0x7FFFFFFFll || B * g > 0x7FFFFFFFll - TR || (prefix_units(B, G, g) + prefix_slots(Hkv)) * UNIT > 0x7FFFFFFFll ||
+      prefix_units(B, G, g) * (2 * ((static_cast<int64_t>(max_prefix_blocks) * P + TK - 1) / TK) + kUnitCost) > 0x7FFFFFFFll)
     return fail(KVQ_ERR_UNSUPPORTED, "shared_prefix: problem too large");
   const DecodePartialPlan own = decode_partial_plan(B, Hq, Hkv, D, max_blocks);
-  if (static_cast<int64_t>(B) * Hkv * own.splits > 0x7FFFFFFFll)
+  if (own.items > 0x7FFFFFFFll || static_cast<int64_t>(B) * max_blocks > 0x7FFFFFFFll)
     return fail(KVQ_ERR_UNSUPPORTED, "shared_prefix: problem too large");
   const Layout l = layout_of(B, G, Hq, Hkv, D, max_blocks);
   if (workspace_bytes < l.total)
@@ -1019,12 +1061,11 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
   a.Hkv = Hkv;
   a.D = D;
   a.max_blocks = max_blocks;
-  a.splits = own.splits;
   a.num_blocks = num_blocks;
   a.sm_scale = sm_scale;
   a.e5m2 = e5;
   a.dev_status = dev_status;
-  const kvq_status_t st = decode_partials(a, s);
+  const kvq_status_t st = decode_partials(a, own, s);
   if (st != KVQ_OK) return st;
 
   SharedParams p;
@@ -1055,11 +1096,15 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
   p.kseg = p.slots + p.max_units;
   p.dev_status = dev_status;
   p.stall_ns = stall_ns();
+  p.parts = reinterpret_cast<int4*>(ws + l.parts);
+  p.seq_lens = seq_lens;
+  p.max_blocks = max_blocks;
+  p.own_slots = own.slots;
   MergeParams mp;
   mp.sp = p;
   mp.o_own = a.o_part;
   mp.lse_own = a.lse_part;
-  mp.per_row = own.per_row;
+  mp.own_splits = own.splits;
   mp.out = static_cast<__nv_bfloat16*>(out);
   if (e5) return D == 128 ? launch_shared<128, true>(p, mp, s) : launch_shared<64, true>(p, mp, s);
   return D == 128 ? launch_shared<128, false>(p, mp, s) : launch_shared<64, false>(p, mp, s);

@@ -51,6 +51,8 @@ CASES = {
     "e5m2_d64": ([2049], [0, 5], [16, 0, 1, 300, 31], 4, 3, 64, FP8_E5M2),
     "many_groups": ([(37 * i) % 300 for i in range(40)], list(range(0, 82, 2)), [(11 * i) % 60 for i in range(80)], 1, 2,
                     64, FP8),
+    "batch_256": ([40, 300], [0, 100, 250], [(13 * i) % 70 for i in range(256)], 1, 1, 64, FP8),
+    "batch_300": ([100], [5, 300], [(13 * i) % 40 for i in range(300)], 2, 2, 64, FP8),
     "more_heads_than_sms": ([200], [0, 2], [3, 40], 160, 1, 64, FP8),
 }
 
