@@ -135,8 +135,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current device's current stream as a raw handle; torch.cuda.current_stream()
+# builds a Python object around it, several microseconds a call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

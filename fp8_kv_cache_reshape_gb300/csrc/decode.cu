@@ -1167,15 +1167,12 @@ struct CombinePlan {
   int B, Hq, max_blocks, window, num_slots, kseg;
 };
 template <int NW>
-__global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __restrict__ o_part,
-                                                                 const float* __restrict__ lse_part,
-                                                                 __nv_bfloat16* __restrict__ out,
-                                                                 const CombinePlan cp, int D) {
+KVQ_DEVINL void combine_row(const float* __restrict__ o_part, const float* __restrict__ lse_part,
+                            __nv_bfloat16* __restrict__ out, const CombinePlan& cp, int D, int row, int dim_block) {
   static_assert(NW >= 1 && NW <= 32, "one lane per warp in the final merge");
   __shared__ float m_s[NW];
   __shared__ float den_s[NW];
   __shared__ float acc_s[NW][33];
-  const int row = blockIdx.x;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   size_t first = static_cast<size_t>(row) * cp.S;
   int S = cp.S;
@@ -1200,7 +1197,7 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
   // CTAs would wait beside this call's partial CTAs, the slowest of which
   // set the call's time)
   grid_launch_dependents();
-  const int d = blockIdx.y * 32 + lane;
+  const int d = dim_block * 32 + lane;
   const float* lp = lse_part + first;
   const float* op = o_part + first * D + d;
   float m = -INFINITY, den = 0.f, acc = 0.f;
@@ -1253,22 +1250,36 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
   }
 }
 
+template <int NW>
+__global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __restrict__ o_part,
+                                                                 const float* __restrict__ lse_part,
+                                                                 __nv_bfloat16* __restrict__ out,
+                                                                 const CombinePlan cp, int D) {
+  combine_row<NW>(o_part, lse_part, out, cp, D, blockIdx.x, blockIdx.y);
+}
+
 // weights[b][kvh][j] = decay * weights[b][kvh][j] + sum over the group's query
 // heads of 2^(score - lse), j < L_b, from the scores and log-sum-exps that the
 // partial kernel left.  Bound by memory: per token and KV head 4 gp bytes of
 // scores (in L2 from the partial kernel where they fit) and 8 of weights.
-// Grid (chunks of kWeightTokens tokens, B * Hkv): each CTA merges its heads'
-// log-sum-exps (a warp per head), then one thread per token adds the heads in
+// One grid with the combine, which depends on the same partials: CTAs
+// [0, chunks * B * Hkv) take the weights, a chunk of tokens each, the rest the
+// output rows.  (Two kernels, one after the other, took 77 and 60 us where one
+// takes XX and XX: 8 x 20K and 128K tokens.)  A CTA merges its heads'
+// log-sum-exps (a warp per head), then a thread per token adds the heads in
 // order, so that results do not depend on timing.
-constexpr int kWeightThreads = 256;
-constexpr int kWeightTokens = 1024;
+constexpr int kWeightPer = 4;  // tokens per thread
 struct WeightsParams {
   const float* scores;
   const float* lse_part;
+  const float* o_part;
   float* weights;
+  __nv_bfloat16* out;
   int64_t stride;  // floats between the rows of consecutive (sequence, KV head) pairs
   float decay;
-  int Hkv, g, gp;
+  int Hkv, g, gp, D;
+  int chunks;       // per (sequence, KV head)
+  int weight_ctas;  // chunks * B * Hkv
   CombinePlan cp;
 };
 // The partials of row (b, hq): first index and count.
@@ -1288,48 +1299,88 @@ KVQ_DEVINL void row_partials(const CombinePlan& cp, int b, int hq, int lane, siz
   first = (static_cast<size_t>(hq) * cp.kseg + k0) * kNW;
   S = cnt * kNW;
 }
-__global__ void __launch_bounds__(kWeightThreads) decode_weights_kernel(const WeightsParams p) {
+template <int NW>
+__global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_constant__ WeightsParams p) {
+  if (static_cast<int>(blockIdx.x) >= p.weight_ctas) {
+    const int i = blockIdx.x - p.weight_ctas;
+    combine_row<NW>(p.o_part, p.lse_part, p.out, p.cp, p.D, i / (p.D / 32), i % (p.D / 32));
+    return;
+  }
   __shared__ float lse_s[8];
-  const int pair = blockIdx.y, b = pair / p.Hkv, kvh = pair - b * p.Hkv;
+  const int pair = blockIdx.x / p.chunks, chunk = blockIdx.x - pair * p.chunks;
+  const int b = pair / p.Hkv, kvh = pair - b * p.Hkv;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  grid_dependency_wait();
-  const int L = seq_len_of(p.cp.seq_lens, b, p.cp.max_blocks, nullptr, false);
+  // the lengths and the weights were final before any partial CTA passed its
+  // own wait, and this grid launches only after that; L2-only loads see them
+  const int cap = p.cp.max_blocks * kPage;
+  const int L = min(max(ld_l2only_s32(p.cp.seq_lens + b), 0), cap);
   const int lo = (p.cp.window > 0 && L > p.cp.window) ? L - p.cp.window : 0;
-  const int t0 = blockIdx.x * kWeightTokens;
-  if (t0 >= L) return;
-  if (wid < p.g) {
+  const int t0 = chunk * (NW * 32 * kWeightPer) + threadIdx.x;
+  float* w = p.weights + static_cast<size_t>(pair) * p.stride;
+  const int from = p.decay == 1.f ? lo : 0;  // tokens before it keep their weight
+  float a[kWeightPer];
+#pragma unroll
+  for (int i = 0; i < kWeightPer; ++i) {
+    const int t = t0 + i * NW * 32;
+    a[i] = t >= from && t < L ? __ldcg(w + t) * p.decay : 0.f;
+  }
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const float* sc = p.scores + static_cast<size_t>(pair) * cap * p.gp;
+  // the scores of two heads at a time; the first two are loaded while the
+  // log-sum-exps are merged
+  auto load = [&](int i, int h) {
+    const int t = t0 + i * NW * 32;
+    return t >= lo && t < L ? __ldcg(reinterpret_cast<const float2*>(sc + static_cast<size_t>(t) * p.gp + h))
+                            : make_float2(-INFINITY, -INFINITY);
+  };
+  float2 x[kWeightPer];
+#pragma unroll
+  for (int i = 0; i < kWeightPer; ++i) x[i] = load(i, 0);
+  for (int h = wid; h < p.g; h += NW) {
     size_t first;
     int S;
-    row_partials(p.cp, b, kvh * p.g + wid, lane, first, S);
-    float m = -INFINITY;
-    for (int s = lane; s < S; s += 32) m = fmaxf(m, __ldg(p.lse_part + first + s));
+    row_partials(p.cp, b, kvh * p.g + h, lane, first, S);
+    float m = -INFINITY, sum = 0.f;
+    for (int s0 = 0; s0 < S; s0 += 32 * 8) {  // eight loads in flight
+      float v[8], mn = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    float sum = 0.f;
-    if (m != -INFINITY)
-      for (int s = lane; s < S; s += 32) sum += ex2(__ldg(p.lse_part + first + s) - m);
+      for (int k = 0; k < 8; ++k) {
+        v[k] = s0 + 32 * k + lane < S ? __ldcg(p.lse_part + first + s0 + 32 * k + lane) : -INFINITY;
+        mn = fmaxf(mn, v[k]);
+      }
+      if (mn == -INFINITY) continue;
+      sum *= ex2(m - mn);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum += ex2(v[k] - mn);
+      m = mn;
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    sum = M == -INFINITY ? 0.f : sum * ex2(m - M);  // m = -inf: 0
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     // a head that attends to nothing: every score is -inf, and 2^(-inf - 0) = 0
-    if (lane == 0) lse_s[wid] = sum > 0.f ? m + log2f(sum) : 0.f;
+    if (lane == 0) lse_s[h] = sum > 0.f ? M + log2f(sum) : 0.f;
   }
   __syncthreads();
-  const int t1 = min(t0 + kWeightTokens, L);
-  float* w = p.weights + static_cast<size_t>(pair) * p.stride;
-  const float* sc = p.scores + static_cast<size_t>(pair) * p.cp.max_blocks * kPage * p.gp;
-  for (int t = t0 + threadIdx.x; t < t1; t += kWeightThreads) {
-    if (t < lo && p.decay == 1.f) continue;
-    float a = w[t] * p.decay;
-    if (t >= lo) {
-      float sum = 0.f;
-      for (int h = 0; h < p.g; h += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(sc + static_cast<size_t>(t) * p.gp + h);
-        sum += ex2(x.x - lse_s[h]);
-        if (h + 1 < p.g) sum += ex2(x.y - lse_s[h + 1]);
-      }
-      a += sum;
+  float sum[kWeightPer];
+#pragma unroll
+  for (int i = 0; i < kWeightPer; ++i) sum[i] = 0.f;
+  for (int h = 0; h < p.g; h += 2) {
+    const float l0 = lse_s[h], l1 = h + 1 < p.g ? lse_s[h + 1] : INFINITY;  // no such head: weight 0
+#pragma unroll
+    for (int i = 0; i < kWeightPer; ++i) {
+      sum[i] += ex2(x[i].x - l0);
+      sum[i] += ex2(x[i].y - l1);
+      if (h + 2 < p.g) x[i] = load(i, h + 2);
     }
-    w[t] = a;
+  }
+#pragma unroll
+  for (int i = 0; i < kWeightPer; ++i) {
+    const int t = t0 + i * NW * 32;
+    if (t >= from && t < L) w[t] = a[i] + sum[i];
   }
 }
 
@@ -1446,27 +1497,28 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
   const int parts = (p.num_splits + (p.balanced ? 2 : 0)) * kNW;
   const float* op = p.o_part;
   const float* lp = p.lse_part;
-  if (parts <= 4 * kCombinePer) {
-    cfg.blockDim = dim3(4 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<4>, op, lp, out, cp, D);
-  } else if (parts <= 8 * kCombinePer) {
-    cfg.blockDim = dim3(8 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<8>, op, lp, out, cp, D);
-  } else if (parts <= 16 * kCombinePer) {
-    cfg.blockDim = dim3(16 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<16>, op, lp, out, cp, D);
-  } else {
-    cfg.blockDim = dim3(32 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_combine_kernel<32>, op, lp, out, cp, D);
-  }
-  if constexpr (SC) {
-    if (e != cudaSuccess) return cuda_status(e, "decode combine launch");
-    weights->cp = cp;
-    cfg.gridDim = dim3((p.max_blocks * kPage + kWeightTokens - 1) / kWeightTokens, p.B * p.Hkv);
-    cfg.blockDim = dim3(kWeightThreads);
-    e = cudaLaunchKernelEx(&cfg, decode_weights_kernel, *weights);
-    return cuda_status(e, "decode weights launch");
-  }
+  auto finish = [&](auto warps) {
+    constexpr int NW = decltype(warps)::value;
+    cfg.blockDim = dim3(NW * 32);
+    if constexpr (SC) {
+      weights->cp = cp;
+      const int per_cta = NW * 32 * kWeightPer;
+      weights->chunks = (p.max_blocks * kPage + per_cta - 1) / per_cta;
+      weights->weight_ctas = weights->chunks * p.B * p.Hkv;
+      cfg.gridDim = dim3(weights->weight_ctas + p.B * p.Hq * (D / 32));
+      return cudaLaunchKernelEx(&cfg, decode_weights_kernel<NW>, *weights);
+    } else {
+      return cudaLaunchKernelEx(&cfg, decode_combine_kernel<NW>, op, lp, out, cp, D);
+    }
+  };
+  if (parts <= 4 * kCombinePer)
+    e = finish(std::integral_constant<int, 4>());
+  else if (parts <= 8 * kCombinePer)
+    e = finish(std::integral_constant<int, 8>());
+  else if (parts <= 16 * kCombinePer)
+    e = finish(std::integral_constant<int, 16>());
+  else
+    e = finish(std::integral_constant<int, 32>());
   return cuda_status(e, "decode combine launch");
 }
 
@@ -1618,10 +1670,10 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
                   static_cast<long long>(wts->stride));
     if (!(wts->decay >= 0.f) || !(wts->decay <= 1.f))
       return fail(KVQ_ERR_INVALID_ARG, "paged_decode_weights: decay must be in [0, 1]");
-    if (static_cast<int64_t>(B) * Hkv > 65535)
-      return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: more than 65535 (sequence, KV head) pairs");
-    if (static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFF - kWeightTokens)
-      return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: block table too long");
+    // CTAs of the last kernel: at least 512 tokens, or 32 dimensions of a row, each
+    if ((static_cast<int64_t>(max_blocks) * P / 512 + 1) * B * Hkv + static_cast<int64_t>(B) * Hq * (D / 32) > 0x7FFFFFFF ||
+        static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFF - 32 * 32 * kWeightPer)
+      return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: problem too large");
   }
   int S, pps;
   split_plan(B, Hkv, D, P, max_blocks, window, num_splits, &S, &pps);
@@ -1688,6 +1740,9 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
     wp.Hkv = Hkv;
     wp.g = prm.g;
     wp.gp = prm.gp;
+    wp.D = D;
+    wp.o_part = prm.o_part;
+    wp.out = o;
     if (per_token) {
       if (D == 128)
         return e5 ? launch_decode<128, true, true, true, false, false, 0, true>(prm, o, s, &wp)

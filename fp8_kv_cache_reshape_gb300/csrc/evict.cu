@@ -34,7 +34,7 @@ struct EvictParams {
   int Hkv, max_blocks, max_dst;
   int64_t num_blocks;
   int sink, recent;
-  int seg_cap;  // keys of a CTA's segment held in shared memory (0: read from global memory each pass)
+  int seg_cap;  // weights of a CTA's segment held in shared memory (0: read from global memory each pass)
   int* dev_status;
 };
 
@@ -98,8 +98,7 @@ KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
 // owns the k-th of C equal segments of the candidate positions.  Histograms
 // and counts meet through distributed shared memory.
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ __align__(16) uint32_t dyn[];
-  uint32_t* keys = dyn;  // [seg_cap]
+  extern __shared__ __align__(16) float held_w[];  // [seg_cap] the segment's weights
   __shared__ uint32_t hist[3][kBins];  // one per pass; the leader's collect the cluster's
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ int totals[2];  // this CTA's counts above and at the threshold, read by the cluster
@@ -149,9 +148,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
   if (held) {
 #pragma unroll 4
-    for (int i = tid; i < len; i += kSelThreads) keys[i] = weight_key(wseg[i]);
+    for (int i = tid; i < len; i += kSelThreads) held_w[i] = wseg[i];
   }
-  auto key_at = [&](int i) { return held ? keys[i] : weight_key(wseg[i]); };
+  auto weight_at = [&](int i) { return held ? held_w[i] : wseg[i]; };
   sync_all();  // every histogram is zero
 
   // threshold: the m-th largest key, digit by digit from the top.  The CTAs add
@@ -159,13 +158,12 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   // finds the digit and hands it out.
   uint32_t prefix = 0, mask = 0;
   int need = m;
-  constexpr int kShift[3] = {21, 10, 0};
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
-    const int shift = kShift[pass], bins = pass < 2 ? 2048 : 1024;
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
 #pragma unroll 4
     for (int i = tid; i < len; i += kSelThreads) {
-      const uint32_t k = key_at(i);
+      const uint32_t k = weight_key(weight_at(i));
       if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
     }
     if (rank != 0) {
@@ -209,7 +207,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   int gt = 0, eq = 0;
   for (int j = j0; j < j1; j += 32) {
     const int i = j + lane;
-    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    const uint32_t k = i < j1 ? weight_key(weight_at(i)) : 0u;
     gt += __popc(__ballot_sync(0xffffffffu, i < j1 && k > prefix));
     eq += __popc(__ballot_sync(0xffffffffu, i < j1 && k == prefix));
   }
@@ -235,7 +233,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const uint32_t below = (1u << lane) - 1u;
   for (int j = j0; j < j1; j += 32) {
     const int i = j + lane;
-    const uint32_t k = i < j1 ? key_at(i) : 0u;
+    const float wi = i < j1 ? weight_at(i) : 0.f;
+    const uint32_t k = weight_key(wi);
     const uint32_t g = __ballot_sync(0xffffffffu, i < j1 && k > prefix);
     const uint32_t e = __ballot_sync(0xffffffffu, i < j1 && k == prefix);
     const int eq_rank = eq_before + __popc(e & below);
@@ -243,7 +242,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     if (take) {
       const int pos = cut.s + gt_before + __popc(g & below) + min(eq_rank, need);
       kept[pos] = cut.s + i0 + i;
-      dw[pos] = wseg[i];
+      dw[pos] = wi;
     }
     gt_before += __popc(g);
     eq_before += __popc(e);
@@ -380,7 +379,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
 }
 
 constexpr int kMaxCluster = 8;
-constexpr int kKeysMax = 48 * 1024;  // keys a CTA holds in shared memory (192 KiB)
+constexpr int kKeysMax = 48 * 1024;  // weights a CTA holds in shared memory (192 KiB)
 
 // CTAs per (sequence, KV head): clusters as large as the GPU holds at once (a
 // CTA fills an SM; further waves cost a whole selection each), with at least

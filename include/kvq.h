@@ -450,7 +450,7 @@ kvq_status_t kvq_paged_decode_attention_shared_prefix(const void* q, const void*
  *  Other arguments, caches and the declared rounding as for
  *  kvq_paged_decode_attention (and _per_token); the scores and sums behind
  *  the weights are float32, and heads are added in order (no atomics), so
- *  results are deterministic.  B * Hkv <= 65535.
+ *  results are deterministic.
  */
 size_t kvq_decode_weights_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks, int window,
                                          int num_splits);

@@ -62,7 +62,7 @@ WEIGHTS_SIG = [p] * 9 + [i64, f32] + [i] * 6 + [i64, f32] + [i] * 4 + [p, sz, p,
     ({"w": None}, INVALID), ({"w": FAR + 2}, INVALID), ({"stride": 63}, INVALID), ({"decay": -0.1}, INVALID),
     ({"decay": 1.5}, INVALID), ({"decay": float("nan")}, INVALID), ({"B": 0}, INVALID), ({"window": 0}, INVALID),
     ({"D": 256}, UNSUPPORTED), ({"Hq": 18}, UNSUPPORTED), ({"ks": None}, INVALID), ({"per_token": 1, "dtype": 1}, INVALID),
-    ({"wb": 4096}, INVALID), ({"out": None}, INVALID), ({"B": 40000}, UNSUPPORTED),
+    ({"wb": 4096}, INVALID), ({"out": None}, INVALID), ({"B": 1 << 29}, UNSUPPORTED),
     ({"max_blocks": 134217727, "stride": 1 << 40}, UNSUPPORTED)])
 def test_weights(lib, change, status):
     assert _call(lib, "kvq_paged_decode_attention_weights", WEIGHTS_SIG, WEIGHTS, change) == status
