@@ -1264,8 +1264,7 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
 // scores (in L2 from the partial kernel where they fit) and 8 of weights.
 // One grid with the combine, which depends on the same partials: CTAs
 // [0, chunks * B * Hkv) take the weights, a chunk of tokens each, the rest the
-// output rows.  (Two kernels, one after the other, took 77 and 60 us where one
-// takes XX and XX: 8 x 20K and 128K tokens.)  A CTA merges its heads'
+// output rows.  A CTA merges its heads'
 // log-sum-exps (a warp per head), then a thread per token adds the heads in
 // order, so that results do not depend on timing.
 constexpr int kWeightPer = 4;  // tokens per thread
@@ -1382,6 +1381,12 @@ __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_co
     const int t = t0 + i * NW * 32;
     if (t >= from && t < L) w[t] = a[i] + sum[i];
   }
+  // The scores are spent: their lines leave L2 without being written to memory.
+  __syncthreads();
+  const int begin = chunk * (NW * 32 * kWeightPer), stop = min(begin + NW * 32 * kWeightPer, (L + kPage - 1) / kPage * kPage);
+  const char* spent = reinterpret_cast<const char*>(sc + static_cast<size_t>(begin) * p.gp);
+  for (int o = threadIdx.x * 128; o < (stop - begin) * p.gp * 4; o += NW * 32 * 128)
+    asm volatile("discard.global.L2 [%0], 128;" ::"l"(spent + o) : "memory");
 }
 
 int decode_pages(int P, int max_blocks, int window) {
@@ -1628,7 +1633,7 @@ struct WeightsArgs {
 int even_group(int g) { return g + (g & 1); }
 // Bytes of the base-2 scores [B][Hkv][max_blocks * P][even group].
 size_t score_bytes(int B, int Hq, int Hkv, int max_blocks) {
-  return static_cast<size_t>(B) * Hkv * max_blocks * kPage * even_group(Hq / Hkv) * sizeof(float);
+  return static_cast<size_t>(B) * Hkv * max_blocks * kPage * even_group(Hq / Hkv) * sizeof(float) + 128;  // to align
 }
 
 // Shared by the per-head and the per-token entry points.  per_token: the
@@ -1718,7 +1723,8 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   prm.k_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(k_cache)) : nullptr;
   prm.v_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(v_cache)) : nullptr;
   prm.stall_ns = stall_ns();
-  prm.scores = wts ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + partial_bytes) : nullptr;
+  prm.scores = wts ? reinterpret_cast<float*>(
+                         (reinterpret_cast<uintptr_t>(workspace) + partial_bytes + 127) / 128 * 128) : nullptr;
   prm.gp = even_group(prm.g);
   {
     const int64_t page_b = static_cast<int64_t>(kPage) * D * (fp8 ? 1 : 2);

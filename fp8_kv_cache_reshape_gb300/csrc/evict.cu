@@ -98,7 +98,7 @@ KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
 // owns the k-th of C equal segments of the candidate positions.  Histograms
 // and counts meet through distributed shared memory.
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
-  extern __shared__ __align__(16) float held_w[];  // [seg_cap] the segment's weights
+  extern __shared__ __align__(16) uint32_t held_k[];  // [seg_cap] the segment's keys
   __shared__ uint32_t hist[3][kBins];  // one per pass; the leader's collect the cluster's
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
   __shared__ int totals[2];  // this CTA's counts above and at the threshold, read by the cluster
@@ -117,18 +117,21 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const int N = cut.L - cut.r - cut.s;   // candidates
   const int m = cut.n - cut.r - cut.s;   // chosen among them
   if (rank == 0 && h == 0 && tid == 0) p.dst_lens[b] = cut.n;
+  // the protected ends, and zeros behind the kept tokens: thread i of n
+  auto ends = [&](int i, int n) {
+    for (int j = i; j < cut.s; j += n) {
+      kept[j] = j;
+      dw[j] = w[j];
+    }
+    for (int j = i; j < cut.r; j += n) {
+      const int src = cut.L - cut.r + j, pos = cut.n - cut.r + j;
+      kept[pos] = src;
+      dw[pos] = w[src];
+    }
+    for (int64_t j = cut.n + i; j < p.dst_stride; j += n) dw[j] = 0.f;
+  };
   const int gtid = rank * kSelThreads + tid, gthreads = C * kSelThreads;
-  // the protected ends, and zeros behind the kept tokens
-  for (int i = gtid; i < cut.s; i += gthreads) {
-    kept[i] = i;
-    dw[i] = w[i];
-  }
-  for (int i = gtid; i < cut.r; i += gthreads) {
-    const int src = cut.L - cut.r + i, pos = cut.n - cut.r + i;
-    kept[pos] = src;
-    dw[pos] = w[src];
-  }
-  for (int64_t i = cut.n + gtid; i < p.dst_stride; i += gthreads) dw[i] = 0.f;
+  if (m <= 0 || m == N) ends(gtid, gthreads);
   if (m <= 0) return;  // uniform over the cluster
   if (m == N) {
     for (int i = gtid; i < N; i += gthreads) {
@@ -147,10 +150,10 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const bool held = len <= p.seg_cap;
   for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
   if (held) {
-#pragma unroll 4
-    for (int i = tid; i < len; i += kSelThreads) held_w[i] = wseg[i];
+#pragma unroll 8
+    for (int i = tid; i < len; i += kSelThreads) held_k[i] = weight_key(wseg[i]);
   }
-  auto weight_at = [&](int i) { return held ? held_w[i] : wseg[i]; };
+  auto key_at = [&](int i) { return held ? held_k[i] : weight_key(wseg[i]); };
   sync_all();  // every histogram is zero
 
   // threshold: the m-th largest key, digit by digit from the top.  The CTAs add
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
 #pragma unroll 4
     for (int i = tid; i < len; i += kSelThreads) {
-      const uint32_t k = weight_key(weight_at(i));
+      const uint32_t k = key_at(i);
       if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
     }
     if (rank != 0) {
@@ -175,7 +178,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
       }
     }
     sync_all();
-    if (rank == 0) {
+    if (rank != 0) {  // while the leader looks for the digit
+      if (pass == 0) ends(gtid - kSelThreads, gthreads - kSelThreads);
+    } else {
       // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
       const int hi = kBins - 1 - 2 * tid;
       const uint32_t c0 = hist[pass][hi], c1 = hist[pass][hi - 1];
@@ -201,16 +206,37 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     mask |= static_cast<uint32_t>(bins - 1) << shift;
     need = static_cast<int>(found[pass][1]);
   }
-  // prefix is the threshold; of the keys equal to it the first `need` are taken
-  const int sub = (((len + kSelWarps - 1) / kSelWarps) + 31) / 32 * 32;
+  if (C == 1) ends(tid, kSelThreads);
+  // prefix is the threshold; of the keys equal to it the first `need` are taken.
+  // A warp takes a run of the segment, each lane four neighbours at a time.
+  const int sub = (((len + kSelWarps - 1) / kSelWarps) + 127) / 128 * 128;
   const int j0 = min(len, wid * sub), j1 = min(len, j0 + sub);
+  auto keys4 = [&](int i, uint32_t (&k)[4]) {  // keys i .. i + 3 (0, and not counted, past the run)
+    if (held && i + 4 <= j1) {
+      const uint4 v = *reinterpret_cast<const uint4*>(held_k + i);
+      k[0] = v.x;
+      k[1] = v.y;
+      k[2] = v.z;
+      k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) k[e] = i + e < j1 ? key_at(i + e) : 0u;
+    }
+  };
+  auto is_eq = [&](int i, int e, uint32_t k) { return k == prefix && i + e < j1; };
   int gt = 0, eq = 0;
-  for (int j = j0; j < j1; j += 32) {
-    const int i = j + lane;
-    const uint32_t k = i < j1 ? weight_key(weight_at(i)) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < j1 && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < j1 && k == prefix));
+  for (int j = j0; j < j1; j += 128) {
+    const int i = j + 4 * lane;
+    uint32_t k[4];
+    keys4(i, k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      gt += k[e] > prefix;
+      eq += is_eq(i, e, k[e]);
+    }
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     warp_gt[wid] = gt;
     warp_eq[wid] = eq;
@@ -224,29 +250,47 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   }
   sync_all();
   int gt_before = __shfl_sync(0xffffffffu, gx, wid), eq_before = __shfl_sync(0xffffffffu, ex, wid);
-  for (int k = 0; k < rank; ++k) {
-    const int* other = cluster.map_shared_rank(totals, k);
-    gt_before += other[0];
-    eq_before += other[1];
+  {
+    int og = 0, oe = 0;
+    if (lane < rank) {  // at most 8 CTAs
+      const int* other = cluster.map_shared_rank(totals, lane);
+      og = other[0];
+      oe = other[1];
+    }
+    gt_before += __reduce_add_sync(0xffffffffu, og);
+    eq_before += __reduce_add_sync(0xffffffffu, oe);
+  }
+  for (int j = j0; j < j1; j += 128) {
+    const int i = j + 4 * lane;
+    uint32_t k[4];
+    keys4(i, k);
+    int g = 0, q = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      g += k[e] > prefix;
+      q += is_eq(i, e, k[e]);
+    }
+    int both;  // counts of the lanes before this one: at most 128 each
+    const int before = warp_scan_excl(g | (q << 16), lane, both);
+    int gp = gt_before + (before & 0xFFFF), qp = eq_before + (before >> 16);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool is_g = k[e] > prefix, is_q = is_eq(i, e, k[e]);
+      if (is_g || (is_q && qp < need)) {
+        const int pos = cut.s + gp + min(qp, need);
+        kept[pos] = cut.s + i0 + i + e;
+        // the weight back from its key; what the key does not tell (which zero,
+        // which NaN) is read again
+        const uint32_t u = (k[e] & 0x80000000u) ? (k[e] & 0x7FFFFFFFu) : ~k[e];
+        dw[pos] = (k[e] == 0u || k[e] == 0x80000000u) ? wseg[i + e] : __uint_as_float(u);
+      }
+      gp += is_g;
+      qp += is_q;
+    }
+    gt_before += both & 0xFFFF;
+    eq_before += both >> 16;
   }
   if (C > 1) cluster.sync();  // no CTA leaves while its totals may be read
-  const uint32_t below = (1u << lane) - 1u;
-  for (int j = j0; j < j1; j += 32) {
-    const int i = j + lane;
-    const float wi = i < j1 ? weight_at(i) : 0.f;
-    const uint32_t k = weight_key(wi);
-    const uint32_t g = __ballot_sync(0xffffffffu, i < j1 && k > prefix);
-    const uint32_t e = __ballot_sync(0xffffffffu, i < j1 && k == prefix);
-    const int eq_rank = eq_before + __popc(e & below);
-    const bool take = ((g >> lane) & 1u) || (((e >> lane) & 1u) && eq_rank < need);
-    if (take) {
-      const int pos = cut.s + gt_before + __popc(g & below) + min(eq_rank, need);
-      kept[pos] = cut.s + i0 + i;
-      dw[pos] = wi;
-    }
-    gt_before += __popc(g);
-    eq_before += __popc(e);
-  }
 }
 
 // ------------------------------------------------------------------ move ---
@@ -264,7 +308,7 @@ KVQ_DEVINL void load16(const uint8_t* src, uint32_t* w) {
 // hold the rows (dimensions) of one source page at a time, read whole, and put
 // the kept tokens' bytes into their destination rows with byte permutes.
 // (Reading one 32-bit word per row and token instead touches every sector as
-// often as the page holds kept tokens: 80 against XX us for 8 x 20K to 8K.)
+// often as the page holds kept tokens: 80 against 64 us for 8 x 20K to 8K.)
 template <int D, int ESZ, bool PT>
 __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int ROWB = D * ESZ;
@@ -274,10 +318,13 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
   const int h = blockIdx.y, b = blockIdx.z;
   const int page = blockIdx.x * kMoveWarps + (threadIdx.x >> 5);
   grid_dependency_wait();
-  const int n = p.dst_lens[b];
-  if (page * kPage >= n) return;
+  // the length, the destination page and the tokens' positions in one round trip
+  if (page >= p.max_dst) return;
   const size_t pair = static_cast<size_t>(b) * p.Hkv + h;
-  const int dst_blk = p.dst_table[static_cast<size_t>(b) * p.max_dst + page];
+  const int n = __ldcg(p.dst_lens + b);
+  const int dst_blk = __ldg(p.dst_table + static_cast<size_t>(b) * p.max_dst + page);
+  const int pos = lane < kPage ? __ldcg(p.kept + pair * p.max_dst * kPage + page * kPage + lane) : 0;
+  if (page * kPage >= n) return;
   if (dst_blk < 0 || static_cast<int64_t>(dst_blk) >= p.num_blocks) {
     if (lane == 0) set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
     return;
@@ -286,8 +333,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
   int64_t src_page = -1;
   int src_off = 0;
   if (lane < kPage && page * kPage + lane < n) {
-    const int pos = p.kept[pair * p.max_dst * kPage + page * kPage + lane];
-    const int blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + pos / kPage];
+    const int blk = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + pos / kPage);
     src_off = pos % kPage;
     if (blk < 0 || static_cast<int64_t>(blk) >= p.num_blocks)
       set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
@@ -299,21 +345,42 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
   auto k_off = [](int t, int j) { return ESZ == 1 ? fp8_k_offset(t, j, D) : k_chunk_offset(t, j, ROWB); };
   uint8_t* kd = p.k_cache + dst_page * p.k_str;
   uint8_t* vd = p.v_cache + dst_page * p.v_str;
+  // first tokens of each source page, in order
+  const int64_t prev = __shfl_up_sync(0xffffffffu, src_page, 1);
+  const uint32_t heads = __ballot_sync(0xffffffffu, src_page >= 0 && (lane == 0 || src_page != prev));
+  constexpr int KU = kPage * CH / 32;
+  uint4 kk[KU];
 #pragma unroll
-  for (int u = 0; u < kPage * CH / 32; ++u) {
+  for (int u = 0; u < KU; ++u) {
     const int t = (u * 32 + lane) / CH, j = (u * 32 + lane) % CH;
     const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
     const int so = __shfl_sync(0xffffffffu, src_off, t);
-    if (sp >= 0)
-      *reinterpret_cast<uint4*>(kd + k_off(t, j)) =
-          __ldcg(reinterpret_cast<const uint4*>(p.k_cache + sp * p.k_str + k_off(so, j)));
+    kk[u] = __ldcg(reinterpret_cast<const uint4*>(p.k_cache + max(sp, int64_t(0)) * p.k_str + k_off(so, j)));
   }
+  auto store_k = [&]() {
+#pragma unroll
+    for (int u = 0; u < KU; ++u) {
+      const int t = (u * 32 + lane) / CH, j = (u * 32 + lane) % CH;
+      if ((live >> t) & 1) *reinterpret_cast<uint4*>(kd + k_off(t, j)) = kk[u];
+    }
+  };
+  if constexpr (ESZ == 2) store_k();  // twice the registers: not held beside V
   constexpr int WORDS = kPage * ESZ / 4;  // 32-bit words of a V row
   constexpr int VEC = WORDS / 4;          // 16-byte pieces of a V row
   constexpr int RPL = D / 32 < 4 / VEC ? D / 32 : 4 / VEC;  // rows per lane at a time
 #pragma unroll 1
   for (int d0 = lane; d0 < D; d0 += 32 * RPL) {
-    uint32_t row[RPL][WORDS], cur[RPL][WORDS];
+    uint32_t row[RPL][WORDS], cur[RPL][WORDS], nxt[RPL][WORDS];
+    auto load_page = [&](uint32_t from) {  // of the first token in `from`, into nxt
+      if (!from) return;  // uniform
+      const uint8_t* src = p.v_cache + __shfl_sync(0xffffffffu, src_page, __ffs(from) - 1) * p.v_str;
+#pragma unroll
+      for (int i = 0; i < RPL; ++i)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) load16(src + (d0 + 32 * i) * kPage * ESZ + 16 * v, &nxt[i][4 * v]);
+    };
+    load_page(heads);
+    if (ESZ == 1 && d0 == lane) store_k();
 #pragma unroll
     for (int i = 0; i < RPL; ++i) {
       if (live != 0xFFFFu) {  // slots of other tokens stay
@@ -324,19 +391,16 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
         for (int w = 0; w < WORDS; ++w) row[i][w] = 0u;
       }
     }
-    int64_t at = -1;  // the source page held
 #pragma unroll
     for (int t = 0; t < kPage; ++t) {
-      const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
       const int so = __shfl_sync(0xffffffffu, src_off, t);
-      if (sp < 0) continue;  // uniform
-      if (sp != at) {
-        at = sp;
-        const uint8_t* src = p.v_cache + sp * p.v_str;
+      if (!((live >> t) & 1)) continue;  // uniform
+      if ((heads >> t) & 1) {  // the next page's rows are under way while this one's are used
 #pragma unroll
         for (int i = 0; i < RPL; ++i)
 #pragma unroll
-          for (int v = 0; v < VEC; ++v) load16(src + (d0 + 32 * i) * kPage * ESZ + 16 * v, &cur[i][4 * v]);
+          for (int w = 0; w < WORDS; ++w) cur[i][w] = nxt[i][w];
+        load_page(heads & ~((2u << t) - 1u));
       }
 #pragma unroll
       for (int i = 0; i < RPL; ++i) {

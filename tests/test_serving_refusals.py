@@ -96,4 +96,4 @@ def test_workspace_sizes(lib):
     base = lib.kvq_decode_workspace_size
     base.restype, base.argtypes = sz, [i] * 8
     a, b = base(4, 6, 2, 128, 16, 4, -1, 0), lib.kvq_decode_weights_workspace_size(4, 6, 2, 128, 16, 4, -1, 0)
-    assert b - a == 4 * 2 * 4 * 16 * 4 * 4  # float32 scores of four heads (three rounded up)
+    assert b - a == 4 * 2 * 4 * 16 * 4 * 4 + 128  # float32 scores of four heads (three rounded up), and room to align them
