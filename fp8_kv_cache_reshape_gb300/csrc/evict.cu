@@ -341,6 +341,13 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
       src_page = static_cast<int64_t>(blk) * p.Hkv + h;
   }
   const uint32_t live = __ballot_sync(0xffffffffu, src_page >= 0);
+  // this lane's token in its pages: the V row slot it is read from, and the pages
+  const int from_slot = ESZ == 1 ? fp8_v_slot(src_off) : src_off;
+  const uint8_t* k_src = p.k_cache + max(src_page, int64_t(0)) * p.k_str;
+  const uint8_t* v_src = p.v_cache + max(src_page, int64_t(0)) * p.v_str;
+  auto shfl_ptr = [](const uint8_t* x, int t) {
+    return reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(x), t));
+  };
   const int64_t dst_page = static_cast<int64_t>(dst_blk) * p.Hkv + h;
   auto k_off = [](int t, int j) { return ESZ == 1 ? fp8_k_offset(t, j, D) : k_chunk_offset(t, j, ROWB); };
   uint8_t* kd = p.k_cache + dst_page * p.k_str;
@@ -353,9 +360,8 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
 #pragma unroll
   for (int u = 0; u < KU; ++u) {
     const int t = (u * 32 + lane) / CH, j = (u * 32 + lane) % CH;
-    const int64_t sp = __shfl_sync(0xffffffffu, src_page, t);
     const int so = __shfl_sync(0xffffffffu, src_off, t);
-    kk[u] = __ldcg(reinterpret_cast<const uint4*>(p.k_cache + max(sp, int64_t(0)) * p.k_str + k_off(so, j)));
+    kk[u] = __ldcg(reinterpret_cast<const uint4*>(shfl_ptr(k_src, t) + k_off(so, j)));
   }
   auto store_k = [&]() {
 #pragma unroll
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
     uint32_t row[RPL][WORDS], cur[RPL][WORDS], nxt[RPL][WORDS];
     auto load_page = [&](uint32_t from) {  // of the first token in `from`, into nxt
       if (!from) return;  // uniform
-      const uint8_t* src = p.v_cache + __shfl_sync(0xffffffffu, src_page, __ffs(from) - 1) * p.v_str;
+      const uint8_t* src = shfl_ptr(v_src, __ffs(from) - 1);
 #pragma unroll
       for (int i = 0; i < RPL; ++i)
 #pragma unroll
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
     }
 #pragma unroll
     for (int t = 0; t < kPage; ++t) {
-      const int so = __shfl_sync(0xffffffffu, src_off, t);
+      const int so = __shfl_sync(0xffffffffu, from_slot, t);
       if (!((live >> t) & 1)) continue;  // uniform
       if ((heads >> t) & 1) {  // the next page's rows are under way while this one's are used
 #pragma unroll
@@ -405,7 +411,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
 #pragma unroll
       for (int i = 0; i < RPL; ++i) {
         if constexpr (ESZ == 1) {
-          const int from = fp8_v_slot(so), to = fp8_v_slot(t);  // `to` at compile time
+          const int from = so, to = fp8_v_slot(t);  // `to` at compile time
           const uint32_t a = (from & 4) ? cur[i][1] : cur[i][0], b2 = (from & 4) ? cur[i][3] : cur[i][2];
           const uint32_t word = (from & 8) ? b2 : a;
           const uint32_t sel = (0x3210u & ~(0xFu << (4 * (to & 3)))) | ((4u + (from & 3)) << (4 * (to & 3)));
@@ -434,7 +440,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
   }
   if constexpr (PT) {
     if (src_page >= 0) {
-      const float* st = reinterpret_cast<const float*>(p.v_cache + src_page * p.v_str + PAGE_BYTES);
+      const float* st = reinterpret_cast<const float*>(v_src + PAGE_BYTES);
       float* dt = reinterpret_cast<float*>(vd + PAGE_BYTES);
       dt[lane] = st[src_off];
       dt[kPage + lane] = st[kPage + src_off];
