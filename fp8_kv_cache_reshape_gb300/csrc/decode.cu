@@ -95,6 +95,7 @@ struct DecodeParams {
   // base-2 scores, [B][Hkv][max_blocks * P][gp], gp = g rounded up to even
   float* scores;
   int gp;
+  int late;  // wait for the preceding grid at the end (BAL 2)
   // failure-path test hook (kvq_debug_set_stall_ns): > 0 makes consumer warp
   // 0 wait up to this long on a barrier nothing arrives on before its first
   // stage, which fails like a stuck pipeline wait
@@ -506,7 +507,10 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
   if (warp == NW - 1 && !p.direct && blockIdx.x < p.num_items) {
     prefetch_first_pages<D, FP8, PT, BAL>(p, lane, PPS * NW);
   }
-  grid_dependency_wait();
+  // p.late (BAL 2): this grid runs beside the one that precedes it, which it
+  // does not depend on and which started after all that it does depend on had
+  // completed; it waits for it only before it ends.
+  if (BAL != 2 || !p.late) grid_dependency_wait();
   if (!p.direct) grid_launch_dependents();
 
   if (warp == NW) {
@@ -1149,6 +1153,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
       }
     }
   }
+  if (BAL == 2 && p.late) grid_dependency_wait();
 }
 
 // out[row][d] = sum_s 2^(lse_s - M) o_s[d] / sum_s 2^(lse_s - M) over the
@@ -1579,6 +1584,7 @@ kvq_status_t kvq::decode_partials(const DecodePartialArgs& a, const DecodePartia
   prm.num_items = static_cast<int>(plan.items);
   prm.num_slots = plan.slots;
   prm.kseg = plan.slots + a.B - 1;
+  prm.late = a.late ? 1 : 0;
   prm.dev_status = a.dev_status;
   prm.stall_ns = stall_ns();
   const int64_t page_b = static_cast<int64_t>(kPage) * a.D;
@@ -1722,6 +1728,7 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
   prm.slot_new = app ? app->slot_new : nullptr;
   prm.k_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(k_cache)) : nullptr;
   prm.v_cache_w = app ? static_cast<uint8_t*>(const_cast<void*>(v_cache)) : nullptr;
+  prm.late = 0;
   prm.stall_ns = stall_ns();
   prm.scores = wts ? reinterpret_cast<float*>(
                          (reinterpret_cast<uintptr_t>(workspace) + partial_bytes + 127) / 128 * 128) : nullptr;

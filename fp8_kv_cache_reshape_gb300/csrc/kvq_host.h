@@ -54,6 +54,7 @@ struct DecodePartialArgs {
   int64_t num_blocks;
   float sm_scale;
   bool e5m2;
+  bool late;  // launched beside the preceding kernel (programmatic), which it only outlasts (wide plan)
   int* dev_status;
 };
 kvq_status_t decode_partials(const DecodePartialArgs& a, const DecodePartialPlan& plan, cudaStream_t s);

@@ -41,6 +41,7 @@ struct SharedParams {
   int max_units;  // bound of the batch's units
   int kseg;       // slots + max_units
   int* dev_status;
+  int first;  // launched before the own tokens' grid
   // merge table, written by the prefix kernel: [B][g], see RowParts
   int4* parts;
   const int32_t* seq_lens;
@@ -380,6 +381,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;  // S0 | S1 (128 columns each) | O0 | O1 (D each)
+  // Whichever of this grid and the own tokens' is launched first waits for what
+  // precedes the call; the other starts after that, runs beside it and waits
+  // for it only before it ends.
+  if (p.first) grid_dependency_wait();
   grid_launch_dependents();
 
   // a wait of the whole warp; false (for good) after a timeout anywhere
@@ -822,9 +827,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
-  // the decode partials' grid precedes this one and may still run: this grid
-  // must not complete before it, so that the combine sees both
-  grid_dependency_wait();
+  if (!p.first) grid_dependency_wait();
 }
 
 // --------------------------------------------------------------- combine ---
@@ -965,7 +968,8 @@ Layout layout_of(int B, int G, int Hq, int Hkv, int D, int max_blocks) {
 }
 
 template <int D, bool E5>
-kvq_status_t launch_shared(const SharedParams& p, const MergeParams& mp, cudaStream_t s) {
+kvq_status_t launch_shared(const SharedParams& p, const MergeParams& mp, const DecodePartialArgs& a,
+                           const DecodePartialPlan& own, cudaStream_t s) {
   constexpr int smem = Geo<D>::SMEM;
   auto kern = prefix_kernel<D, E5>;
   static int configured_mask = 0;  // devices whose attribute is set
@@ -986,7 +990,12 @@ kvq_status_t launch_shared(const SharedParams& p, const MergeParams& mp, cudaStr
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  cudaError_t e = cudaSuccess;
+  if (p.first) e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return cuda_status(e, "shared_prefix launch");
+  const kvq_status_t st = decode_partials(a, own, s);
+  if (st != KVQ_OK) return st;
+  if (!p.first) e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return cuda_status(e, "shared_prefix launch");
   cfg.gridDim = dim3(p.B * p.Hq);
   cfg.blockDim = dim3(kMergeWarps * 32);
@@ -1065,9 +1074,6 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
   a.sm_scale = sm_scale;
   a.e5m2 = e5;
   a.dev_status = dev_status;
-  const kvq_status_t st = decode_partials(a, own, s);
-  if (st != KVQ_OK) return st;
-
   SharedParams p;
   p.q = q;
   p.k_cache = a.k_cache;
@@ -1100,12 +1106,21 @@ extern "C" kvq_status_t kvq_paged_decode_attention_shared_prefix(
   p.seq_lens = seq_lens;
   p.max_blocks = max_blocks;
   p.own_slots = own.slots;
+  // A long prefix goes first: its CTAs end microseconds apart, and the own
+  // tokens' fill what they leave (128 sequences after 32K: 118 us, 125 the other
+  // way).  A short one second: the own tokens' grid, small enough to be placed
+  // while the preceding kernel still runs, starts faster (32 after 8K: 33 us
+  // against 35).  By the tiles per CTA; more sequences than the wide plan takes
+  // have no partials that wait late.
+  const int64_t tiles = (B * g + TR - 1) / TR * ((static_cast<int64_t>(max_prefix_blocks) * P + TK - 1) / TK);
+  p.first = own.slots > 0 && tiles >= 8ll * p.slots;
+  a.late = p.first != 0;
   MergeParams mp;
   mp.sp = p;
   mp.o_own = a.o_part;
   mp.lse_own = a.lse_part;
   mp.own_splits = own.splits;
   mp.out = static_cast<__nv_bfloat16*>(out);
-  if (e5) return D == 128 ? launch_shared<128, true>(p, mp, s) : launch_shared<64, true>(p, mp, s);
-  return D == 128 ? launch_shared<128, false>(p, mp, s) : launch_shared<64, false>(p, mp, s);
+  if (e5) return D == 128 ? launch_shared<128, true>(p, mp, a, own, s) : launch_shared<64, true>(p, mp, a, own, s);
+  return D == 128 ? launch_shared<128, false>(p, mp, a, own, s) : launch_shared<64, false>(p, mp, a, own, s);
 }
