@@ -402,7 +402,7 @@ def kvq_prefill_attention_per_token(q8, q_scale, k_cache, v_cache, block_table, 
 
 
 def _check_tensor(t, dtype, shape, name):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 

@@ -108,7 +108,7 @@ struct Cut {
   KVQ_DEVINL Cut(const SharedParams& p, int W) {
     W -= kUnitCost;
     used = max(0, min(W, p.slots));
-    q = used ? W / used : 0;
+    q = used ? static_cast<unsigned>(W) / static_cast<unsigned>(used) : 0;
     rem = used ? W - q * used : 0;
   }
   KVQ_DEVINL int start(int slot) const { return kUnitCost + slot * q + min(slot, rem); }
@@ -175,7 +175,7 @@ struct SegWalk {
   KVQ_DEVINL bool next(const SharedParams& p, Segment& s, int lane) {
 #pragma unroll 1
     while (pos < end && gi < p.G) {
-      if (gi >= base + 32 || gi < base) load(p, gi & ~31, lane, false);
+      if (__builtin_expect(gi >= base + 32 || gi < base, 0)) load(p, gi & ~31, lane, false);
       const int at = gi - base;
       const int tiles = __shfl_sync(0xffffffffu, mine.tiles, at), K = __shfl_sync(0xffffffffu, mine.K, at);
       const int cost = tiles * K > 0 ? tiles * K + (tiles + 1) / 2 * kUnitCost : 0;
@@ -185,7 +185,8 @@ struct SegWalk {
         ++gi;
         continue;
       }
-      const int u = (pos - gstart) / (2 * K + kUnitCost);
+      int u = 0;
+      if (pos - gstart >= 2 * K + kUnitCost) u = static_cast<unsigned>(pos - gstart) / static_cast<unsigned>(2 * K + kUnitCost);
       const int ustart = gstart + u * (2 * K + kUnitCost) + kUnitCost;  // past its starting cost
       s.once = tiles <= 2;
       s.nq = min(2, tiles - 2 * u);
