@@ -406,6 +406,45 @@ def _check_tensor(t, dtype, shape, name):
         raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
 
 
+def _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks):
+    """The caches' bytes against what the head dim and format say (a wrong one
+    would read and write past a page); returns the block count."""
+    kpage = PAGE * D * (2 if dt == KVQ_DTYPE_BF16 else 1)
+    vpage = kpage + (SCALE_TAIL_BYTES if per_token else 0)
+    nb = k_cache.shape[0]
+    if v_cache.data_ptr() == k_cache.data_ptr() + kpage:
+        ok = k_cache.nbytes == nb * Hkv * (kpage + vpage)
+    else:
+        ok = k_cache.nbytes == nb * Hkv * kpage and v_cache.nbytes == nb * Hkv * vpage
+    if not ok:
+        raise ValueError("k_cache and v_cache must be alloc_kv_cache() tensors of this head dim and cache dtype")
+    if num_blocks is None:
+        return nb
+    if num_blocks > nb:
+        raise ValueError(f"num_blocks {num_blocks} > the caches' {nb}")
+    return num_blocks
+
+
+def _check_scales(k_scale, v_scale, Hkv):
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _check_tensor(t, torch.float32, (Hkv,), name)
+
+
+def _check_device(t):
+    if t.is_cuda and t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one "
+                         f"(cuda:{torch.cuda.current_device()})")
+
+
+def _workspace(need, like, stream):
+    """A workspace for one call; kept from reuse until the call's stream is past it."""
+    w = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    if stream is not None:
+        w.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
+    return w
+
+
 def kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix_blocks, max_blocks):
     return lib.kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, PAGE, max_prefix_blocks, max_blocks)
 
@@ -428,14 +467,16 @@ def kvq_paged_decode_attention_shared_prefix(q, k_cache, v_cache, k_scale, v_sca
     _check_tensor(block_table, torch.int32, (B, block_table.shape[1]), "block_table")
     _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
     max_blocks = block_table.shape[1]
+    dt = _dtype_code(cache_dtype)
+    _check_scales(k_scale, v_scale, Hkv)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, False, num_blocks)
+    _check_device(q)
     if workspace is None:
-        need = kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix, max_blocks)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix, max_blocks), q, stream)
     _check(lib.kvq_paged_decode_attention_shared_prefix(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table), _ptr(prefix_lens),
         _ptr(group_starts), _ptr(block_table), _ptr(seq_lens), _ptr(out), B, G, Hq, Hkv, D, PAGE, max_prefix,
-        max_blocks, k_cache.shape[0] if num_blocks is None else num_blocks,
-        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), _dtype_code(cache_dtype), _ptr(workspace),
+        max_blocks, num_blocks, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), dt, _ptr(workspace),
         workspace.numel(), _ptr(dev_status), _stream(stream)), "kvq_paged_decode_attention_shared_prefix")
     return out
 
@@ -460,14 +501,16 @@ def kvq_paged_decode_attention_weights(q, k_cache, v_cache, k_scale, v_scale, bl
     _check_tensor(block_table, torch.int32, (B, max_blocks), "block_table")
     _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
     _check_tensor(weights, torch.float32, (B, Hkv, weights.shape[-1]), "weights")
+    dt = _dtype_code(cache_dtype)
+    _check_scales(k_scale, v_scale, Hkv)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
+    _check_device(q)
     if workspace is None:
-        need = kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits), q, stream)
     _check(lib.kvq_paged_decode_attention_weights(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
-        _ptr(out), _ptr(weights), weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks,
-        k_cache.shape[0] if num_blocks is None else num_blocks,
-        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, _dtype_code(cache_dtype),
+        _ptr(out), _ptr(weights), weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, dt,
         1 if per_token else 0, num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)),
         "kvq_paged_decode_attention_weights")
     return out
@@ -492,10 +535,11 @@ def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens
     _check_tensor(dst_weights, torch.float32, (B, Hkv, dst_weights.shape[-1]), "dst_weights")
     _check_tensor(dst_seq_lens, torch.int32, (B,), "dst_seq_lens")
     _check_tensor(kept, torch.int32, (B, Hkv, max_dst * PAGE), "kept")
+    dt = _dtype_code(cache_dtype)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, head_dim, dt, per_token, num_blocks)
+    _check_device(weights)
     _check(lib.kvq_evict_tokens(
         _ptr(weights), weights.shape[-1], _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
         _ptr(keep_lens), _ptr(dst_block_table), _ptr(dst_weights), dst_weights.shape[-1], _ptr(dst_seq_lens),
-        _ptr(kept), B, Hkv, head_dim, PAGE, max_blocks, max_dst,
-        k_cache.shape[0] if num_blocks is None else num_blocks, sink, recent, _dtype_code(cache_dtype),
-        1 if per_token else 0, _ptr(dev_status), _stream(stream)), "kvq_evict_tokens")
+        _ptr(kept), B, Hkv, head_dim, PAGE, max_blocks, max_dst, num_blocks, sink, recent, dt, 1 if per_token else 0, _ptr(dev_status), _stream(stream)), "kvq_evict_tokens")
     return dst_seq_lens

@@ -133,10 +133,10 @@ int kvq_version(void);
  * pipeline waits (the pages have no counterpart; it exists so that the path
  * a stuck wait takes can be run without faulting or hanging a GPU).
  *
- * With ns > 0, every decode-partial and prefill kernel launched afterwards
- * (on any thread) makes one of its waits -- consumer warp 0 of each decode
- * CTA before its first stage; the softmax warps of each prefill CTA before
- * the first key tile -- a wait of at most ns nanoseconds on a barrier that
+ * With ns > 0, every decode-partial, prefill and shared-prefix kernel launched
+ * afterwards (on any thread) makes one of its waits -- consumer warp 0 of each
+ * decode CTA before its first stage; the softmax warps of each prefill or
+ * shared-prefix CTA before the first key tile -- a wait of at most ns nanoseconds on a barrier that
  * nothing arrives on.  It fails like any pipeline wait that exceeded its
  * bound: the kernel ORs KVQ_DEV_TIMEOUT into *dev_status, abandons its work
  * (the outputs are then meaningless), lets every bulk copy it issued land,
@@ -413,8 +413,19 @@ kvq_status_t kvq_paged_decode_attention_per_token(const void* q, const void* k_c
  *  workspace     kvq_shared_prefix_workspace_size(...) bytes, 16-byte aligned;
  *                contents on entry are ignored; calls sharing it must not
  *                overlap.
- *  The work split is a function of the lengths and groups alone: results are
- *  deterministic.
+ *  Three kernels: the prefix on tensor cores (tcgen05), the own tokens on the
+ *  split-KV decode's, and their merge by log-sum-exps in FP32.  The first two
+ *  run beside each other.  The work split is a function of the lengths and
+ *  groups alone: results are deterministic.
+ *  Declared rounding: own tokens as for kvq_paged_decode_attention.  Prefix --
+ *  per query head, sigma = 2^(7 - floor(log2 max_d |q_d|)) and the query enters
+ *  as the sum of two E4M3 terms, hi = e4m3(q * sigma) and lo = e4m3(q * sigma -
+ *  hi) (exact but for elements under 2^-9 of the head's maximum, which are off
+ *  by at most 2^-17 of it); scores are FP32 sums of exact products with the
+ *  cache's codes; probabilities 2^(s2 - M + 8), M at most 7 below the running
+ *  maximum of the base-2 scores, are rounded to float16 (11 significant bits)
+ *  and multiplied with the codes converted to float16 (exact), FP32 sums; the
+ *  row sum adds them unrounded.  The output is rounded to bf16 once, at the end.
  */
 size_t kvq_shared_prefix_workspace_size(int B, int G, int Hq, int Hkv, int D, int P, int max_prefix_blocks,
                                         int max_blocks);
@@ -446,7 +457,8 @@ kvq_status_t kvq_paged_decode_attention_shared_prefix(const void* q, const void*
  *                  (k_scale and v_scale are ignored and may be NULL).
  *  workspace       kvq_decode_weights_workspace_size(...) bytes: the decode's
  *                  partials and float32 scores [B][Hkv][max_blocks * P][Hq /
- *                  Hkv rounded up to even].
+ *                  Hkv rounded up to even] (in L2 between the two kernels of a
+ *                  call, where they fit, and discarded from it).
  *  Other arguments, caches and the declared rounding as for
  *  kvq_paged_decode_attention (and _per_token); the scores and sums behind
  *  the weights are float32, and heads are added in order (no atomics), so

@@ -142,3 +142,43 @@ def test_stuck_wait_ends_the_shared_prefix_call():
     ref, mag = serving.shared_prefix_decode(qv, pool.k, pool.v, pool.k_scale, pool.v_scale, pre, [700], [0, 4], mine,
                                             [20, 5, 0, 33], 1 / np.sqrt(128), FP8)
     assert_output(out, ref, mag)
+
+
+def test_pages_beyond_32_bit_offsets():
+    """Pages at the end of caches of 5 GB each: byte offsets beyond 2^32."""
+    k = _k()
+    dim, L, own, keep = 128, 300, [20, 33], 90
+    pool = Pool(60, 1, dim, FP8, 43)
+    table, mine, dst = pool.table([L]), pool.table(own), pool.table([keep], fill=False)
+    q, qv = pool.query(2, 4)
+    weights = pool.rng.exponential(size=(1, 1, table.shape[1] * P)).astype(np.float32)
+    blocks = 5 * (1 << 30) // (P * dim)
+    small_k, small_v = pool.device()
+    kd, vd = (torch.empty(blocks, 1, P * dim, dtype=torch.uint8, device="cuda") for _ in range(2))
+    kd[-60:], vd[-60:] = small_k, small_v
+    up = blocks - 60
+    scales, st = pool.device_scales(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    k.kvq_paged_decode_attention_shared_prefix(q, kd, vd, *scales, i32(table + up), i32([L]), i32([0, 2]), i32(mine + up), i32(own),
+                                               out, dev_status=st)
+    one = torch.empty_like(q[:1])
+    w = torch.zeros(1, 1, table.shape[1] * P, device="cuda")
+    k.kvq_paged_decode_attention_weights(q[:1].contiguous(), kd, vd, *scales, i32(table + up), i32([L]), one, w, dev_status=st)
+    dw, dl = torch.zeros(1, 1, dst.shape[1] * P, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(1, 1, dst.shape[1] * P, dtype=torch.int32, device="cuda")
+    k.kvq_evict_tokens(torch.from_numpy(weights).cuda(), kd, vd, i32(table + up), i32([L]), i32([keep]), i32(dst + up), dw, dl,
+                       kept, head_dim=dim, sink=2, recent=8, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, mag = serving.shared_prefix_decode(qv, pool.k, pool.v, pool.k_scale, pool.v_scale, table, [L], [0, 2], mine, own,
+                                            1 / np.sqrt(dim), FP8)
+    assert_output(out, ref, mag)
+    ref, mag, acc, _ = serving.decode_weights(qv[:1], pool.k, pool.v, pool.k_scale, pool.v_scale, table, [L],
+                                              np.zeros(weights.shape), 1.0, 1 / np.sqrt(dim), -1, FP8)
+    assert_output(one, ref, mag)
+    assert np.allclose(w.cpu().numpy(), acc, rtol=1e-4, atol=1e-9)
+    ek, ev, _, rw, _, rk = serving.evict(weights, pool.k, pool.v, table, [L], [keep], dst, np.zeros(dw.shape, np.float32),
+                                         np.zeros(kept.shape, np.int32), 2, 8)
+    pk, pv = layout.to_device_format(ek, ev)
+    assert np.array_equal(kept.cpu().numpy(), rk) and np.array_equal(dw.cpu().numpy(), rw)
+    assert np.array_equal(kd[-60:].cpu().numpy(), pk) and np.array_equal(vd[-60:].cpu().numpy(), pv)
