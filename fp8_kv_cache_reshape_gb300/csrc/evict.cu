@@ -149,12 +149,16 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   const float* wseg = w + cut.s + i0;
   const bool held = len <= p.seg_cap;
   for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
-  if (held) {
+  __syncthreads();
+  // the keys, and their first digit's histogram on the way
 #pragma unroll 8
-    for (int i = tid; i < len; i += kSelThreads) held_k[i] = weight_key(wseg[i]);
+  for (int i = tid; i < len; i += kSelThreads) {
+    const uint32_t k = weight_key(wseg[i]);
+    if (held) held_k[i] = k;
+    atomicAdd(&hist[0][k >> 21], 1u);
   }
   auto key_at = [&](int i) { return held ? held_k[i] : weight_key(wseg[i]); };
-  sync_all();  // every histogram is zero
+  sync_all();  // every CTA's histograms hold their own counts or zeros
 
   // threshold: the m-th largest key, digit by digit from the top.  The CTAs add
   // their counts to the leader's histogram (bins that hold any: few), which
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
 #pragma unroll 4
-    for (int i = tid; i < len; i += kSelThreads) {
+    for (int i = pass ? tid : len; i < len; i += kSelThreads) {
       const uint32_t k = key_at(i);
       if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
     }
@@ -453,7 +457,10 @@ constexpr int kKeysMax = 48 * 1024;  // weights a CTA holds in shared memory (19
 
 // CTAs per (sequence, KV head): clusters as large as the GPU holds at once (a
 // CTA fills an SM; further waves cost a whole selection each), with at least
-// 2,048 candidates per CTA.
+// 2,048 candidates per CTA (1,024 or 8,192 instead: the same within 2 us).  Two
+// CTAs to an SM and clusters of up to 16 were slower: the eight barriers of a
+// selection cost more in a larger cluster (128K tokens 60 against 52.5 us a
+// call, 8 x 20K 81.5 against 75.8).
 int select_cluster(int64_t tokens, int64_t pairs) {
   int c = 1;
   while (c < kMaxCluster && 2 * c * pairs <= sm_count() && tokens >= 4096ll * c) c *= 2;
