@@ -1272,7 +1272,7 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
 // output rows.  A CTA merges its heads'
 // log-sum-exps (a warp per head), then a thread per token adds the heads in
 // order, so that results do not depend on timing.
-constexpr int kWeightPer = 4;  // tokens per thread
+constexpr int kMorePer = 8;
 struct WeightsParams {
   const float* scores;
   const float* lse_part;
@@ -1303,7 +1303,8 @@ KVQ_DEVINL void row_partials(const CombinePlan& cp, int b, int hq, int lane, siz
   first = (static_cast<size_t>(hq) * cp.kseg + k0) * kNW;
   S = cnt * kNW;
 }
-template <int NW>
+// PER: tokens per thread.
+template <int NW, int PER>
 __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_constant__ WeightsParams p) {
   if (static_cast<int>(blockIdx.x) >= p.weight_ctas) {
     const int i = blockIdx.x - p.weight_ctas;
@@ -1319,12 +1320,12 @@ __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_co
   const int cap = p.cp.max_blocks * kPage;
   const int L = min(max(ld_l2only_s32(p.cp.seq_lens + b), 0), cap);
   const int lo = (p.cp.window > 0 && L > p.cp.window) ? L - p.cp.window : 0;
-  const int t0 = chunk * (NW * 32 * kWeightPer) + threadIdx.x;
+  const int t0 = chunk * (NW * 32 * PER) + threadIdx.x;
   float* w = p.weights + static_cast<size_t>(pair) * p.stride;
   const int from = p.decay == 1.f ? lo : 0;  // tokens before it keep their weight
-  float a[kWeightPer];
+  float a[PER];
 #pragma unroll
-  for (int i = 0; i < kWeightPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int t = t0 + i * NW * 32;
     a[i] = t >= from && t < L ? __ldcg(w + t) * p.decay : 0.f;
   }
@@ -1338,9 +1339,9 @@ __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_co
     return t >= lo && t < L ? __ldcg(reinterpret_cast<const float2*>(sc + static_cast<size_t>(t) * p.gp + h))
                             : make_float2(-INFINITY, -INFINITY);
   };
-  float2 x[kWeightPer];
+  float2 x[PER];
 #pragma unroll
-  for (int i = 0; i < kWeightPer; ++i) x[i] = load(i, 0);
+  for (int i = 0; i < PER; ++i) x[i] = load(i, 0);
   for (int h = wid; h < p.g; h += NW) {
     size_t first;
     int S;
@@ -1369,26 +1370,26 @@ __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_co
     if (lane == 0) lse_s[h] = sum > 0.f ? M + log2f(sum) : 0.f;
   }
   __syncthreads();
-  float sum[kWeightPer];
+  float sum[PER];
 #pragma unroll
-  for (int i = 0; i < kWeightPer; ++i) sum[i] = 0.f;
+  for (int i = 0; i < PER; ++i) sum[i] = 0.f;
   for (int h = 0; h < p.g; h += 2) {
     const float l0 = lse_s[h], l1 = h + 1 < p.g ? lse_s[h + 1] : INFINITY;  // no such head: weight 0
 #pragma unroll
-    for (int i = 0; i < kWeightPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
       sum[i] += ex2(x[i].x - l0);
       sum[i] += ex2(x[i].y - l1);
       if (h + 2 < p.g) x[i] = load(i, h + 2);
     }
   }
 #pragma unroll
-  for (int i = 0; i < kWeightPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int t = t0 + i * NW * 32;
     if (t >= from && t < L) w[t] = a[i] + sum[i];
   }
   // The scores are spent: their lines leave L2 without being written to memory.
   __syncthreads();
-  const int begin = chunk * (NW * 32 * kWeightPer), stop = min(begin + NW * 32 * kWeightPer, (L + kPage - 1) / kPage * kPage);
+  const int begin = chunk * (NW * 32 * PER), stop = min(begin + NW * 32 * PER, (L + kPage - 1) / kPage * kPage);
   const char* spent = reinterpret_cast<const char*>(sc + static_cast<size_t>(begin) * p.gp);
   for (int o = threadIdx.x * 128; o < (stop - begin) * p.gp * 4; o += NW * 32 * 128)
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(spent + o) : "memory");
@@ -1512,11 +1513,18 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
     cfg.blockDim = dim3(NW * 32);
     if constexpr (SC) {
       weights->cp = cp;
-      const int per_cta = NW * 32 * kWeightPer;
-      weights->chunks = (p.max_blocks * kPage + per_cta - 1) / per_cta;
+      // Four tokens per thread, and kMorePer where that still leaves work for
+      // every SM: fewer CTAs merge the log-sum-exps (8 x 20K: 69.6 us a call with 4,
+      // 67.5 with 8, 71.2 with 16; 128K: 54.3, 52.2, 54.3; 8 x 2.5K: 15.8 with 4,
+      // 17.5 with 8).
+      const int64_t tokens = static_cast<int64_t>(p.max_blocks) * kPage;
+      const bool more = tokens * p.B * p.Hkv >= static_cast<int64_t>(kMorePer) * 512 * sms;
+      const int per_cta = NW * 32 * (more ? kMorePer : 4);
+      weights->chunks = static_cast<int>((tokens + per_cta - 1) / per_cta);
       weights->weight_ctas = weights->chunks * p.B * p.Hkv;
       cfg.gridDim = dim3(weights->weight_ctas + p.B * p.Hq * (D / 32));
-      return cudaLaunchKernelEx(&cfg, decode_weights_kernel<NW>, *weights);
+      return more ? cudaLaunchKernelEx(&cfg, decode_weights_kernel<NW, kMorePer>, *weights)
+                  : cudaLaunchKernelEx(&cfg, decode_weights_kernel<NW, 4>, *weights);
     } else {
       return cudaLaunchKernelEx(&cfg, decode_combine_kernel<NW>, op, lp, out, cp, D);
     }
@@ -1683,7 +1691,7 @@ kvq_status_t paged_decode(const void* q, const void* k_cache, const void* v_cach
       return fail(KVQ_ERR_INVALID_ARG, "paged_decode_weights: decay must be in [0, 1]");
     // CTAs of the last kernel: at least 512 tokens, or 32 dimensions of a row, each
     if ((static_cast<int64_t>(max_blocks) * P / 512 + 1) * B * Hkv + static_cast<int64_t>(B) * Hq * (D / 32) > 0x7FFFFFFF ||
-        static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFF - 32 * 32 * kWeightPer)
+        static_cast<int64_t>(max_blocks) * P > 0x7FFFFFFF - 32 * 32 * kMorePer)
       return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_weights: problem too large");
   }
   int S, pps;
