@@ -55,11 +55,11 @@ struct SharedParams {
 // Rows of group i: its sequences x the query heads of a KV head, in tiles of
 // 128; a unit is two tiles (the last of a group maybe one) over the prefix's
 // key tiles.  The cost of a unit is tiles x key tiles, after kUnitCost for
-// starting it (its queries, its first scores, its output: measured as about
-// twelve tiles' time).  Per KV head the batch's units are laid end to end and,
+// starting it (its queries, its first scores, its output: about as long as that
+// many tiles; 8 and 18 were within 2%).  Per KV head the batch's units are laid end to end and,
 // less the first unit's start, which every CTA pays, cut into equal slots, one
 // per CTA; a slot's part inside a unit is a segment.
-constexpr int kUnitCost = 12;
+constexpr int kUnitCost = 16;
 struct Group {
   int a, nb;        // first sequence, sequences
   int L, tiles, K;  // prefix tokens, row tiles, key tiles
@@ -286,6 +286,12 @@ KVQ_DEVINL void write_parts(const SharedParams& p, int lane) {
 // M is a row's first tile maximum and moves only when a later one is more than
 // 2^kSlack times larger (P then reaches at most 2^(8 + kSlack)), so that the
 // rescale of O by tensor-memory round trips is rare.
+// Bound by shared memory over long prefixes: a key tile of both streams moves
+// 272 KiB through it (Q and K for S twice over the two terms, V for O, the
+// copies and the conversion), 2,125 cycles at 128 bytes each; measured 2,850 (64
+// sequences of 4 heads after 128K tokens: 108 us, 1.27 PFLOP/s of 1.88).  Over
+// short ones by what a unit costs to start and end, about 10 us, most of it the
+// first fetch of the code.
 // MMAs of a CTA complete in issue order, and each S_j commit covers the P.V
 // issued before it: a stream's softmax sees O complete when S_j arrives, and
 // its P_j may lie over S_j.
@@ -523,6 +529,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
               // O += P V: a page per MMA (two halves of eight tokens, D * 16 bytes apart)
               const uint64_t vd = v_desc + (t & 1) * (2 * G::TILE >> 4);
               // the first half of the keys while the softmax works on the second
+              // (whole tiles: 19% slower over long prefixes; quarters: 25%)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
                 if (!wait(&bars->p_full[x][h], np & 1)) break;
@@ -569,43 +576,38 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         const int valid = s.L - kt * TK;  // tokens of the tile, if less than TK
         const uint8_t* src = smem + G::OFF_V + st * G::TILE;
         uint8_t* dst = smem + G::OFF_VH + (it & 1) * 2 * G::TILE;
-        constexpr int IT = TK / kPage * D / (kConvWarps * 32), CHUNK = 4;
-        const bool edge = dead != 0 || valid < TK;
-#pragma unroll 1
-        for (int i0 = 0; i0 < IT; i0 += CHUNK) {
-          uint4 c[CHUNK];
+        constexpr int IT = TK / kPage * D / (kConvWarps * 32);  // rows per thread
+        uint4 c[IT];  // all in flight (half of them at a time: 6% slower at head dim 128)
 #pragma unroll
-          for (int u = 0; u < CHUNK; ++u)
-            c[u] = *reinterpret_cast<const uint4*>(src + (t + (i0 + u) * kConvWarps * 32) * 16);
-          if (edge) {
+        for (int u = 0; u < IT; ++u) c[u] = *reinterpret_cast<const uint4*>(src + (t + u * kConvWarps * 32) * 16);
+        if (dead != 0 || valid < TK) {
 #pragma unroll 1
-            for (int u = 0; u < CHUNK; ++u) {
-              const int pg = (t + (i0 + u) * kConvWarps * 32) / D, left = valid - pg * kPage;
-              uint32_t m[4] = {0, 0, 0, 0};
-              if (!((dead >> pg) & 1)) {
+          for (int u = 0; u < IT; ++u) {
+            const int pg = (t + u * kConvWarps * 32) / D, left = valid - pg * kPage;
+            uint32_t m[4] = {0, 0, 0, 0};
+            if (!((dead >> pg) & 1)) {
 #pragma unroll
-                for (int tok = 0; tok < kPage; ++tok) {
-                  const int sl = fp8_v_slot(tok);
-                  if (tok < left) m[sl >> 2] |= 0xFFu << (8 * (sl & 3));
-                }
+              for (int tok = 0; tok < kPage; ++tok) {
+                const int sl = fp8_v_slot(tok);
+                if (tok < left) m[sl >> 2] |= 0xFFu << (8 * (sl & 3));
               }
-#pragma unroll
-              for (int k = 0; k < CHUNK; ++k)
-                if (k == u) c[k] = make_uint4(c[k].x & m[0], c[k].y & m[1], c[k].z & m[2], c[k].w & m[3]);
             }
-          }
 #pragma unroll
-          for (int u = 0; u < CHUNK; ++u) {
-            const int i = t + (i0 + u) * kConvWarps * 32, pg = i / D, d = i % D;
-            uint4 lo, hi;
-            fp8x4_to_f16x2x2<E5>(c[u].x, lo.x, lo.y);
-            fp8x4_to_f16x2x2<E5>(c[u].y, lo.z, lo.w);
-            fp8x4_to_f16x2x2<E5>(c[u].z, hi.x, hi.y);
-            fp8x4_to_f16x2x2<E5>(c[u].w, hi.z, hi.w);
-            uint8_t* o = dst + pg * 2 * G::PAGE + d * 16;
-            *reinterpret_cast<uint4*>(o) = lo;
-            *reinterpret_cast<uint4*>(o + D * 16) = hi;
+            for (int k = 0; k < IT; ++k)
+              if (k == u) c[k] = make_uint4(c[k].x & m[0], c[k].y & m[1], c[k].z & m[2], c[k].w & m[3]);
           }
+        }
+#pragma unroll
+        for (int u = 0; u < IT; ++u) {
+          const int i = t + u * kConvWarps * 32, pg = i / D, d = i % D;
+          uint4 lo, hi;
+          fp8x4_to_f16x2x2<E5>(c[u].x, lo.x, lo.y);
+          fp8x4_to_f16x2x2<E5>(c[u].y, lo.z, lo.w);
+          fp8x4_to_f16x2x2<E5>(c[u].z, hi.x, hi.y);
+          fp8x4_to_f16x2x2<E5>(c[u].w, hi.z, hi.w);
+          uint8_t* o = dst + pg * 2 * G::PAGE + d * 16;
+          *reinterpret_cast<uint4*>(o) = lo;
+          *reinterpret_cast<uint4*>(o + D * 16) = hi;
         }
         fence_proxy_async_smem();
         __syncwarp();

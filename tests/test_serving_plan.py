@@ -3,7 +3,7 @@ import random
 
 import numpy as np
 
-UNIT, TR, TK, UNIT_COST = 256, 128, 128, 12
+UNIT, TR, TK, UNIT_COST = 256, 128, 128, 16
 
 
 def _groups(g, spans, lens):
