@@ -34,7 +34,7 @@ struct EvictParams {
   int Hkv, max_blocks, max_dst;
   int64_t num_blocks;
   int sink, recent;
-  int seg_cap;  // weights of a CTA's segment held in shared memory (0: read from global memory each pass)
+  int seg_cap;  // keys of a CTA's segment held in shared memory (0: read from global memory each pass)
   int* dev_status;
 };
 
@@ -96,7 +96,9 @@ KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
 
 // Grid (cluster size, Hkv, B), one cluster per (sequence, KV head): CTA k of C
 // owns the k-th of C equal segments of the candidate positions.  Histograms
-// and counts meet through distributed shared memory.
+// and counts meet through distributed shared memory.  Bound by latency: ten
+// cluster barriers and three passes over the segment, 20.7 us cold for 64 pairs of
+// 20K candidates (their 5.2 MB of weights would take 0.8 us).
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint32_t held_k[];  // [seg_cap] the segment's keys
   __shared__ uint32_t hist[3][kBins];  // one per pass; the leader's collect the cluster's
@@ -182,9 +184,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
       }
     }
     sync_all();
-    if (rank != 0) {  // while the leader looks for the digit
-      if (pass == 0) ends(gtid - kSelThreads, gthreads - kSelThreads);
-    } else {
+    if (rank == 0) {
       // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
       const int hi = kBins - 1 - 2 * tid;
       const uint32_t c0 = hist[pass][hi], c1 = hist[pass][hi - 1];
@@ -210,7 +210,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     mask |= static_cast<uint32_t>(bins - 1) << shift;
     need = static_cast<int>(found[pass][1]);
   }
-  if (C == 1) ends(tid, kSelThreads);
   // prefix is the threshold; of the keys equal to it the first `need` are taken.
   // A warp takes a run of the segment, each lane four neighbours at a time.
   const int sub = (((len + kSelWarps - 1) / kSelWarps) + 127) / 128 * 128;
@@ -264,6 +263,9 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     gt_before += __reduce_add_sync(0xffffffffu, og);
     eq_before += __reduce_add_sync(0xffffffffu, oe);
   }
+  if (C > 1) cluster.sync();  // no CTA leaves while its totals may be read
+  // stores to global memory only after the last barrier, which would wait for them
+  ends(gtid, gthreads);
   for (int j = j0; j < j1; j += 128) {
     const int i = j + 4 * lane;
     uint32_t k[4];
@@ -294,7 +296,6 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     gt_before += both & 0xFFFF;
     eq_before += both >> 16;
   }
-  if (C > 1) cluster.sync();  // no CTA leaves while its totals may be read
 }
 
 // ------------------------------------------------------------------ move ---
@@ -312,7 +313,11 @@ KVQ_DEVINL void load16(const uint8_t* src, uint32_t* w) {
 // hold the rows (dimensions) of one source page at a time, read whole, and put
 // the kept tokens' bytes into their destination rows with byte permutes.
 // (Reading one 32-bit word per row and token instead touches every sector as
-// often as the page holds kept tokens: 80 against 64 us for 8 x 20K to 8K.)
+// often as the page holds kept tokens: 80 against 64 us for 8 x 20K to 8K when
+// it was tried.)  Bound by DRAM: 8 x 20K to 8K reads nearly every V page and 0.4
+// of the K rows, 333 MB with what it writes, in 59 us (5.7 TB/s).  Two warps per
+// page (79 to 85 us a call), and prefetches of the V pages into L2 during the
+// selection (80 to 85) or one page ahead, gained nothing.
 template <int D, int ESZ, bool PT>
 __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __grid_constant__ EvictParams p) {
   constexpr int ROWB = D * ESZ;
@@ -458,7 +463,7 @@ constexpr int kKeysMax = 48 * 1024;  // weights a CTA holds in shared memory (19
 // CTAs per (sequence, KV head): clusters as large as the GPU holds at once (a
 // CTA fills an SM; further waves cost a whole selection each), with at least
 // 2,048 candidates per CTA (1,024 or 8,192 instead: the same within 2 us).  Two
-// CTAs to an SM and clusters of up to 16 were slower: the eight barriers of a
+// CTAs to an SM and clusters of up to 16 were slower: the barriers of a
 // selection cost more in a larger cluster (128K tokens 60 against 52.5 us a
 // call, 8 x 20K 81.5 against 75.8).
 int select_cluster(int64_t tokens, int64_t pairs) {
