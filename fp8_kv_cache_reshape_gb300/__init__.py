@@ -431,10 +431,24 @@ def _check_scales(k_scale, v_scale, Hkv):
             _check_tensor(t, torch.float32, (Hkv,), name)
 
 
-def _check_device(t):
-    if t.is_cuda and t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one "
-                         f"(cuda:{torch.cuda.current_device()})")
+def _device_ptrs(*tensors):
+    """Addresses of contiguous tensors on the current device (None for None)."""
+    if not tensors[0].is_cuda:
+        raise ValueError("libkvq takes CUDA tensors only")
+    current = torch.cuda.current_device()
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != current:
+            if not t.is_cuda:
+                raise ValueError("libkvq takes CUDA tensors only")
+            raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one (cuda:{current})")
+        if not t.is_contiguous():
+            raise ValueError("libkvq takes contiguous tensors only")
+        out.append(t.data_ptr())
+    return out
 
 
 def _workspace(need, like, stream):
@@ -470,14 +484,14 @@ def kvq_paged_decode_attention_shared_prefix(q, k_cache, v_cache, k_scale, v_sca
     dt = _dtype_code(cache_dtype)
     _check_scales(k_scale, v_scale, Hkv)
     num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, False, num_blocks)
-    _check_device(q)
     if workspace is None:
         workspace = _workspace(kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix, max_blocks), q, stream)
+    *ptrs, ws, status = _device_ptrs(q, k_cache, v_cache, k_scale, v_scale, prefix_table, prefix_lens, group_starts,
+                                     block_table, seq_lens, out, workspace, dev_status)
     _check(lib.kvq_paged_decode_attention_shared_prefix(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(prefix_table), _ptr(prefix_lens),
-        _ptr(group_starts), _ptr(block_table), _ptr(seq_lens), _ptr(out), B, G, Hq, Hkv, D, PAGE, max_prefix,
-        max_blocks, num_blocks, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), dt, _ptr(workspace),
-        workspace.numel(), _ptr(dev_status), _stream(stream)), "kvq_paged_decode_attention_shared_prefix")
+        *ptrs, B, G, Hq, Hkv, D, PAGE, max_prefix, max_blocks, num_blocks,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), dt, ws, workspace.nbytes, status,
+        _stream(stream)), "kvq_paged_decode_attention_shared_prefix")
     return out
 
 
@@ -504,15 +518,14 @@ def kvq_paged_decode_attention_weights(q, k_cache, v_cache, k_scale, v_scale, bl
     dt = _dtype_code(cache_dtype)
     _check_scales(k_scale, v_scale, Hkv)
     num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
-    _check_device(q)
     if workspace is None:
         workspace = _workspace(kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits), q, stream)
+    *ptrs, ws, status = _device_ptrs(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, weights, workspace,
+                                     dev_status)
     _check(lib.kvq_paged_decode_attention_weights(
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table), _ptr(seq_lens),
-        _ptr(out), _ptr(weights), weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
-        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, dt,
-        1 if per_token else 0, num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream)),
-        "kvq_paged_decode_attention_weights")
+        *ptrs, weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, dt, 1 if per_token else 0, num_splits, ws,
+        workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_weights")
     return out
 
 
@@ -537,9 +550,11 @@ def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens
     _check_tensor(kept, torch.int32, (B, Hkv, max_dst * PAGE), "kept")
     dt = _dtype_code(cache_dtype)
     num_blocks = _check_cache(k_cache, v_cache, Hkv, head_dim, dt, per_token, num_blocks)
-    _check_device(weights)
+    (w, kc, vc, bt, lens, keep, dst, dst_w, dst_lens, src, status) = _device_ptrs(
+        weights, k_cache, v_cache, block_table, seq_lens, keep_lens, dst_block_table, dst_weights, dst_seq_lens, kept,
+        dev_status)
     _check(lib.kvq_evict_tokens(
-        _ptr(weights), weights.shape[-1], _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seq_lens),
-        _ptr(keep_lens), _ptr(dst_block_table), _ptr(dst_weights), dst_weights.shape[-1], _ptr(dst_seq_lens),
-        _ptr(kept), B, Hkv, head_dim, PAGE, max_blocks, max_dst, num_blocks, sink, recent, dt, 1 if per_token else 0, _ptr(dev_status), _stream(stream)), "kvq_evict_tokens")
+        w, weights.shape[-1], kc, vc, bt, lens, keep, dst, dst_w, dst_weights.shape[-1], dst_lens, src, B, Hkv, head_dim,
+        PAGE, max_blocks, max_dst, num_blocks, min(sink, 2**31 - 1), min(recent, 2**31 - 1), dt, 1 if per_token else 0,
+        status, _stream(stream)), "kvq_evict_tokens")
     return dst_seq_lens

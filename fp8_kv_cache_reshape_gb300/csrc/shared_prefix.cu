@@ -56,9 +56,9 @@ struct SharedParams {
 // 128; a unit is two tiles (the last of a group maybe one) over the prefix's
 // key tiles.  The cost of a unit is tiles x key tiles, after kUnitCost for
 // starting it (its queries, its first scores, its output: about as long as that
-// many tiles; 8 and 18 were within 2%).  Per KV head the batch's units are laid end to end and,
-// less the first unit's start, which every CTA pays, cut into equal slots, one
-// per CTA; a slot's part inside a unit is a segment.
+// many tiles; 8 and 18 were within 2%).  Per KV head the batch's units are
+// laid end to end and, less the first unit's start, which every CTA pays, cut
+// into equal slots, one per CTA; a slot's part inside a unit is a segment.
 constexpr int kUnitCost = 16;
 struct Group {
   int a, nb;        // first sequence, sequences
@@ -100,9 +100,10 @@ KVQ_DEVINL void scan_groups(int& cost, int& units, int lane) {
     }
   }
 }
-// The cut of the stream [kUnitCost, W) of cost (below 2^31, checked on the
-// host; with faulty groups it may wrap, which the clamps keep in bounds) into
-// used slots: the first `rem` slots hold q + 1, the others q.
+// The cut of the stream [kUnitCost, W) of cost into used slots: the first `rem`
+// slots hold q + 1, the others q.  The host checks that W is below 2^31 for
+// groups in order; faulty ones, which may overlap, can make it wrap, and what
+// follows from it is then clamped or dropped where it would index out of bounds.
 struct Cut {
   int q, rem, used;
   KVQ_DEVINL Cut(const SharedParams& p, int W) {
@@ -115,7 +116,7 @@ struct Cut {
   KVQ_DEVINL int slot_of(int x) const {
     x -= kUnitCost;
     const int y = x - rem * (q + 1);
-    return min(used - 1, y < 0 ? x / (q + 1) : rem + y / q);
+    return max(0, min(used - 1, y < 0 ? x / (q + 1) : rem + y / q));
   }
 };
 
@@ -191,7 +192,8 @@ struct SegWalk {
       s.once = tiles <= 2;
       s.nq = min(2, tiles - 2 * u);
       const int stop = min(end, ustart + s.nq * K);
-      if (stop <= ustart) break;  // the slot ends before the unit's first tile
+      // the slot ends before the unit's first tile; or a wrapped stream
+      if (stop <= ustart || u < 0 || u >= (tiles + 1) / 2) break;
       pos = max(pos, ustart);
       s.k0 = s.nq == 2 ? (pos - ustart + 1) >> 1 : pos - ustart;
       s.k1 = s.nq == 2 ? (stop - ustart + 1) >> 1 : stop - ustart;
@@ -202,7 +204,8 @@ struct SegWalk {
       s.group = gi;
       s.unit = ubase + u;
       pos = stop;
-      return s.unit < p.max_units;  // false only with faulty group_starts (reported)
+      // false only with faulty group_starts (reported)
+      return s.k0 >= 0 && s.k1 >= s.k0 && s.k1 <= K && s.unit >= 0 && s.unit < p.max_units;
     }
     return false;
   }
@@ -245,10 +248,10 @@ KVQ_DEVINL void write_parts(const SharedParams& p, int lane) {
     }
     int4 e = make_int4(0, 1 << 24, 0, 0);
     const int row = (b - a) * p.g + lane, un = row / UNIT;
-    if (found && K > 0 && lane < p.g && ubase + un < p.max_units) {
+    if (found && K > 0 && lane < p.g && ubase + un >= 0 && ubase + un < p.max_units) {
       const int nq = min(2, tiles - 2 * un), c0 = gstart + un * (2 * K + kUnitCost) + kUnitCost;
       const Cut cut(p, W);
-      const int s0 = cut.slot_of(c0), ns = cut.slot_of(c0 + nq * K - 1) - s0 + 1;
+      const int s0 = cut.slot_of(c0), ns = max(1, cut.slot_of(c0 + nq * K - 1) - s0 + 1);
       e.x = (s0 + ubase + un) * UNIT + row % UNIT;
       e.y = nq == 1 ? (2 * ns) | (2 << 24) : ns | (1 << 24);
     }
@@ -292,9 +295,9 @@ KVQ_DEVINL void write_parts(const SharedParams& p, int lane) {
 // sequences of 4 heads after 128K tokens: 108 us, 1.27 PFLOP/s of 1.88).  Over
 // short ones by what a unit costs to start and end, about 10 us, most of it the
 // first fetch of the code.
-// MMAs of a CTA complete in issue order, and each S_j commit covers the P.V
-// issued before it: a stream's softmax sees O complete when S_j arrives, and
-// its P_j may lie over S_j.
+// A stream's MMAs, issued by one thread, complete in order, and each S_j commit
+// covers the P.V issued before it: its softmax sees O complete when S_j arrives,
+// and its P_j may lie over S_j.
 constexpr int kSoftWarps = 8;           // 0-3 stream 0, 4-7 stream 1
 constexpr int kConvWarps = 4;           // 8-11
 constexpr int W_K = 12, W_V = 13, W_MMA = 14;  // an issuing warp per stream: 14, 15

@@ -78,3 +78,41 @@ def test_cpu_tensors_are_refused(k, call):
     """Everything else in order: the tensors are not on a GPU."""
     with pytest.raises(ValueError, match="CUDA tensors only"):
         call(k)
+
+
+class _OnGpu:
+    is_cuda = True
+
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 16 * self.index
+
+
+def test_tensors_of_another_device_are_refused(k, monkeypatch):
+    """Any of them, whatever its place in the call."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert k._device_ptrs(_OnGpu(1), None, _OnGpu(1)) == [16, None, 16]
+    for bad in ((_OnGpu(0),), (_OnGpu(1), None, _OnGpu(0))):
+        with pytest.raises(ValueError, match=r"cuda:0\) must be the current one \(cuda:1\)"):
+            k._device_ptrs(*bad)
+    with pytest.raises(ValueError, match="CUDA tensors only"):
+        k._device_ptrs(_OnGpu(1), torch.zeros(1))
+
+
+def test_a_protected_end_beyond_32_bits_means_every_token(k, monkeypatch):
+    seen = {}
+    monkeypatch.setattr(k, "_device_ptrs", lambda *t: [None] * len(t))
+    monkeypatch.setattr(k, "_stream", lambda s: None)
+    monkeypatch.setattr(k.lib, "kvq_evict_tokens", lambda *a: seen.update(sink=a[19], recent=a[20]) or 0)
+    a = _base(k)
+    k.kvq_evict_tokens(torch.zeros(B, H, 48), a["kd"], a["vd"], a["bt"], a["sl"], _i(B), _i(B, 2), torch.zeros(B, H, 32),
+                       _i(B), _i(B, H, 32), D, sink=2**32, recent=10**12)
+    assert seen == {"sink": 2**31 - 1, "recent": 2**31 - 1}

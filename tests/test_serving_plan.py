@@ -81,6 +81,70 @@ def test_prefix_plan_covers_every_tile_once_and_the_merge_finds_it():
             gstart, ubase = gstart + cost, ubase + units
 
 
+def _w(x):
+    """x as a 32-bit integer wraps."""
+    return (x + 2**31) % 2**32 - 2**31
+
+
+def _div(a, b):
+    """C's division (toward zero); a division by zero gives some value."""
+    return (abs(a) // abs(b)) * (1 if (a < 0) == (b < 0) else -1) if b else -1
+
+
+def test_a_wrapped_plan_stays_in_bounds():
+    """Overlapping groups (reported as faulty) can push the summed cost past 32
+    bits; no segment and no merge entry may then leave its arrays."""
+    rng = random.Random(3)
+    for _ in range(20000):
+        max_units, slots = rng.randint(1, 4000), rng.randint(1, 152)
+        tiles, K = rng.randint(1, 4000), rng.randint(1, 1 << 20)
+        nb_rows = rng.randint((tiles - 1) * TR + 1, tiles * TR)
+        W = rng.choice([_w(rng.getrandbits(32)), rng.randint(-40, 40), 2**31 - 1 - rng.randint(0, 40)])
+        gstart, ubase = _w(rng.getrandbits(32)), rng.choice([rng.randint(0, 4000), _w(rng.getrandbits(32))])
+        w = _w(W - UNIT_COST)
+        used = max(0, min(w, slots))
+        q = w // used if used else 0
+        rem = w - q * used if used else 0
+
+        def slot_of(x):
+            x = _w(x - UNIT_COST)
+            y = _w(x - _w(rem * _w(q + 1)))
+            return max(0, min(used - 1, _div(x, _w(q + 1)) if y < 0 else _w(rem + _div(y, q))))
+
+        units = (tiles + 1) // 2
+        # the merge table's entry of a row of the group
+        un = rng.randint(0, nb_rows - 1) // UNIT
+        if 0 <= _w(ubase + un) < max_units:
+            c0 = _w(gstart + _w(un * (2 * K + UNIT_COST)) + UNIT_COST)
+            s0 = slot_of(c0)
+            ns = max(1, slot_of(_w(c0 + min(2, tiles - 2 * un) * K - 1)) - s0 + 1)
+            assert 0 <= s0 and s0 + ns <= slots and 0 <= _w(ubase + un) + s0 + ns - 1 < slots + max_units
+        # a step of a slot's walk
+        slot = rng.randint(0, slots - 1)
+        if slot >= used:
+            continue
+        pos = _w(UNIT_COST + _w(slot * q) + min(slot, rem))
+        end = _w(UNIT_COST + _w((slot + 1) * q) + min(slot + 1, rem))
+        cost = _w(tiles * K + units * UNIT_COST)
+        if pos >= end or pos >= _w(gstart + cost):
+            continue
+        u = 0
+        if _w(pos - gstart) >= 2 * K + UNIT_COST:
+            u = _w((_w(pos - gstart) % 2**32) // (2 * K + UNIT_COST))
+        first = _w(gstart + _w(u * (2 * K + UNIT_COST)) + UNIT_COST)
+        nq = min(2, _w(tiles - _w(2 * u)))
+        stop = min(end, _w(first + _w(nq * K)))
+        if stop <= first or u < 0 or u >= units:
+            continue
+        pos = max(pos, first)
+        k0, k1 = ((_w(_w(x - first) + 1) >> 1) if nq == 2 else _w(x - first) for x in (pos, stop))
+        unit = _w(ubase + u)
+        if not (k0 >= 0 and k1 >= k0 and k1 <= K and 0 <= unit < max_units):
+            continue
+        assert nq in (1, 2) and 0 <= k0 <= k1 <= K and 0 <= slot + unit < slots + max_units
+        assert 0 < min(UNIT, nb_rows - u * UNIT)  # its rows are the group's
+
+
 def test_wide_plan_covers_every_page_once():
     """The own tokens' plan: slots of the batch's pages laid end to end."""
     rng = random.Random(2)
