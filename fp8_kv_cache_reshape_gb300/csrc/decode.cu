@@ -509,7 +509,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
   }
   // p.late (BAL 2): this grid runs beside the one that precedes it, which it
   // does not depend on and which started after all that it does depend on had
-  // completed; it waits for it only before it ends.
+  // completed; its last CTA waits for it before it ends, and so the grid does
+  // not complete before it (every CTA waiting would keep the SMs from the next).
   if (BAL != 2 || !p.late) grid_dependency_wait();
   if (!p.direct) grid_launch_dependents();
 
@@ -1153,7 +1154,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, ctas_per_sm<D>()) decode_partia
       }
     }
   }
-  if (BAL == 2 && p.late) grid_dependency_wait();
+  if (BAL == 2 && p.late && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 // out[row][d] = sum_s 2^(lse_s - M) o_s[d] / sum_s 2^(lse_s - M) over the

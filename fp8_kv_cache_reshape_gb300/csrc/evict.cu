@@ -42,6 +42,7 @@ struct EvictParams {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
 
 // Order-preserving image of a weight: a < b <=> image(a) < image(b); the two
 // zeros are equal, NaN ranks below everything.
@@ -96,15 +97,16 @@ KVQ_DEVINL int warp_scan_excl(int x, int lane, int& total) {
 
 // Grid (cluster size, Hkv, B), one cluster per (sequence, KV head): CTA k of C
 // owns the k-th of C equal segments of the candidate positions.  Histograms
-// and counts meet through distributed shared memory.  Bound by latency: ten
-// cluster barriers and three passes over the segment, 20.7 us cold for 64 pairs of
-// 20K candidates (their 5.2 MB of weights would take 0.8 us).
+// and counts meet through distributed shared memory.  Bound by latency:
+// four cluster barriers (eight in clusters of more than two) and three passes
+// over the segment, 16 us for 64 pairs of 20K candidates (their 5.2 MB of weights
+// would take 0.8 us).
 __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __grid_constant__ EvictParams p) {
   extern __shared__ __align__(16) uint32_t held_k[];  // [seg_cap] the segment's keys
-  __shared__ uint32_t hist[3][kBins];  // one per pass; the leader's collect the cluster's
+  __shared__ __align__(8) uint32_t hist[3][kBins];  // counts, one histogram per pass
   __shared__ int warp_gt[kSelWarps], warp_eq[kSelWarps];
-  __shared__ int totals[2];  // this CTA's counts above and at the threshold, read by the cluster
-  __shared__ uint32_t found[3][2];  // per pass: chosen bin, keys still needed inside it
+  __shared__ int2 totals[kMaxCluster];  // each CTA's counts above and at the threshold
+  __shared__ uint32_t found[3][2];      // per pass: chosen bin, keys still needed inside it
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
@@ -142,16 +144,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     }
     return;
   }
-  auto sync_all = [&]() {
-    if (C == 1) __syncthreads();
-    else cluster.sync();
-  };
   const int seg = (N + C - 1) / C;
   const int i0 = min(N, rank * seg), i1 = min(N, i0 + seg), len = i1 - i0;
   const float* wseg = w + cut.s + i0;
   const bool held = len <= p.seg_cap;
   for (int i = tid; i < 3 * kBins; i += kSelThreads) hist[0][i] = 0;
   __syncthreads();
+  const bool lead = C > 2;  // see the passes
+  if (lead) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   // the keys, and their first digit's histogram on the way
 #pragma unroll 8
   for (int i = tid; i < len; i += kSelThreads) {
@@ -160,52 +160,79 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
     atomicAdd(&hist[0][k >> 21], 1u);
   }
   auto key_at = [&](int i) { return held ? held_k[i] : weight_key(wseg[i]); };
-  sync_all();  // every CTA's histograms hold their own counts or zeros
+  if (lead) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // the leader's histograms are zeroed
 
-  // threshold: the m-th largest key, digit by digit from the top.  The CTAs add
-  // their counts to the leader's histogram (bins that hold any: few), which
-  // finds the digit and hands it out.
+  // threshold: the m-th largest key, digit by digit from the top.  In a pair of
+  // CTAs each adds the other's counts to its own and finds the digit for itself,
+  // with one barrier a pass (8 x 20K: 73.6 us a call, 75.0 with a leader).  In a
+  // larger cluster the others add their counts (bins that hold any: few) to the
+  // leader's histogram, and it finds the digit and hands it out (128K in clusters
+  // of eight: 51.1 us a call; every CTA reading all the histograms: 54.6).
   uint32_t prefix = 0, mask = 0;
   int need = m;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass < 2 ? 2048 : 1024;
+    if (pass) {
+      auto add = [&](uint32_t k) {
+        if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
+      };
+      if (held) {
+        const int quads = len >> 2;
+#pragma unroll 2
+        for (int i = tid; i < quads; i += kSelThreads) {
+          const uint4 k = reinterpret_cast<const uint4*>(held_k)[i];
+          add(k.x);
+          add(k.y);
+          add(k.z);
+          add(k.w);
+        }
+        for (int i = 4 * quads + tid; i < len; i += kSelThreads) add(held_k[i]);
+      } else {
 #pragma unroll 4
-    for (int i = pass ? tid : len; i < len; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if ((k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
-    }
-    if (rank != 0) {
-      __syncthreads();
-      uint32_t* lead = cluster.map_shared_rank(&hist[pass][0], 0);
-      for (int i = tid; i < bins; i += kSelThreads) {
-        const uint32_t c = hist[pass][i];
-        if (c) atomicAdd(lead + i, c);
+        for (int i = tid; i < len; i += kSelThreads) add(weight_key(wseg[i]));
       }
     }
-    sync_all();
-    if (rank == 0) {
+    if (lead && rank != 0) {
+      __syncthreads();
+      uint32_t* theirs = cluster.map_shared_rank(&hist[pass][0], 0);
+      for (int i = tid; i < bins; i += kSelThreads) {
+        const uint32_t c = hist[pass][i];
+        if (c) atomicAdd(theirs + i, c);
+      }
+    }
+    if (C == 1) __syncthreads();
+    else cluster.sync();
+    if (!lead || rank == 0) {
       // bin pairs from the top: thread t sums bins kBins - 1 - 2t and the one below
       const int hi = kBins - 1 - 2 * tid;
-      const uint32_t c0 = hist[pass][hi], c1 = hist[pass][hi - 1];
+      uint2 c = *reinterpret_cast<const uint2*>(&hist[pass][hi - 1]);
+      if (C == 2) {
+        const uint2 o = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&hist[pass][hi - 1], rank ^ 1));
+        c.x += o.x;
+        c.y += o.y;
+      }
       int tot;
-      const int excl = warp_scan_excl(static_cast<int>(c0 + c1), lane, tot);
+      const int excl = warp_scan_excl(static_cast<int>(c.x + c.y), lane, tot);
       if (lane == 0) warp_gt[wid] = tot;
       __syncthreads();
       int all;
       const int wx = warp_scan_excl(warp_gt[lane], lane, all);
       const int before = excl + __shfl_sync(0xffffffffu, wx, wid);
-      if (before < need && before + static_cast<int>(c0 + c1) >= need) {  // exactly one thread
-        const bool first = before + static_cast<int>(c0) >= need;
-        const uint32_t bin = first ? hi : hi - 1, left = need - (first ? before : before + static_cast<int>(c0));
-        for (int k = 0; k < C; ++k) {
+      if (before < need && before + static_cast<int>(c.x + c.y) >= need) {  // exactly one thread
+        const bool first = before + static_cast<int>(c.y) >= need;
+        const uint32_t bin = first ? hi : hi - 1, left = need - (first ? before : before + static_cast<int>(c.y));
+        found[pass][0] = bin;
+        found[pass][1] = left;
+        for (int k = 1; lead && k < C; ++k) {
           uint32_t* f = cluster.map_shared_rank(&found[pass][0], k);
           f[0] = bin;
           f[1] = left;
         }
       }
     }
-    sync_all();
+    if (lead) cluster.sync();
+    else __syncthreads();
     prefix |= found[pass][0] << shift;
     mask |= static_cast<uint32_t>(bins - 1) << shift;
     need = static_cast<int>(found[pass][1]);
@@ -247,23 +274,14 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(const __gr
   __syncthreads();
   int gt_all, eq_all;
   const int gx = warp_scan_excl(warp_gt[lane], lane, gt_all), ex = warp_scan_excl(warp_eq[lane], lane, eq_all);
-  if (tid == 0) {
-    totals[0] = gt_all;
-    totals[1] = eq_all;
-  }
-  sync_all();
   int gt_before = __shfl_sync(0xffffffffu, gx, wid), eq_before = __shfl_sync(0xffffffffu, ex, wid);
-  {
-    int og = 0, oe = 0;
-    if (lane < rank) {  // at most 8 CTAs
-      const int* other = cluster.map_shared_rank(totals, lane);
-      og = other[0];
-      oe = other[1];
-    }
-    gt_before += __reduce_add_sync(0xffffffffu, og);
-    eq_before += __reduce_add_sync(0xffffffffu, oe);
+  if (C > 1) {
+    if (tid < C) *cluster.map_shared_rank(&totals[rank], tid) = make_int2(gt_all, eq_all);
+    cluster.sync();  // the last access to another CTA's memory is behind it
+    const int2 other = lane < rank ? totals[lane] : make_int2(0, 0);  // at most 8 CTAs
+    gt_before += __reduce_add_sync(0xffffffffu, other.x);
+    eq_before += __reduce_add_sync(0xffffffffu, other.y);
   }
-  if (C > 1) cluster.sync();  // no CTA leaves while its totals may be read
   // stores to global memory only after the last barrier, which would wait for them
   ends(gtid, gthreads);
   for (int j = j0; j < j1; j += 128) {
@@ -457,8 +475,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __gri
   }
 }
 
-constexpr int kMaxCluster = 8;
-constexpr int kKeysMax = 48 * 1024;  // weights a CTA holds in shared memory (192 KiB)
+constexpr int kKeysMax = 48 * 1024;  // keys a CTA holds in shared memory (192 KiB)
 
 // CTAs per (sequence, KV head): clusters as large as the GPU holds at once (a
 // CTA fills an SM; further waves cost a whole selection each), with at least
