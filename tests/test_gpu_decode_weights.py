@@ -93,6 +93,21 @@ def test_split_counts(splits):
     assert np.allclose(got.sum(-1), 4.0, rtol=1e-5)
 
 
+@pytest.mark.parametrize("splits", [3, 9, 20, 60])
+@pytest.mark.parametrize("blocks", [150, 5000])  # table columns: four and eight tokens per thread of the last kernel
+def test_every_merge_width(splits, blocks):
+    lens = [2300, 900]
+    pool = Pool(220, 8, 64, FP8, 6)
+    table = np.full((2, blocks), -1, np.int32)
+    short = pool.table(lens)
+    table[:, :short.shape[1]] = short
+    q, qv = pool.query(2, 3)
+    weights = pool.rng.exponential(size=(2, 8, blocks * P)).astype(np.float32)
+    out, got, st = _run(pool, table, lens, q, weights, 0.5, num_splits=splits)
+    assert st == 0
+    _check(pool, table, lens, qv, weights, 0.5, -1, out, got)
+
+
 @pytest.mark.parametrize("dtype,per_token", [(FP8, False), (FP8_E5M2, False), (BF16, False), (FP8, True)])
 def test_output_is_the_plain_decodes(dtype, per_token):
     """The same plan and kernels as kvq_paged_decode_attention: equal bits

@@ -133,6 +133,32 @@ def test_selection_of_a_long_sequence():
     assert int(dl) == keep
 
 
+@pytest.mark.parametrize("L,heads,keep", [(20_000, 50, 3000), (20_001, 20, 9999), (70_000, 9, 501),  # clusters of 2, 4, 8
+                                          (420_000, 2, 30_000), (60_000, 80, 2000)])  # keys read from memory each pass
+def test_selection_over_clusters_and_lengths(L, heads, keep):
+    k = _k()
+    gen = torch.Generator(device="cuda").manual_seed(L)
+    blocks, nd = -(-L // P), -(-keep // P)
+    table = torch.arange(blocks, dtype=torch.int32, device="cuda")[None]
+    dst = torch.arange(blocks, blocks + nd, dtype=torch.int32, device="cuda")[None]
+    kd, vd = k.alloc_kv_cache(blocks + nd, heads, 64, fill=0)
+    w = torch.zeros(1, heads, blocks * P, device="cuda")
+    # ties around every threshold; in the odd heads a value for most tokens
+    w[..., :L] = torch.floor(torch.rand(1, heads, L, generator=gen, device="cuda") * 300)
+    w[:, 1::2] = torch.maximum(w[:, 1::2], torch.tensor(250.0, device="cuda"))
+    dw, kept = torch.empty(1, heads, nd * P, device="cuda"), torch.zeros(1, heads, nd * P, dtype=torch.int32, device="cuda")
+    dl = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k.kvq_evict_tokens(w, kd, vd, table, i32([L]), i32([keep]), dst, dw, dl, kept, head_dim=64, sink=4, recent=100)
+    score = w.clone()
+    score[..., :4] = float("inf")
+    score[..., L - 100:L] = float("inf")
+    score[..., L:] = float("-inf")
+    best = torch.sort(score, descending=True, stable=True).indices[..., :keep].sort().values
+    assert torch.equal(kept[..., :keep].long(), best)
+    assert torch.equal(dw[..., :keep], w.gather(-1, best))
+    assert int(dl) == keep
+
+
 def test_bad_pages_and_lengths_are_reported():
     pool = Pool(60, 1, 64, FP8, 19)
     table = pool.table([200, 60])

@@ -69,6 +69,42 @@ def test_matches_oracle(name, paired):
     assert_output(out, ref, mag)
 
 
+# prefixes long enough, for their KV heads, that the prefix's grid goes first (eight tiles per CTA or more)
+PREFIX_FIRST = {
+    "one_slot_per_head": ([1000], [0, 2], [3, 40], 160, 1, 64, FP8),
+    "two_tiles": ([1500], [0, 32], [(29 * i) % 100 for i in range(32)], 40, 8, 64, FP8_E5M2),
+    "groups": ([1100, 0, 700], [0, 20, 22, 39], [(17 * i) % 50 for i in range(40)], 40, 8, 128, FP8),
+    "nothing_of_their_own": ([1500], [0, 32], [0] * 32, 40, 8, 128, FP8),
+}
+
+
+@pytest.mark.parametrize("name", list(PREFIX_FIRST))
+def test_long_prefix_first(name):
+    prefixes, starts, own, heads, group, dim, dtype = PREFIX_FIRST[name]
+    pool, pre, mine, (q, qv), starts = _case(prefixes, starts, own, heads, group, dim, dtype)
+    out, st = _run(pool, pre, prefixes, starts, mine, own, q)
+    assert st == 0
+    ref, mag = serving.shared_prefix_decode(qv, pool.k, pool.v, pool.k_scale, pool.v_scale, pre, prefixes, starts, mine,
+                                            own, 1.0 / np.sqrt(dim), dtype)
+    assert_output(out, ref, mag)
+    # in stream order over one workspace, eager and captured: the same bits
+    k = _k()
+    kd, vd = pool.device()
+    args = [q, kd, vd, *pool.device_scales(), i32(pre), i32(prefixes), i32(starts), i32(mine), i32(own)]
+    ws = torch.empty(k.kvq_shared_prefix_workspace_size(len(own), len(prefixes), heads * group, heads, dim, pre.shape[1],
+                                                        mine.shape[1]), dtype=torch.uint8, device="cuda")
+    outs, g = [torch.zeros_like(q) for _ in range(4)], torch.cuda.CUDAGraph()
+    for o in outs[:2]:
+        k.kvq_paged_decode_attention_shared_prefix(*args, o, cache_dtype=dtype, workspace=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        for o in outs[2:]:
+            k.kvq_paged_decode_attention_shared_prefix(*args, o, cache_dtype=dtype, workspace=ws)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o.view(torch.int16), out.view(torch.int16)) for o in outs)
+
+
 def test_equals_plain_decode_over_the_joined_table():
     """A prefix of whole pages: the same attention as plain decode over the
     prefix's and the sequence's pages in one table."""
