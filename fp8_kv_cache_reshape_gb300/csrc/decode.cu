@@ -1510,17 +1510,19 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
   const int parts = (p.num_splits + (p.balanced ? 2 : 0)) * kNW;
   const float* op = p.o_part;
   const float* lp = p.lse_part;
+  // The weights: four tokens per thread, and kMorePer where that still leaves work
+  // for every SM, fewer CTAs then merging the log-sum-exps (8 x 20K: 69.6 us a call
+  // with 4, 67.5 with 8, 71.2 with 16; 128K: 54.3, 52.2, 54.3; 8 x 2.5K: 15.8 with
+  // 4, 17.5 with 8).  There the combine's rows, which run beside them, take half
+  // the warps (8 x 20K: 66.5 to 65.0 us, 128K: 51.4 to 50.6).
+  const int64_t tokens = static_cast<int64_t>(p.max_blocks) * kPage;
+  const bool more = SC && tokens * p.B * p.Hkv >= static_cast<int64_t>(kMorePer) * 512 * sms;
+  const int per_warp = more ? 2 * kCombinePer : kCombinePer;
   auto finish = [&](auto warps) {
     constexpr int NW = decltype(warps)::value;
     cfg.blockDim = dim3(NW * 32);
     if constexpr (SC) {
       weights->cp = cp;
-      // Four tokens per thread, and kMorePer where that still leaves work for
-      // every SM: fewer CTAs merge the log-sum-exps (8 x 20K: 69.6 us a call with 4,
-      // 67.5 with 8, 71.2 with 16; 128K: 54.3, 52.2, 54.3; 8 x 2.5K: 15.8 with 4,
-      // 17.5 with 8).
-      const int64_t tokens = static_cast<int64_t>(p.max_blocks) * kPage;
-      const bool more = tokens * p.B * p.Hkv >= static_cast<int64_t>(kMorePer) * 512 * sms;
       const int per_cta = NW * 32 * (more ? kMorePer : 4);
       weights->chunks = static_cast<int>((tokens + per_cta - 1) / per_cta);
       weights->weight_ctas = weights->chunks * p.B * p.Hkv;
@@ -1531,11 +1533,11 @@ kvq_status_t launch_decode(const DecodeParams& p, __nv_bfloat16* out, cudaStream
       return cudaLaunchKernelEx(&cfg, decode_combine_kernel<NW>, op, lp, out, cp, D);
     }
   };
-  if (parts <= 4 * kCombinePer)
+  if (parts <= 4 * per_warp)
     e = finish(std::integral_constant<int, 4>());
-  else if (parts <= 8 * kCombinePer)
+  else if (parts <= 8 * per_warp)
     e = finish(std::integral_constant<int, 8>());
-  else if (parts <= 16 * kCombinePer)
+  else if (parts <= 16 * per_warp)
     e = finish(std::integral_constant<int, 16>());
   else
     e = finish(std::integral_constant<int, 32>());
