@@ -1273,7 +1273,7 @@ __global__ void __launch_bounds__(NW * 32) decode_combine_kernel(const float* __
 // output rows.  A CTA merges its heads' log-sum-exps (a warp per head), then a
 // thread per token adds the heads in order, so that results do not depend on
 // timing.  8 x 20K tokens of 8 KV heads, 4 query heads each (21 MB of scores, 10
-// of weights): 17 us with cold caches, 11 in a call, where the scores are in L2.
+// of weights): 17 us with cold caches, 10 in a call, where the scores are in L2.
 constexpr int kMorePer = 8;
 struct WeightsParams {
   const float* scores;
