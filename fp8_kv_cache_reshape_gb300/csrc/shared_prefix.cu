@@ -11,6 +11,7 @@
 #include "kvq_device.cuh"
 #include "kvq_host.h"
 #include "kvq_plan.cuh"
+#include "kvq_prefix_smem.h"
 #include "kvq_tcgen05.cuh"
 
 namespace kvq {
@@ -18,8 +19,8 @@ namespace kvq {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int TR = 128;         // query rows per tile
-constexpr int TK = 128;         // keys per tile (8 pages)
+constexpr int TR = kTileRows;   // query rows per tile
+constexpr int TK = kTileKeys;   // keys per tile (8 pages)
 constexpr int UNIT = 2 * TR;    // rows of a unit: two tiles over the same keys
 
 struct SharedParams {
@@ -302,7 +303,7 @@ KVQ_DEVINL void write_parts(const SharedParams& p, int lane, int w, int n) {
 // A stream's MMAs, issued by one thread, complete in order, and each S_j commit
 // covers the P.V issued before it: its softmax sees O complete when S_j arrives,
 // and its P_j may lie over S_j.
-constexpr int kSoftWarps = 8;           // 0-3 stream 0, 4-7 stream 1
+static_assert(kSoftWarps == 8, "warps 0-3 stream 0, 4-7 stream 1");
 constexpr int kConvWarps = 4;           // 8-11
 constexpr int W_K = 12, W_V = 13, W_MMA = 14;  // an issuing warp per stream: 14, 15
 constexpr int kPrefixThreads = 512;
@@ -314,26 +315,7 @@ constexpr float kSlack = 7.f;
 constexpr int kInfo = 16;  // tile flags kept: more than the tiles in flight
 
 template <int D>
-struct Geo {
-  static constexpr int NST = D == 128 ? 3 : 6;      // K stages, V stages
-  static constexpr int TILE = TK * D;               // bytes of a K or V tile
-  static constexpr int PAGE = kPage * D;
-  static constexpr int QT = TR * D;                 // one term of a query tile
-  static constexpr int OFF_Q = 0;                   // [stream][term]
-  static constexpr int OFF_K = OFF_Q + 4 * QT;
-  static constexpr int OFF_V = OFF_K + NST * TILE;
-  static constexpr int OFF_VH = OFF_V + NST * TILE;  // two f16 V tiles
-  // output staging: 32 rows of 32 floats per softmax warp, rows 16 bytes off
-  // each other's banks.  Head dim 128: in the warp's quarter of its stream's Q
-  // tile, whose MMAs are done by then; head dim 64, whose Q is half that: apart.
-  static constexpr int PITCH = 36;
-  static constexpr int STAGE_WARP = D == 128 ? 2 * QT / 4 : 32 * PITCH * 4;
-  static constexpr int OFF_STAGE = D == 128 ? OFF_Q : OFF_VH + 2 * 2 * TILE;
-  static_assert(32 * PITCH * 4 <= STAGE_WARP, "staging");
-  static constexpr int OFF_BAR = OFF_VH + 2 * 2 * TILE + (D == 128 ? 0 : kSoftWarps * STAGE_WARP);
-  static constexpr int SMEM = OFF_BAR + 1024 + 1024;  // + alignment slack
-  static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
-};
+using Geo = PrefixSmem<D>;
 template <int NST>
 struct Bars {
   uint64_t k_full[NST], k_empty[NST], v_full[NST], v_empty[NST];
@@ -352,7 +334,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   using G = Geo<D>;
   constexpr int NST = G::NST;
   using B = Bars<NST>;
-  static_assert(sizeof(B) <= 1024, "barrier block");
+  static_assert(sizeof(B) <= G::BAR_BYTES, "barrier block");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023) & ~1023u) - raw);
@@ -705,7 +687,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
               lo[e] = f32x2_to_e4m3x2(a0 - b0.x, a1 - b0.y) | (f32x2_to_e4m3x2(a2 - b1.x, a3 - b1.y) << 16);
             }
             const int c8 = c4 + 4 * k, c = c8 >> 1;  // piece, 16-byte chunk of the row
-            uint8_t* qs = smem + G::OFF_Q + x * 2 * G::QT + rq * D + ((D == 128 ? c ^ (rq & 7) : c ^ ((rq >> 1) & 3)) << 4) + (c8 & 1) * 8;
+            uint8_t* qs = smem + G::q_row(x, 0, rq) + ((D == 128 ? c ^ (rq & 7) : c ^ ((rq >> 1) & 3)) << 4) + (c8 & 1) * 8;
             *reinterpret_cast<uint2*>(qs) = make_uint2(hi[0], hi[1]);
             *reinterpret_cast<uint2*>(qs + G::QT) = make_uint2(lo[0], lo[1]);
 #pragma unroll
@@ -800,8 +782,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
         const float f = l > 0.f ? vscale / l : 0.f;
         // A lane holds a row; through shared memory the rows leave as 128-byte
         // runs instead of 16-byte ones (which cost 9,000 cycles per segment).
-        constexpr int PITCH = G::PITCH;
-        float* stage = reinterpret_cast<float*>(smem + G::OFF_STAGE + warp * G::STAGE_WARP);
+        auto stage = [&](int rr, int col) {  // row of the warp, dimension of the 32
+          return reinterpret_cast<float4*>(smem + G::stage_row(x, quarter, rr) + col * 4);
+        };
         const int nrow = min(32, s.rows - (pair ? x * TR : 0) - quarter * 32);  // live rows of the warp
         float* dst = p.o_part + (idx - lane) * D;
         if (warp_live) {
@@ -811,7 +794,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             tmem_ld32(o_t + 32 * c, o);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(stage + lane * PITCH + 4 * i) =
+              *stage(lane, 4 * i) =
                   make_float4(__uint_as_float(o[4 * i]) * f, __uint_as_float(o[4 * i + 1]) * f,
                               __uint_as_float(o[4 * i + 2]) * f, __uint_as_float(o[4 * i + 3]) * f);
             __syncwarp();
@@ -819,8 +802,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
             for (int i = 0; i < 8; ++i) {
               const int rr = 4 * i + (lane >> 3);
               if (rr < nrow)
-                *reinterpret_cast<float4*>(dst + rr * D + 32 * c + 4 * (lane & 7)) =
-                    *reinterpret_cast<const float4*>(stage + rr * PITCH + 4 * (lane & 7));
+                *reinterpret_cast<float4*>(dst + rr * D + 32 * c + 4 * (lane & 7)) = *stage(rr, 4 * (lane & 7));
             }
             __syncwarp();
           }
