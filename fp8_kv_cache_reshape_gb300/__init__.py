@@ -452,11 +452,12 @@ def _device_ptrs(*tensors):
 
 
 def _workspace(need, like, stream):
-    """A workspace for one call; kept from reuse until the call's stream is past it."""
-    w = torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-    if stream is not None:
-        w.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
-    return w
+    """A workspace for one call, from the memory of the call's own stream: work
+    queued on another one neither still uses it nor reuses it while the call runs."""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
 
 
 def kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix_blocks, max_blocks):
