@@ -266,6 +266,15 @@ def kvq_decode_workspace_size(B, Hq, Hkv, D, max_blocks, window=-1, num_splits=0
     return lib.kvq_decode_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, window, num_splits)
 
 
+def _workspace(need, like, stream):
+    """A workspace for one call, from the memory of the call's own stream: work
+    queued on another one neither still uses it nor reuses it while the call runs."""
+    if stream is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream):
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+
+
 def kvq_paged_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out,
                                num_blocks=None, sm_scale=None, window=-1, cache_dtype="fp8_e4m3",
                                num_splits=0, workspace=None, dev_status=None, stream=None, accumulation=None):
@@ -287,7 +296,7 @@ def kvq_paged_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_tabl
         sm_scale = 1.0 / math.sqrt(D)
     need = kvq_decode_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q, stream)
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
             _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), window, dt,
             num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
@@ -319,7 +328,7 @@ def kvq_paged_decode_attention_append(q, k_new, v_new, slot_new, k_cache, v_cach
         raise ValueError("slot_new must be int64 [B]")
     need = kvq_decode_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q, stream)
     _check(lib.kvq_paged_decode_attention_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
         _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
@@ -341,7 +350,7 @@ def kvq_paged_decode_attention_per_token(q, k_cache, v_cache, block_table, seq_l
         sm_scale = 1.0 / math.sqrt(D)
     need = kvq_decode_workspace_size(B, Hq, Hkv, D, max_blocks, window, num_splits)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _workspace(need, q, stream)
     _check(lib.kvq_paged_decode_attention_per_token(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
         _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), window,
@@ -449,15 +458,6 @@ def _device_ptrs(*tensors):
             raise ValueError("libkvq takes contiguous tensors only")
         out.append(t.data_ptr())
     return out
-
-
-def _workspace(need, like, stream):
-    """A workspace for one call, from the memory of the call's own stream: work
-    queued on another one neither still uses it nor reuses it while the call runs."""
-    if stream is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream):
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
 
 
 def kvq_shared_prefix_workspace_size(B, G, Hq, Hkv, D, max_prefix_blocks, max_blocks):

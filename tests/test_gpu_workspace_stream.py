@@ -41,7 +41,29 @@ def _weights(k):
             lambda outs, **kw: k.kvq_paged_decode_attention_weights(*args, *outs, **kw))
 
 
-@pytest.mark.parametrize("make", [_shared, _weights])
+def _plain(k):
+    pool, q, tables, width = _decode_inputs()
+    args = (q, *pool.device(), *pool.device_scales(), *tables)
+    return (k.kvq_decode_workspace_size(3, 8, 2, 128, width), [torch.zeros_like(q)],
+            lambda outs, **kw: k.kvq_paged_decode_attention(*args, *outs, **kw))
+
+
+def _append(k):
+    pool, q, tables, width = _decode_inputs()
+    new, slots = torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda"), torch.full((3,), -1, device="cuda")  # no slot: nothing written
+    args = (q, new, new, slots, *pool.device(), *pool.device_scales(), *tables)
+    return (k.kvq_decode_workspace_size(3, 8, 2, 128, width), [torch.zeros_like(q)],
+            lambda outs, **kw: k.kvq_paged_decode_attention_append(*args, *outs, **kw))
+
+
+def _per_token(k):
+    pool, q, tables, width = _decode_inputs(per_token=True)
+    args = (q, *pool.device(), *tables)
+    return (k.kvq_decode_workspace_size(3, 8, 2, 128, width), [torch.zeros_like(q)],
+            lambda outs, **kw: k.kvq_paged_decode_attention_per_token(*args, *outs, **kw))
+
+
+@pytest.mark.parametrize("make", [_shared, _weights, _plain, _append, _per_token])
 def test_memory_given_back_by_another_stream_is_left_alone(make):
     k = _k()
     size, outs, call = make(k)
