@@ -157,6 +157,8 @@ KVQ_DEVINL void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" :::
 // this grid's completion in grid_dependency_wait()).
 KVQ_DEVINL void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+KVQ_DEVINL void fence_acq_rel_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 // max(a, b, c) in one instruction (sm_100 and later); NaN inputs are ignored as by fmaxf.
 KVQ_DEVINL float fmax3(float a, float b, float c) {
   float d;

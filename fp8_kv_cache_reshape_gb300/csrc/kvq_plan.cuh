@@ -11,7 +11,8 @@ constexpr int kWidePages = 4;  // least pages per slot, where that leaves a slot
 constexpr int kPartialWarps = 4;  // partials of a segment: one per consumer warp of the decode kernel
 
 // seq_lens[b] clamped to the block table; spec: read before the preceding
-// kernel has completed (a hint) or beside it (L2 only: no stale line).
+// kernel has completed (a hint) or beside it (L2 only: no stale line); otherwise
+// after a wait or a fence of the reader's own.
 KVQ_DEVINL int wide_len(const int32_t* seq_lens, int b, int max_blocks, bool spec) {
   const int L = spec ? ld_l2only_s32(seq_lens + b) : seq_lens[b];
   return min(max(L, 0), max_blocks * kPage);

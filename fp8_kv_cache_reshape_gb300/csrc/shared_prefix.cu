@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
   const uint32_t tmem = bars->tmem_base;  // S0 | S1 (128 columns each) | O0 | O1 (D each)
   // Whichever of this grid and the own tokens' is launched first waits for what
   // precedes the call; the other starts after that, runs beside it and waits
-  // for it only before it ends.
+  // for it only before it ends (and so reads what precedes the call past L1).
   if (p.first) grid_dependency_wait();
   grid_launch_dependents();
 
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
     const uint32_t t_lane = static_cast<uint32_t>(quarter * 32) << 16;
     const int row = quarter * 32 + lane;     // of the stream's tile
     const uint32_t s_t = tmem + t_lane + x * TK, o_t = tmem + t_lane + 2 * TK + x * D;
-    const float kscale_raw = __ldg(p.k_scale + kvh), vscale = __ldg(p.v_scale + kvh);  // used after the walk's loads
+    const float kscale_raw = __ldcg(p.k_scale + kvh), vscale = __ldcg(p.v_scale + kvh);  // used after the walk's loads
     SegWalk walk(p, slot, lane, false);
     const float kscale = __fmul_rn(__fmul_rn(kscale_raw, p.sm_scale), kLog2e);
     uint32_t tile0 = 0, ns = 0, nseg = 0;  // tiles of earlier segments; S tiles seen; O sums taken

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from oracle import serving
+from oracle.kv_cache import FP8
 from tests.serving_testlib import P, Pool, assert_output, i32
 from tests.test_serving_segments import SEGMENTS, most_segments, starts_of
 
@@ -41,3 +42,63 @@ def test_matches_oracle_and_repeats(name):
                                             1 / np.sqrt(dim), dtype)
     assert_output(outs[0], ref, mag)
     assert all(torch.equal(o.view(torch.int16), outs[0].view(torch.int16)) for o in outs[1:])
+
+
+@pytest.mark.parametrize("prefixes", [[1100, 700], [200, 100]], ids=["prefix_first", "own_first"])
+def test_inputs_written_by_the_preceding_kernels(prefixes):
+    """The call's inputs change in place between calls, in stream order: each
+    call sees its own, whichever of its grids goes first, eager and captured."""
+    k = _k()
+    heads, group, dim, B = 40, 8, 128, 40
+    pool = Pool(sum(-(-n // P) for n in prefixes) + 4 * B + 3, heads, dim, FP8, 11)
+    pre, mine = pool.table(prefixes), pool.table([64] * B)
+    kd, vd = pool.device()
+    ks, vs = pool.device_scales()
+    sets = []
+    for i in range(4):
+        q, qv = pool.query(B, group)
+        own = [(29 * j + 13 * i) % 65 for j in range(B)]
+        sets.append(((q, ks * (1 + 0.25 * i), vs * (1 + 0.5 * i), i32(pre[::-1].copy() if i % 2 else pre),
+                      i32([(min(prefixes) - 37 * i), min(prefixes) - i]), i32([0, 20 + i, 39 - i]), i32(np.roll(mine, i, 0)), i32(own)),
+                     qv, own))
+
+    def call(a, out, ws):
+        q, s, t, *tables = a
+        k.kvq_paged_decode_attention_shared_prefix(q, kd, vd, s, t, *tables, out, workspace=ws)
+
+    ws = torch.empty(k.kvq_shared_prefix_workspace_size(B, 2, heads * group, heads, dim, pre.shape[1], mine.shape[1]),
+                     dtype=torch.uint8, device="cuda")
+    alone = [torch.zeros_like(sets[0][0][0]) for _ in sets]
+    for (a, _, _), o in zip(sets, alone):
+        call(a, o, ws)
+        torch.cuda.synchronize()
+    for i in (0, 3):
+        a, qv, own = sets[i]
+        table, plens, starts, rows = (t.cpu().numpy() for t in a[3:7])
+        ref, mag = serving.shared_prefix_decode(qv, pool.k, pool.v, a[1].cpu().numpy(), a[2].cpu().numpy(), table, plens, starts,
+                                                rows, own, 1 / np.sqrt(dim), FP8)
+        assert_output(alone[i], ref, mag)
+    now = [torch.zeros_like(t) for t in sets[0][0]]
+    outs = [torch.zeros_like(o) for o in alone]
+
+    def steps():
+        for (a, _, _), o in zip(sets, outs):
+            for dst, src in zip(now, a):
+                dst.copy_(src)
+            call(now, o, ws)
+
+    def check():
+        torch.cuda.synchronize()
+        assert all(torch.equal(a.view(torch.int16), b.view(torch.int16)) for a, b in zip(alone, outs))
+        for o in outs:
+            o.zero_()
+
+    for _ in range(3):
+        steps()
+        check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        steps()
+    for _ in range(3):
+        g.replay()
+        check()
