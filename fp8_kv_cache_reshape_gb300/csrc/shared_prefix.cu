@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) prefix_kernel(const __grid_
           const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
           const float inv = __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
           const float mine = __shfl_sync(0xffffffffu, inv, (lane & 7) * 4);
-          if ((lane >> 3) == i) coef = kscale * mine;
+          if ((lane >> 3) == i) coef = fmaxf(kscale * mine, FLT_MIN);  // not 0: times a dead key's -inf
 #pragma unroll
           for (int k = 0; k < NP; ++k) {
             const uint32_t w[4] = {u[0][k].x, u[0][k].y, u[0][k].z, u[0][k].w};

@@ -102,3 +102,25 @@ def test_inputs_written_by_the_preceding_kernels(prefixes):
     for _ in range(3):
         g.replay()
         check()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_scores_below_the_smallest_float(dim):
+    """Queries and a K scale so small that no score differs from 0: every key
+    counts alike, and those behind the prefix's end still count nothing."""
+    k = _k()
+    prefixes, own = [300], [20, 0, 5]
+    pool = Pool(30, 1, dim, FP8, 13)
+    pre, mine = pool.table(prefixes), pool.table(own)
+    pool.k_scale[:] = 2.0 ** -45
+    q, _ = pool.query(3, 4)
+    q = q * 2.0 ** -110
+    kd, vd = pool.device()
+    out, st = torch.empty_like(q), torch.zeros(1, dtype=torch.int32, device="cuda")
+    k.kvq_paged_decode_attention_shared_prefix(q, kd, vd, *pool.device_scales(), i32(pre), i32(prefixes), i32([0, 3]), i32(mine),
+                                               i32(own), out, dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, mag = serving.shared_prefix_decode(q.double().cpu().numpy(), pool.k, pool.v, pool.k_scale, pool.v_scale, pre, prefixes,
+                                            [0, 3], mine, own, 1 / np.sqrt(dim), FP8)
+    assert_output(out, ref, mag)
