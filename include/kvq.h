@@ -412,22 +412,31 @@ kvq_status_t kvq_paged_decode_attention_per_token(const void* q, const void* k_c
  *  Hq / Hkv <= 8; G >= 1, max_prefix_blocks >= 1, max_blocks >= 1.
  *  workspace     kvq_shared_prefix_workspace_size(...) bytes, 16-byte aligned;
  *                contents on entry are ignored; calls sharing it must not
- *                overlap.
+ *                overlap.  Mostly the prefix's partials: per KV head 256 rows of
+ *                D + 1 floats for each of (SMs / Hkv + B * (Hq / Hkv) / 256 + G)
+ *                parts of a unit (below), however few rows the unit has (32 query
+ *                and 8 KV heads of 128 on a GB300: 308 MB for 1,024 sequences in
+ *                256 groups, 578 MB in 512).
  *  Three kernels: the prefix on tensor cores (tcgen05), the own tokens on the
  *  split-KV decode's, and their merge by log-sum-exps in FP32.  The first two
  *  run beside each other.  The work split is a function of the lengths and
  *  groups alone: results are deterministic.  A unit of work (up to 256 query
  *  rows of a KV head over the prefix) takes about 10 us to start and end, so
  *  that for few sequences or short prefixes kvq_paged_decode_attention with
- *  the prefix's pages in each block table is faster (on a GB300, 8 KV heads of
- *  128: up to about 8 sequences after 8K tokens, 16 after 2K, 32 after 1K).
+ *  the prefix's pages in each block table is faster: on a GB300, one group, 8 KV
+ *  heads of 128, 4 query heads each, up to about 6 sequences after 8K tokens, 16
+ *  after 2K, 48 after 1K.  Every group has units of its own, so many small groups
+ *  with short prefixes are slower too (256 sequences in 64 groups after up to 256
+ *  tokens by 8%; 1,024 in 512 groups after up to 512, 2 KV heads of 64, 2.2
+ *  times).
  *  Declared rounding: own tokens as for kvq_paged_decode_attention.  Prefix --
  *  per query head, sigma = 2^(7 - floor(log2 max_d |q_d|)) and the query enters
  *  as the sum of two E4M3 terms, hi = e4m3(q * sigma) and lo = e4m3(q * sigma -
  *  hi) (exact but for elements under 2^-9 of the head's maximum, which are off
  *  by at most 2^-17 of it); scores are FP32 sums of exact products with the
  *  cache's codes; probabilities 2^(s2 - M + 8), M at most 7 below the running
- *  maximum of the base-2 scores, are rounded to float16 (11 significant bits)
+ *  maximum of the base-2 scores, are rounded to float16 (11 significant bits;
+ *  those below 2^-22 of 2^M are float16 subnormals, off by up to 2^-33 of 2^M)
  *  and multiplied with the codes converted to float16 (exact), FP32 sums; the
  *  row sum adds them unrounded.  The output is rounded to bf16 once, at the end.
  */
@@ -463,6 +472,9 @@ kvq_status_t kvq_paged_decode_attention_shared_prefix(const void* q, const void*
  *                  partials and float32 scores [B][Hkv][max_blocks * P][Hq /
  *                  Hkv rounded up to even] (in L2 between the two kernels of a
  *                  call, where they fit, and discarded from it).
+ *  The last kernel's grid follows max_blocks, not the lengths: every 512 to 8,192
+ *  tokens of that width are a CTA that merges its heads' log-sum-exps, so a block
+ *  table much wider than its sequences costs time.
  *  Other arguments, caches and the declared rounding as for
  *  kvq_paged_decode_attention (and _per_token); the scores and sums behind
  *  the weights are float32, and heads are added in order (no atomics), so
