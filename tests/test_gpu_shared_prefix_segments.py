@@ -124,3 +124,25 @@ def test_scores_below_the_smallest_float(dim):
     ref, mag = serving.shared_prefix_decode(q.double().cpu().numpy(), pool.k, pool.v, pool.k_scale, pool.v_scale, pre, prefixes,
                                             [0, 3], mine, own, 1 / np.sqrt(dim), FP8)
     assert_output(out, ref, mag)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls with several segments per CTA on two streams, each with its own
+    workspace, beside each other: the bits of each alone."""
+    k = _k()
+    calls = []
+    for seed, (prefixes, sizes, heads, group, dim) in enumerate([([700, 900], [10, 32], 80, 4, 128), ([1500], [40], 8, 4, 128)]):
+        own = [(31 * i) % 90 for i in range(sum(sizes))]
+        pool = Pool(sum(-(-n // P) for n in prefixes + own) + 3, heads, dim, FP8, 17 + seed)
+        pre, mine = pool.table(prefixes), pool.table(own)
+        q, _ = pool.query(len(own), group)
+        args = (q, *pool.device(), *pool.device_scales(), i32(pre), i32(prefixes), i32(starts_of(sizes)), i32(mine), i32(own))
+        alone = k.kvq_paged_decode_attention_shared_prefix(*args, torch.zeros_like(q))
+        calls.append((args, alone, [torch.zeros_like(q) for _ in range(20)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for i in range(20):
+        for args, _, outs, side in calls:
+            k.kvq_paged_decode_attention_shared_prefix(*args, outs[i], stream=side)
+    torch.cuda.synchronize()
+    for _, alone, outs, _ in calls:
+        assert all(torch.equal(alone.view(torch.int16), o.view(torch.int16)) for o in outs)
