@@ -31,6 +31,7 @@ KVQ_ERR_DEVICE_FAULT = 4
 KVQ_DTYPE_FP8_E4M3 = 0
 KVQ_DTYPE_BF16 = 1
 KVQ_DTYPE_FP8_E5M2 = 2
+KVQ_DTYPE_FP4_E2M1 = 3
 
 KVQ_ACC_TWO_LEVEL = 0
 KVQ_ACC_SINGLE_LEVEL = 1
@@ -41,6 +42,7 @@ KVQ_DEV_BAD_SEQLEN = 0x4
 KVQ_DEV_TIMEOUT = 0x8
 KVQ_DEV_BAD_QROWS = 0x10
 KVQ_DEV_BAD_GROUP = 0x20
+KVQ_DEV_BAD_AXIS = 0x40
 
 PAGE = 16
 
@@ -113,6 +115,29 @@ lib.kvq_evict_tokens.argtypes = [_p, _i64, _p, _p, _p, _p, _p, _p, _p, _i64, _p,
                                  _i, _i, _i, _p, _p]
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [("positions", _p), ("positions_stride", _i64), ("inv_freq", _p), ("pair_axis", _p), ("num_axes", _i),
+                ("rot_dim", _i), ("interleaved", _i), ("scale", _f)]
+
+
+class _HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", _p), ("k_weight", _p), ("eps", _f)]
+
+
+_rot, _norm = ctypes.POINTER(_Rotary), ctypes.POINTER(_HeadNorm)
+lib.kvq_qk_norm_rope.restype = _i
+lib.kvq_qk_norm_rope.argtypes = [_p, _i64, _p, _i64, _norm, _rot, _p, _i64, _p, _i64, _i, _i, _i, _i, _p, _p]
+lib.kvq_rope_and_cache.restype = _i
+lib.kvq_rope_and_cache.argtypes = [_p, _i64, _p, _i64, _p, _i64, _norm, _rot, _p, _p, _p, _p, _p, _p, _i64, _p, _p, _i, _i,
+                                   _i, _i, _i, _i64, _i, _i, _p, _p]
+lib.kvq_gather_cache.restype = _i
+lib.kvq_gather_cache.argtypes = [_p] * 7 + [_i, _i, _i, _i, _i64, _i, _i, _p, _p]
+lib.kvq_decode_fp4_workspace_size.restype = _sz
+lib.kvq_decode_fp4_workspace_size.argtypes = [_i] * 6
+lib.kvq_paged_decode_attention_fp4.restype = _i
+lib.kvq_paged_decode_attention_fp4.argtypes = [_p] * 8 + [_i] * 6 + [_i64, _f, _i, _p, _sz, _p, _p]
+
+
 class KvqError(RuntimeError):
     def __init__(self, status: int, where: str):
         msg = lib.kvq_last_error_string().decode(errors="replace")
@@ -157,6 +182,8 @@ def _dtype_code(cache_dtype: str) -> int:
         return KVQ_DTYPE_BF16
     if cache_dtype in ("fp8_e5m2", KVQ_DTYPE_FP8_E5M2):
         return KVQ_DTYPE_FP8_E5M2
+    if cache_dtype in ("fp4", "fp4_e2m1", KVQ_DTYPE_FP4_E2M1):
+        return KVQ_DTYPE_FP4_E2M1
     raise ValueError(f"unknown cache dtype {cache_dtype!r}")
 
 
@@ -182,18 +209,28 @@ def kvq_debug_set_stall_ns(ns: int):
 SCALE_TAIL_BYTES = 2 * PAGE * 4
 
 
+def _page_bytes(head_dim, dt):
+    """Bytes of a K page: FP4 codes and their block scales, FP8 codes or bf16."""
+    if dt == KVQ_DTYPE_FP4_E2M1:
+        return PAGE * (head_dim // 2 + head_dim // 16)
+    return PAGE * head_dim * (2 if dt == KVQ_DTYPE_BF16 else 1)
+
+
 def alloc_kv_cache(num_blocks: int, kv_heads: int, head_dim: int, cache_dtype="fp8_e4m3",
                    device="cuda", fill=None, per_token=False, paired=False):
     """Allocate (k_cache, v_cache) as uint8 tensors in the library's paged
     format ([num_blocks][Hkv][P][D] and [num_blocks][Hkv][D][P] elements).
     per_token: each V page also carries its scale tail (FP8 only).
+    "fp4_e2m1": 4-bit codes and a block scale per 16 dims (head dims 64, 128).
     paired: one allocation [num_blocks][Hkv][K page | V page]; k_cache is it
     and v_cache a flat view starting one K page in (the library recognizes
     the layout from the pointers and moves each pair with one copy)."""
-    esz = 2 if _dtype_code(cache_dtype) == KVQ_DTYPE_BF16 else 1
-    if per_token and esz != 1:
+    dt = _dtype_code(cache_dtype)
+    if per_token and dt not in (KVQ_DTYPE_FP8_E4M3, KVQ_DTYPE_FP8_E5M2):
         raise ValueError("per-token scales need an FP8 cache")
-    kpage = PAGE * head_dim * esz
+    if dt == KVQ_DTYPE_FP4_E2M1 and head_dim not in (64, 128):
+        raise ValueError("an FP4 cache has head dim 64 or 128")
+    kpage = _page_bytes(head_dim, dt)
     vpage = kpage + (SCALE_TAIL_BYTES if per_token else 0)
     make = (lambda shape: torch.empty(shape, dtype=torch.uint8, device=device)) if fill is None else \
         (lambda shape: torch.full(shape, fill, dtype=torch.uint8, device=device))
@@ -220,8 +257,9 @@ def kvq_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_
     """Quantize (or copy) new tokens k, v (bf16 [T][Hkv][D]) into the cache."""
     T, Hkv, D = k.shape
     dt = _dtype_code(cache_dtype)
-    esz = 2 if dt == KVQ_DTYPE_BF16 else 1
-    num_blocks = _num_blocks(k_cache, v_cache, Hkv, PAGE * D * esz)
+    num_blocks = _num_blocks(k_cache, v_cache, Hkv, _page_bytes(D, dt))
+    if dt == KVQ_DTYPE_FP4_E2M1:
+        _check_cache(k_cache, v_cache, Hkv, D, dt, False, num_blocks)
     _check(lib.kvq_reshape_and_cache(_ptr(k), _ptr(v), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
                                      _ptr(k_scale), _ptr(v_scale), T, Hkv, D, PAGE, num_blocks, dt,
                                      _ptr(dev_status), _stream(stream)), "kvq_reshape_and_cache")
@@ -418,7 +456,7 @@ def _check_tensor(t, dtype, shape, name):
 def _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks):
     """The caches' bytes against what the head dim and format say (a wrong one
     would read and write past a page); returns the block count."""
-    kpage = PAGE * D * (2 if dt == KVQ_DTYPE_BF16 else 1)
+    kpage = _page_bytes(D, dt)
     vpage = kpage + (SCALE_TAIL_BYTES if per_token else 0)
     nb = k_cache.shape[0]
     if v_cache.data_ptr() == k_cache.data_ptr() + kpage:
@@ -559,3 +597,185 @@ def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens
         PAGE, max_blocks, max_dst, num_blocks, min(sink, 2**31 - 1), min(recent, 2**31 - 1), dt, 1 if per_token else 0,
         status, _stream(stream)), "kvq_evict_tokens")
     return dst_seq_lens
+
+
+def _rows(t, heads, D, name):
+    """Tokens' heads (bf16 [T][heads][D]) with any stride between tokens:
+    that stride in elements."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be bf16 [T][{heads}][{D}], got {t.dtype} {list(t.shape)}")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: a token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def _device_ptr(t):
+    """_device_ptrs for a tensor whose strides are checked by its user."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("libkvq takes CUDA tensors only")
+    current = torch.cuda.current_device()
+    if t.get_device() != current:
+        raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one (cuda:{current})")
+    return t.data_ptr()
+
+
+def _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D):
+    """The shapes of the rotation's and norms' tensors."""
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _check_tensor(t, torch.bfloat16, (D,), name)
+    if positions is None:
+        if inv_freq is not None or pair_axis is not None:
+            raise ValueError("inv_freq and pair_axis need positions")
+        return
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _check_tensor(positions, torch.int64, (axes, T) if positions.dim() == 2 else (T,), "positions")
+    if positions.stride(-1) != 1 and T > 1:
+        raise ValueError("positions: an axis's tokens must be contiguous")
+    if inv_freq is None:
+        raise ValueError("positions need inv_freq")
+    _check_tensor(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+    if pair_axis is not None:
+        _check_tensor(pair_axis, torch.int32, (inv_freq.numel(),), "pair_axis")
+    elif axes > 1:
+        raise ValueError("several position axes need pair_axis")
+
+
+def _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps):
+    """kvq_head_norm and kvq_rotary of checked tensors (None: no norm, no rotation)."""
+    norm = rotary = None
+    if q_weight is not None or k_weight is not None:
+        norm = _HeadNorm(*(None if t is None else _device_ptrs(t)[0] for t in (q_weight, k_weight)), float(eps))
+    if positions is not None:
+        axes, T = positions.shape[0] if positions.dim() == 2 else 1, positions.shape[-1]
+        stride = positions.stride(0) if axes > 1 else T
+        freq, axis = _device_ptrs(inv_freq, pair_axis)
+        rotary = _Rotary(_device_ptr(positions), stride, freq, axis, axes, 2 * inv_freq.numel(), 1 if interleaved else 0,
+                         float(rope_scale))
+    return norm, rotary
+
+
+def kvq_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, pair_axis=None,
+                     interleaved=False, rope_scale=1.0, dev_status=None, stream=None):
+    """Head norms and rotary positions of queries and keys in one pass.
+
+    q, k: bf16 [T][heads][D] with any stride between tokens (a slice of the
+    projection's output), either may be None; q_out, k_out: alike, and may be q
+    and k.  positions: int64 [T], or [axes][T] with pair_axis (int32 [pairs])
+    naming each pair's axis; None: no rotation.  inv_freq: float32 [pairs],
+    2 * pairs dims of each head are turned, pairs of dims pairs apart or
+    (interleaved) neighbours.  q_weight, k_weight: bf16 [D] norm weights, None:
+    no norm."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    T, _, D = x.shape
+    heads, strides = [], []
+    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
+        heads.append(0 if t is None else t.shape[1])
+        if t is None:
+            strides.append((0, 0))
+            continue
+        strides.append((_rows(t, heads[-1], D, name), 0 if out is None else _rows(out, heads[-1], D, name + "_out")))
+        if t.shape[0] != T or out is None or out.shape[0] != T:
+            raise ValueError(f"{name} and {name}_out must have the same tokens, and q's")
+    _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
+    norm, rotary = _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps)
+    (qs, qos), (ks, kos) = strides
+    _check(lib.kvq_qk_norm_rope(_device_ptr(q), qs, _device_ptr(k), ks, norm, rotary, _device_ptr(None if q is None else q_out),
+                                qos, _device_ptr(None if k is None else k_out), kos, T, *heads, D,
+                                None if dev_status is None else _device_ptrs(dev_status)[0], _stream(stream)),
+           "kvq_qk_norm_rope")
+    return q_out, k_out
+
+
+def kvq_rope_and_cache(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_cache, k_scale=None, v_scale=None, q_out=None,
+                       q8=None, q_scale=None, q_weight=None, k_weight=None, eps=1e-6, pair_axis=None, interleaved=False,
+                       rope_scale=1.0, num_blocks=None, cache_dtype="fp8_e4m3", per_token=False, dev_status=None,
+                       stream=None):
+    """Head norms and rotary positions of q and k as kvq_qk_norm_rope, then k
+    and v into the cache (any dtype of alloc_kv_cache, per_token: dynamic
+    scales) and q out as bf16 (q_out, may be q) or E4M3 codes (q8 with q_scale)
+    or both, in one launch.  q may be None."""
+    T, Hkv, D = k.shape
+    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
+    if v.shape[0] != T:
+        raise ValueError("v must have k's tokens")
+    Hq = qs = qos = 0
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _rows(q, Hq, D, "q")
+        if q.shape[0] != T:
+            raise ValueError("q must have k's tokens")
+        if q_out is None and q8 is None:
+            raise ValueError("q needs q_out or q8")
+        if q_out is not None:
+            qos = _rows(q_out, Hq, D, "q_out")
+            if q_out.shape[0] != T:
+                raise ValueError("q_out must have q's tokens")
+        if q8 is not None:
+            _check_tensor(q8, torch.uint8, (T, Hq, D), "q8")
+            if q_scale is None or q_scale.dtype is not torch.float32 or q_scale.numel() != 1:
+                raise ValueError("q8 needs q_scale, float32 [1]")
+    elif q_out is not None or q8 is not None:
+        raise ValueError("q_out and q8 need q")
+    _check_tensor(slot_mapping, torch.int64, (T,), "slot_mapping")
+    dt = _dtype_code(cache_dtype)
+    _check_scales(k_scale, v_scale, Hkv)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
+    _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
+    slots, kc, vc, ksc, vsc, q8p, qsc, status = _device_ptrs(slot_mapping, k_cache, v_cache, k_scale, v_scale, q8, q_scale,
+                                                             dev_status)
+    norm, rotary = _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps)
+    _check(lib.kvq_rope_and_cache(
+        _device_ptr(q), qs, _device_ptr(k), ks, _device_ptr(v), vs, norm, rotary, slots, kc, vc, ksc, vsc,
+        _device_ptr(q_out), qos, q8p, qsc, T, Hq, Hkv, D, PAGE, num_blocks, dt, 1 if per_token else 0, status,
+        _stream(stream)), "kvq_rope_and_cache")
+    return q_out if q_out is not None else q8
+
+
+def kvq_gather_cache(slot_mapping, k_cache, v_cache, k_out, v_out, k_scale=None, v_scale=None, num_blocks=None,
+                     cache_dtype="fp8_e4m3", per_token=False, dev_status=None, stream=None):
+    """The reverse of the cache writes: the tokens in the slots slot_mapping
+    (int64 [T]) as bf16 k_out, v_out [T][Hkv][D]; rows of negative slots stay
+    as they were."""
+    T, Hkv, D = k_out.shape
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        _check_tensor(t, torch.bfloat16, (T, Hkv, D), name)
+    _check_tensor(slot_mapping, torch.int64, (T,), "slot_mapping")
+    dt = _dtype_code(cache_dtype)
+    _check_scales(k_scale, v_scale, Hkv)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
+    *ptrs, status = _device_ptrs(slot_mapping, k_cache, v_cache, k_scale, v_scale, k_out, v_out, dev_status)
+    _check(lib.kvq_gather_cache(*ptrs, T, Hkv, D, PAGE, num_blocks, dt, 1 if per_token else 0, status, _stream(stream)),
+           "kvq_gather_cache")
+    return k_out, v_out
+
+
+def kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, max_blocks):
+    return lib.kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks)
+
+
+def kvq_paged_decode_attention_fp4(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, num_blocks=None,
+                                   sm_scale=None, window=-1, workspace=None, dev_status=None, stream=None):
+    """One decode step over a 4-bit cache (alloc_kv_cache(..., "fp4_e2m1"));
+    writes out (bf16 [B][Hq][D]).  workspace: a uint8 CUDA tensor of at least
+    kvq_decode_fp4_workspace_size() bytes (allocated here when omitted)."""
+    B, Hq, D = q.shape
+    Hkv = k_cache.shape[1]
+    max_blocks = block_table.shape[1]
+    _check_tensor(q, torch.bfloat16, (B, Hq, D), "q")
+    _check_tensor(out, torch.bfloat16, (B, Hq, D), "out")
+    _check_tensor(block_table, torch.int32, (B, max_blocks), "block_table")
+    _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
+    _check_scales(k_scale, v_scale, Hkv)
+    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, KVQ_DTYPE_FP4_E2M1, False, num_blocks)
+    if workspace is None:
+        workspace = _workspace(kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, max_blocks), q, stream)
+    *ptrs, ws, status = _device_ptrs(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, dev_status)
+    _check(lib.kvq_paged_decode_attention_fp4(
+        *ptrs, B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale),
+        window, ws, workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_fp4")
+    return out

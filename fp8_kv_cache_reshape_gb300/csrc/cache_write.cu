@@ -241,9 +241,10 @@ extern "C" kvq_status_t kvq_reshape_and_cache(const void* k, const void* v, cons
   clear_error();
   if (T < 0 || Hkv < 1 || num_blocks < 1) return fail(KVQ_ERR_INVALID_ARG, "reshape_and_cache: bad sizes");
   if (P != kPage) return fail(KVQ_ERR_UNSUPPORTED, "reshape_and_cache: page size %d (only 16)", P);
-  if (cache_dtype != KVQ_DTYPE_FP8_E4M3 && cache_dtype != KVQ_DTYPE_FP8_E5M2 && cache_dtype != KVQ_DTYPE_BF16)
+  const bool fp4 = cache_dtype == KVQ_DTYPE_FP4_E2M1;
+  if (cache_dtype != KVQ_DTYPE_FP8_E4M3 && cache_dtype != KVQ_DTYPE_FP8_E5M2 && cache_dtype != KVQ_DTYPE_BF16 && !fp4)
     return fail(KVQ_ERR_INVALID_ARG, "reshape_and_cache: bad cache dtype");
-  const bool fp8 = cache_dtype != KVQ_DTYPE_BF16;
+  const bool fp8 = cache_dtype != KVQ_DTYPE_BF16 && !fp4;
   if (D != 64 && D != 128 && !(fp8 && D == 256))
     return fail(KVQ_ERR_UNSUPPORTED, "reshape_and_cache: head_dim %d (64 or 128; 256 for FP8)", D);
   if (T == 0) return KVQ_OK;
@@ -256,6 +257,8 @@ extern "C" kvq_status_t kvq_reshape_and_cache(const void* k, const void* v, cons
     return fail(KVQ_ERR_INVALID_ARG, "reshape_and_cache: pointers must be 16-byte aligned");
   if (Hkv > 65535) return fail(KVQ_ERR_UNSUPPORTED, "reshape_and_cache: too many KV heads");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (fp4)
+    return write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, T, Hkv, D, num_blocks, dev_status, s);
   dim3 grid((T + kPage - 1) / kPage, Hkv);
   const int64_t num_slots = num_blocks * kPage;
   const int64_t page_b = static_cast<int64_t>(kPage) * D * (fp8 ? 1 : 2);

@@ -1,0 +1,634 @@
+// kvq_paged_decode_attention_fp4: one decode step over a 4-bit paged cache.
+//
+// Mathematics.  Online softmax in base 2 per query head, split over the cache
+// and joined by log-sum-exps: with scores s2 = (q . k) sm_scale log2 e and any
+// stabilizer M, a piece's (M, l = sum 2^(s2 - M), O = sum 2^(s2 - M) v) joins
+// another's after scaling by 2^(M - M').  K's value is code * block scale *
+// head scale; code * block scale has at most six significant bits and is at least
+// 2^-10, so it is exact in float16 and K enters the products exactly.  V's block scale
+// belongs to a token and 16 dims: with those 16 dims as the rows of one MMA it
+// moves to the other operand, P, one multiplication for two weights instead of one
+// for every two of V's 16 x 16 values.
+//
+// Bound: memory, 9/16 byte per element of K and V.
+//
+// Layout.  A warp takes one page (16 tokens of a KV head) at a time from a
+// ring of its own in shared memory, filled by 16-byte asynchronous copies: no
+// barrier, no producer warp, nothing between warps until a piece ends.  The
+// page format is the MMA operand order (m16n8k16, tokens as the rows of K Q^T,
+// dims as the rows of V^T P^T), so that a lane reads its whole share of a page
+// with 16-byte loads: lane 4 r + c holds dims 32 c .. 32 c + 31 (at head dim
+// 128) of tokens r and r + 8 of K, and tokens 2c, 2c + 1, 2c + 8, 2c + 9 of
+// dims 2r, 2r + 1 of each 16 of V.
+#include <algorithm>
+#include <cfloat>
+
+#include "kvq_host.h"
+#include "kvq_rows.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
+constexpr int kCtasPerSm = 4;
+constexpr int kMinPart = kWarps;      // pages of a part: a page per warp
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
+constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
+#define NEG_INF __int_as_float(0xff800000)
+
+template <int D>
+struct Fp4 {
+  static constexpr int kCodes = kPage * D / 2;
+  static constexpr int kScales = kPage * D / 16;
+  static constexpr int kPageB = kCodes + kScales;
+  static constexpr int kStageB = 2 * kPageB;           // K page, V page
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kRingB = kStages * kStageB;
+  static constexpr int kSmem = kWarps * kRingB;
+  static constexpr int kTiles = D / 16;                // MMAs per page, of K and of V
+  static constexpr int kRow = D + 8;                   // floats between the queries of a warp's output in shared memory
+  static_assert(kRingB >= 8 * kRow * 4, "a warp's output takes its ring's place");
+  static_assert(kSmem <= 47 * 1024, "no more than a launch gets unasked");
+};
+
+struct Fp4Params {
+  const __nv_bfloat16* q;
+  const uint8_t *k_cache, *v_cache;
+  int64_t k_str, v_str;
+  const float *k_scale, *v_scale;
+  const int32_t *block_table, *seq_lens;
+  __nv_bfloat16* out;
+  float *o_part, *lse_part;
+  int32_t* prefix;  // [B + 1]: attended pages of the sequences before b
+  int B, Hq, Hkv, g, max_blocks;
+  int64_t num_blocks;
+  float sm_scale;
+  int window;
+  int* dev_status;
+};
+
+// Attended tokens [lo, len) of a sequence, and their pages [first, first + n).
+struct Span {
+  int lo, len, first, n;
+};
+KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report) {
+  Span s;
+  const int L = p.seq_lens[b];
+  s.len = min(max(L, 0), p.max_blocks * kPage);
+  if (report && s.len != L) set_status(p.dev_status, KVQ_DEV_BAD_SEQLEN);
+  s.lo = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
+  s.first = s.lo / kPage;
+  s.n = (s.len + kPage - 1) / kPage - s.first;
+  return s;
+}
+// Pages of a part: the stream in `parts` equal ones, but at least a page per warp.
+KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, (total + parts - 1) / parts); }
+
+KVQ_DEVINL void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+KVQ_DEVINL void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+KVQ_DEVINL void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+KVQ_DEVINL uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+KVQ_DEVINL uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+KVQ_DEVINL uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+KVQ_DEVINL uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
+  return v;
+}
+KVQ_DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// The four bytes of a word, each two E2M1 codes, as f16x2 (low nibble in the low half).
+KVQ_DEVINL void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Bytes 0 and 2 of a word.
+KVQ_DEVINL void e2m1x4_to_f16x2(uint32_t w, uint32_t& h0, uint32_t& h2) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
+      : "=r"(h0), "=r"(h2)
+      : "r"(w));
+}
+KVQ_DEVINL uint32_t both(uint32_t h, bool high) { return __byte_perm(h, h, high ? 0x3232 : 0x1010); }
+
+// A warp's state for the queries of one KV head: lane 4 r + c holds the
+// stabilizers and sums of queries 2c, 2c + 1 and, per 16 dims, the outputs
+// O[.][0], O[.][1] of dim 2r and O[.][2], O[.][3] of dim 2r + 1.
+template <int D>
+struct Attend {
+  using F = Fp4<D>;
+  uint32_t q[D / 8];  // query r, dims (D / 4) c .. + D / 4 - 1
+  float coef[2];
+  float m[2], mb[2], l[2];
+  float O[F::kTiles][4];
+
+  KVQ_DEVINL void start(const Fp4Params& p, int b, int h, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const bool live = r < p.g;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.Hq + h * p.g + (live ? r : 0)) * D +
+                                                      c * (D / 4));
+    float mx = 0.f;
+    float x[D / 32][8];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      unpack8_bf16(live ? src[i] : make_uint4(0, 0, 0, 0), x[i]);
+      mx = fmaxf(mx, amax8(x[i]));
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    int e2 = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xFF) - 127 : 0;
+    e2 = max(e2, -100);
+    const float sigma = __uint_as_float(static_cast<uint32_t>(127 + 7 - e2) << 23);
+    const float inv_sigma = __uint_as_float(static_cast<uint32_t>(127 - 7 + e2) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16x2(x[i][2 * e] * sigma, x[i][2 * e + 1] * sigma);
+    const float cf = __fmul_rn(__fmul_rn(p.k_scale[h], p.sm_scale), kLog2e);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      coef[i] = cf * __shfl_sync(0xffffffffu, inv_sigma, 8 * c + 4 * i);
+      m[i] = NEG_INF;
+      mb[i] = 0.f;
+      l[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < F::kTiles; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
+  }
+
+  // Tokens [lo, hi) of the page at shared address `page`.
+  KVQ_DEVINL void take(uint32_t page, int lo, int hi, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const bool whole = lo <= 0 && hi >= kPage;
+    // ---- scores: rows are tokens, and each lane's dims share two scales (one at D = 64) per row
+    uint32_t kw[2][D / 32], ks[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = r + 8 * i;
+      uint32_t s;
+      if constexpr (D == 128) {
+        const uint4 u = lds128(page + t * 64 + c * 16);
+        kw[i][0] = u.x;
+        kw[i][1] = u.y;
+        kw[i][2] = u.z;
+        kw[i][3] = u.w;
+        s = lds16(page + F::kCodes + t * 8 + 2 * c);
+      } else {
+        const uint2 u = lds64(page + t * 32 + c * 8);
+        kw[i][0] = u.x;
+        kw[i][1] = u.y;
+        s = lds8(page + F::kCodes + t * 4 + c);
+      }
+      uint32_t lo2, hi2;
+      e4m3x4_to_f16x2x2(s, lo2, hi2);
+      ks[i][0] = both(lo2, false);
+      ks[i][1] = both(lo2, D == 128);
+    }
+    float s[2][4] = {};
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t a[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        e2m1x8_to_f16x2(kw[i][w], a[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a[i][e] = hmul2(a[i][e], ks[i][w / 2]);
+      }
+      mma_f16(s[0], a[0][0], a[1][0], a[0][1], a[1][1], q[4 * w], q[4 * w + 1], s[0]);
+      mma_f16(s[1], a[0][2], a[1][2], a[0][3], a[1][3], q[4 * w + 2], q[4 * w + 3], s[1]);
+    }
+    // s[0][0], [1]: token r, queries 2c, 2c + 1; [2], [3]: token r + 8
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = (s[0][e] + s[1][e]) * coef[e & 1];
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = r + 8 * (e >> 1);
+        if (t < lo || t >= hi) x[e] = NEG_INF;
+      }
+    }
+    // ---- stabilizer: moved only when a score passes it by more than kLag
+    const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
+    if (__any_sync(0xffffffffu, x0 > m[0] + kLag || x1 > m[1] + kLag)) {
+      float n[2] = {x0, x1};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) n[i] = fmaxf(n[i], __shfl_xor_sync(0xffffffffu, n[i], o));
+        n[i] = fmaxf(n[i], m[i]);
+        const float alpha = m[i] == NEG_INF ? 0.f : ex2(m[i] - n[i]);
+        l[i] *= alpha;
+#pragma unroll
+        for (int d = 0; d < F::kTiles; ++d) {
+          O[d][i] *= alpha;
+          O[d][2 + i] *= alpha;
+        }
+        m[i] = n[i];
+        mb[i] = n[i] == NEG_INF ? 0.f : n[i] - kBase;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = ex2(x[e] - mb[e & 1]);
+    l[0] += x[0] + x[2];
+    l[1] += x[1] + x[3];
+    const uint32_t p0 = movmatrix_t(pack_f16x2(x[0], x[1])), p1 = movmatrix_t(pack_f16x2(x[2], x[3]));
+    // ---- outputs: rows are 16 dims that share a token's scale, which multiplies the weights
+    const uint32_t v = page + F::kPageB;
+    uint32_t keep = 0xffffffffu;  // scale bytes of masked tokens may be anything: zero
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 2 * c + (e & 1) + 8 * (e >> 1);
+        if (t < lo || t >= hi) keep &= ~(0xffu << (8 * e));
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < D / 64; ++half) {
+      const uint4 codes = lds128(v + half * 512 + lane * 16);
+      const uint4 scales = lds128(v + F::kCodes + half * 64 + c * 16);
+      const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+      const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t s0, s1;
+        e4m3x4_to_f16x2x2(sw[i] & keep, s0, s1);
+        // bytes are tokens, nibbles dims 2r and 2r + 1: bytes 0 and 2 of `even`
+        // (`odd`) are dim 2r (2r + 1) of tokens 2c, 2c + 1 and of 2c + 8, 2c + 9
+        constexpr uint32_t kLow = 0x000F000Fu;
+        const uint32_t w4 = cw[i] >> 4, w8 = cw[i] >> 8;
+        const uint32_t even = (cw[i] & kLow) | (w4 & ~kLow), odd = (w4 & kLow) | (w8 & ~kLow);
+        uint32_t a0, a1, a2, a3;
+        e2m1x4_to_f16x2(even, a0, a2);
+        e2m1x4_to_f16x2(odd, a1, a3);
+        float f[4];
+        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_f16(f, a0, a1, a2, a3, hmul2(p0, s0), hmul2(p1, s1), zero);
+        float(&o)[4] = O[half * 4 + i];
+        const float2 u = fadd2(make_float2(o[0], o[1]), make_float2(f[0], f[1]));
+        const float2 z = fadd2(make_float2(o[2], o[3]), make_float2(f[2], f[3]));
+        o[0] = u.x;
+        o[1] = u.y;
+        o[2] = z.x;
+        o[3] = z.y;
+      }
+    }
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(const Fp4Params p) {
+  using F = Fp4<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_scan[kWarps], s_seq, s_before;
+  __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  // ---- the plan: where this CTA's part of the page stream begins
+  const int per = (p.B + kWarps * 32 - 1) / (kWarps * 32);
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += span_of(p, b, blockIdx.x == 0).n;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) incl += s_scan[w];
+    total += s_scan[w];
+  }
+  if (blockIdx.x == 0) {  // for the combine
+    int x = incl - mine;
+    for (int b = b0; b < b1; ++b) {
+      p.prefix[b] = x;
+      x += span_of(p, b, false).n;
+    }
+    if (tid == 0) p.prefix[p.B] = total;
+  }
+  const int chunk = part_pages(total * p.Hkv, gridDim.x);
+  int pos = blockIdx.x * chunk;
+  const int end = min(total * p.Hkv, pos + chunk);
+  if (pos >= end) return;
+  // the thread whose sequences hold the part's first page looks for the one
+  if (pos >= (incl - mine) * p.Hkv && pos < incl * p.Hkv) {
+    int x = incl - mine, b = b0;
+    for (;; ++b) {
+      const int n = span_of(p, b, false).n;
+      if (pos < (x + n) * p.Hkv) break;
+      x += n;
+    }
+    s_seq = b;
+    s_before = x;
+  }
+  __syncthreads();
+  int b = s_seq, before = s_before;
+
+  const uint32_t ring = smem_u32(smem) + warp * F::kRingB;
+  float* const stage = reinterpret_cast<float*>(smem + warp * F::kRingB);
+  Attend<D> at;
+
+  while (pos < end) {
+    const Span sp = span_of(p, b, false);
+    if (sp.n == 0) {  // to the next sequence with pages (there is one: pos < end)
+      do {
+        ++b;
+        const unsigned has = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1), false).n > 0);
+        b += has ? __ffs(has) - 1 : 31;
+        if (has) break;
+      } while (true);
+      continue;
+    }
+    const int within = pos - before * p.Hkv;
+    const int h = within / sp.n, pg0 = within % sp.n;
+    const int n = min(end - pos, sp.n - pg0);
+    const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks + sp.first + pg0;
+
+    // ---- this warp's pages: warp, warp + kWarps, ...
+    const int count = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
+    int ids = 0;         // block ids of 32 pages, one per lane
+    unsigned valid = 0;  // bit i: stage i holds a page
+    auto issue = [&](int i) {
+      if (i < count) {
+        if ((i & 31) == 0) {
+          const int j = i + lane;
+          ids = j < count ? table[warp + j * kWarps] : 0;
+        }
+        const int id = __shfl_sync(0xffffffffu, ids, i & 31);
+        const int st = i % F::kStages;
+        const bool ok = static_cast<unsigned>(id) < static_cast<uint64_t>(p.num_blocks);
+        valid = ok ? valid | (1u << st) : valid & ~(1u << st);
+        if (ok) {
+          const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
+          const uint8_t* k = p.k_cache + page * p.k_str;
+          const uint8_t* v = p.v_cache + page * p.v_str;
+#pragma unroll
+          for (int x = lane * 16; x < F::kStageB; x += 512)
+            copy16(ring + st * F::kStageB + x, x < F::kPageB ? k + x : v + (x - F::kPageB));
+        } else if (lane == 0) {
+          set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+        }
+      }
+      copy_commit();
+    };
+    at.start(p, b, h, lane);
+#pragma unroll
+    for (int i = 0; i < F::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < count; ++i) {
+      copy_wait<F::kStages - 2>();
+      __syncwarp();  // every lane's copies are there, and every lane is done with the stage before
+      issue(i + F::kStages - 1);
+      const int st = i % F::kStages;
+      if (valid >> st & 1) {
+        const int tok = (sp.first + pg0 + warp + i * kWarps) * kPage;
+        at.take(ring + st * F::kStageB, sp.lo - tok, sp.len - tok, lane);
+      }
+    }
+    copy_wait<0>();
+    __syncwarp();
+
+    // ---- the piece's end: the warps' states meet
+    {
+      const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) at.l[i] += __shfl_xor_sync(0xffffffffu, at.l[i], o);
+        if (r == 0) {
+          s_m[warp][2 * c + i] = at.m[i];
+          s_l[warp][2 * c + i] = at.l[i];
+        }
+#pragma unroll
+        for (int d = 0; d < F::kTiles; ++d)
+          *reinterpret_cast<float2*>(stage + (2 * c + i) * F::kRow + 16 * d + 2 * r) = make_float2(at.O[d][i], at.O[d][2 + i]);
+      }
+    }
+    __syncthreads();
+    const bool direct = n == sp.n;  // all of the sequence and KV head
+    const int64_t id = blockIdx.x + static_cast<int64_t>(b) * p.Hkv + h;
+    const float vs = p.v_scale[h];
+    for (int x = tid; x < p.g * D; x += kWarps * 32) {
+      const int qh = x / D, d = x % D;
+      float M = NEG_INF;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][qh]);
+      float l = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = s_m[w][qh] == NEG_INF ? 0.f : ex2(s_m[w][qh] - M);
+        l = fmaf(s_l[w][qh], f, l);
+        if (f != 0.f) o = fmaf(reinterpret_cast<const float*>(smem + w * F::kRingB)[qh * F::kRow + d], f, o);
+      }
+      o = l > 0.f || l != l ? o / l * vs : 0.f;
+      if (direct) {
+        p.out[(static_cast<int64_t>(b) * p.Hq + h * p.g + qh) * D + d] = __float2bfloat16(o);
+      } else {
+        p.o_part[(id * p.g + qh) * D + d] = o;
+        if (d == 0) p.lse_part[id * p.g + qh] = l > 0.f || l != l ? M + log2f(l) : NEG_INF;
+      }
+    }
+    __syncthreads();
+    pos += n;
+    if (within + n == sp.n * p.Hkv) {
+      before += sp.n;
+      ++b;
+    }
+  }
+}
+
+// Joins the pieces of a row: a CTA per (sequence, query head).
+template <int D, int NW>
+__global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Params p, int parts) {
+  __shared__ float s_max[NW], s_o[NW][D], s_l[NW];
+  constexpr int V = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq;
+  const int h = hq / p.g, qh = hq % p.g;
+  grid_dependency_wait();
+  const int total = p.prefix[p.B], before = p.prefix[b], n = p.prefix[b + 1] - before;
+  __nv_bfloat16* out = p.out + (static_cast<int64_t>(b) * p.Hq + hq) * D;
+  if (n == 0) {
+    for (int d = threadIdx.x; d < D; d += NW * 32) out[d] = __float2bfloat16(0.f);
+    return;
+  }
+  const int chunk = part_pages(total * p.Hkv, parts);
+  const int x = before * p.Hkv + h * n;
+  const int first = x / chunk, last = (x + n - 1) / chunk;
+  if (first == last) return;  // written where it was computed
+  const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h;
+  const float* lse = p.lse_part + (first + pair) * p.g + qh;
+  const float* o = p.o_part + ((first + pair) * p.g + qh) * D;
+  const int count = last - first + 1;
+  float M = NEG_INF;
+  for (int i = warp; i < count; i += NW) M = fmaxf(M, lse[static_cast<int64_t>(i) * p.g]);
+  const float base = M == NEG_INF ? 0.f : M;
+  float acc[V] = {}, l = 0.f;
+  for (int i = warp; i < count; i += NW) {
+    const float f = ex2(lse[static_cast<int64_t>(i) * p.g] - base);
+    l += f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = fmaf(o[static_cast<int64_t>(i) * p.g * D + lane * V + e], f, acc[e]);
+  }
+  if (lane == 0) {
+    s_max[warp] = M;
+    s_l[warp] = l;
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += NW * 32) {
+    float top = NEG_INF;
+    for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w]);
+    float sum = 0.f, y = 0.f;
+    for (int w = 0; w < NW; ++w) {
+      const float f = s_max[w] == NEG_INF ? 0.f : ex2(s_max[w] - top);
+      sum = fmaf(s_l[w], f, sum);
+      y = fmaf(s_o[w][d], f, y);
+    }
+    out[d] = __float2bfloat16(sum > 0.f || sum != sum ? y / sum : 0.f);
+  }
+}
+
+// CTAs of a call: one wave, and no more than parts of kMinPart pages.
+int fp4_parts(int B, int Hkv, int max_blocks) {
+  const int64_t most = (static_cast<int64_t>(B) * Hkv * max_blocks + kMinPart - 1) / kMinPart;
+  return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(kCtasPerSm) * sm_count(), most));
+}
+// Rows of partials: piece (part, sequence and KV head) is row part + pair.
+int64_t fp4_rows(int B, int Hq, int Hkv, int max_blocks) {
+  return (fp4_parts(B, Hkv, max_blocks) + static_cast<int64_t>(B) * Hkv) * (Hq / Hkv);
+}
+bool fp4_sizes_ok(int B, int Hq, int Hkv, int D, int P, int max_blocks) {
+  return B >= 1 && Hq >= 1 && Hkv >= 1 && max_blocks >= 1 && Hq % Hkv == 0 && (D == 64 || D == 128) && P == kPage;
+}
+
+template <int D>
+kvq_status_t launch_fp4(const Fp4Params& p, cudaStream_t s) {
+  using F = Fp4<D>;
+  auto kern = decode_fp4_kernel<D>;
+  const int parts = fp4_parts(p.B, p.Hkv, p.max_blocks);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(parts);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = F::kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return cuda_status(e, "paged_decode_fp4 launch");
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq);
+  cfg.dynamicSmemBytes = 0;
+  // warps for the pieces of a row
+  if (parts / (static_cast<int64_t>(p.B) * p.Hkv) >= 8) {
+    cfg.blockDim = dim3(16 * 32);
+    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 16>, p, parts);
+  } else {
+    cfg.blockDim = dim3(4 * 32);
+    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 4>, p, parts);
+  }
+  return cuda_status(e, "paged_decode_fp4 combine launch");
+}
+
+}  // namespace
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" size_t kvq_decode_fp4_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks) {
+  if (!fp4_sizes_ok(B, Hq, Hkv, D, P, max_blocks)) return 0;
+  const int64_t rows = fp4_rows(B, Hq, Hkv, max_blocks);
+  return static_cast<size_t>((rows * (D + 1) + B + 1) * 4 + 15) / 16 * 16;
+}
+
+extern "C" kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache,
+                                                       const float* k_scale, const float* v_scale,
+                                                       const int32_t* block_table, const int32_t* seq_lens, void* out,
+                                                       int B, int Hq, int Hkv, int D, int P, int max_blocks,
+                                                       int64_t num_blocks, float sm_scale, int window, void* workspace,
+                                                       size_t workspace_bytes, int* dev_status, kvq_stream_t stream) {
+  clear_error();
+  if (B < 1 || Hq < 1 || Hkv < 1 || max_blocks < 1 || num_blocks < 1 || Hq % Hkv != 0)
+    return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: bad sizes");
+  if (window == 0 || window < -1) return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: window must be -1 or > 0");
+  if (!(sm_scale > 0.f) || !(sm_scale < FLT_MAX)) return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: bad sm_scale");
+  if (P != kPage) return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: page size %d (only 16)", P);
+  if (D != 64 && D != 128) return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: head_dim %d (64 or 128)", D);
+  if (Hq / Hkv > 8) return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: GQA ratio %d > 8", Hq / Hkv);
+  // positions in the stream of pages, and tokens, are 32-bit
+  if (static_cast<int64_t>(max_blocks) * kPage > 0x7FFFFFFF - kPage || static_cast<int64_t>(B) * Hq > 0x7FFFFFFF ||
+      static_cast<double>(B) * Hkv * max_blocks > 0x7FFFFFFF - 65536.0)
+    return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: problem too large");
+  if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
+    return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: null pointer");
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(workspace, 16) || !aligned(out, 4) ||
+      !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4))
+    return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: misaligned pointer");
+  const size_t need = kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, P, max_blocks);
+  if (workspace_bytes < need)
+    return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: workspace %zu bytes < %zu needed", workspace_bytes, need);
+  const int64_t rows = fp4_rows(B, Hq, Hkv, max_blocks);
+  Fp4Params p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  const PageStrides ps = page_strides(k_cache, v_cache, k_page_bytes(kFP4, D), v_page_bytes(kFP4, D));
+  p.k_str = ps.k;
+  p.v_str = ps.v;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.o_part = static_cast<float*>(workspace);
+  p.lse_part = p.o_part + rows * D;
+  p.prefix = reinterpret_cast<int32_t*>(p.lse_part + rows);
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.g = Hq / Hkv;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.sm_scale = sm_scale;
+  p.window = window;
+  p.dev_status = dev_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return D == 128 ? launch_fp4<128>(p, s) : launch_fp4<64>(p, s);
+}

@@ -33,6 +33,14 @@ inline PageStrides page_strides(const void* k_cache, const void* v_cache, int64_
   return paired ? PageStrides{k_page + v_page, k_page + v_page, true} : PageStrides{k_page, v_page, false};
 }
 
+// The kernels' format of a cache (CacheFormat, kvq_rows.cuh); false where there is none.
+bool cache_format(kvq_dtype_t dtype, bool per_token, int* fmt);
+
+// kvq_reshape_and_cache of a KVQ_DTYPE_FP4_E2M1 cache (rope.cu), its sizes checked.
+kvq_status_t write_fp4(const void* k, const void* v, const int64_t* slot_mapping, void* k_cache, void* v_cache,
+                       const float* k_scale, const float* v_scale, int T, int Hkv, int D, int64_t num_blocks,
+                       int* dev_status, cudaStream_t s);
+
 // The split-KV partials of an FP8 decode (per-head scales, no window) without
 // their combine: float32 outputs [rows][D] and base-2 log-sum-exps [rows].
 // slots > 0: the wide balanced plan (kvq_plan.cuh), a segment (slot, sequence)

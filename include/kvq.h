@@ -52,6 +52,15 @@
  *  - FP8 elements are E4M3 ("OCP FN": bias 7, max 448, min subnormal 2^-9,
  *    0x7F/0xFF NaN, no infinity) or E5M2 (KVQ_DTYPE_FP8_E5M2).  Page bytes =
  *    P * D * esize.
+ *  - FP4 (KVQ_DTYPE_FP4_E2M1): E2M1 codes (bias 1, magnitudes 0, 0.5, 1, 1.5,
+ *    2, 3, 4, 6, bit 3 the sign) with an E4M3 scale per token and block of 16
+ *    dims, beside the float32 scale per KV head.  A page is P * D / 2 bytes
+ *    of codes and then P * D / 16 scale bytes.  A byte holds dims 2j (low
+ *    nibble) and 2j + 1 of one token.  K page: byte j of token t at t * D / 2
+ *    + j; the scale of block i at t * D / 16 + i of the scales.  V page, for
+ *    the tensor-core operand order: with t = 8 hi + 2 c + lo and j = 8 (4 h +
+ *    b) + r, the byte is at h * 512 + r * 64 + c * 16 + b * 4 + hi * 2 + lo
+ *    and the scale of block 4 h + b at h * 64 + c * 16 + b * 4 + hi * 2 + lo.
  *  - Separate or paired.  Two separate allocations [num_blocks][Hkv][K page]
  *    and [num_blocks][Hkv][V page], or one paired allocation
  *    [num_blocks][Hkv][K page | V page]: each (block, KV head) pair's K page
@@ -90,13 +99,20 @@ typedef enum kvq_status {
 typedef enum kvq_dtype {
   KVQ_DTYPE_FP8_E4M3 = 0,    /* 1-byte E4M3 codes with per-KV-head scales */
   KVQ_DTYPE_BF16 = 1,        /* unquantized bfloat16 ("skip layers") */
-  KVQ_DTYPE_FP8_E5M2 = 2     /* 1-byte E5M2 codes with per-KV-head scales:
+  KVQ_DTYPE_FP8_E5M2 = 2,    /* 1-byte E5M2 codes with per-KV-head scales:
                                 [FP8KV] "How to enable it in the engine" lists
                                 fp8_e5m2 among the cache dtypes; [GTNT] section
                                 1: 5 exponent bits, 2 mantissa bits, about
                                 +-57344.  Bias 15, RNE, saturating to +-57344.
                                 Prefill reads it through
                                 kvq_prefill_attention_dtype. */
+  KVQ_DTYPE_FP4_E2M1 = 3     /* 4-bit E2M1 codes, an E4M3 scale per token and 16
+                                dims, per-KV-head scales (the format above).
+                                Written by kvq_reshape_and_cache and
+                                kvq_rope_and_cache, read by
+                                kvq_paged_decode_attention_fp4 and
+                                kvq_gather_cache; every other call refuses it.
+                                The pages have no counterpart. */
 } kvq_dtype_t;
 
 /*
@@ -122,6 +138,7 @@ typedef enum kvq_accumulation {
 #define KVQ_DEV_TIMEOUT      0x8  /* a pipeline wait exceeded its bound: work abandoned */
 #define KVQ_DEV_BAD_QROWS    0x10 /* prefill: new tokens exceed seq_len: rows skipped */
 #define KVQ_DEV_BAD_GROUP    0x20 /* shared prefix: group_starts decreasing or outside [0, B]: clamped */
+#define KVQ_DEV_BAD_AXIS     0x40 /* rotation: pair_axis outside [0, num_axes): taken as axis 0 */
 
 typedef void* kvq_stream_t;   /* cudaStream_t */
 
@@ -160,11 +177,14 @@ const char* kvq_last_error_string(void);
  *                the token; a slot >= num_blocks * P sets KVQ_DEV_BAD_SLOT.
  *  k_cache       [num_blocks][Hkv][P][D] in the format above (written).
  *  v_cache       [num_blocks][Hkv][D][P] in the format above (written).
- *  k_scale,      float32 [Hkv] per-KV-head scales (FP8 only; may be NULL for
+ *  k_scale,      float32 [Hkv] per-KV-head scales (FP8 and FP4; may be NULL for
  *  v_scale       BF16).  Must be finite and > 0.
  *  T >= 0 (T == 0 launches nothing), Hkv >= 1, D in {64, 128} (and 256 for
  *  FP8 caches, which only kvq_prefill_attention reads), P == 16,
- *  num_blocks >= 1.  For BF16 the values are copied bit for bit.  FP8:
+ *  num_blocks >= 1.  For BF16 the values are copied bit for bit.  FP4: per
+ *  token and block of 16 dims, b = e4m3(fl32(max |x| / fl32(6 s))), saturating,
+ *  and code = e2m1(fl32(x / fl32(b s))), nearest even, saturating to +-6 (codes
+ *  0 where b rounds to 0); the value held is code * b * s.  FP8:
  *  code = encode(fl32(x / s[h])), one float32 division, then one
  *  round-to-nearest-even conversion saturating at the format's largest
  *  finite value (448 for E4M3, 57344 for E5M2).
@@ -532,6 +552,156 @@ kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_stride, void
                               int32_t* dst_seq_lens, int32_t* kept, int B, int Hkv, int D, int P, int max_blocks,
                               int max_dst_blocks, int64_t num_blocks, int sink, int recent, kvq_dtype_t cache_dtype,
                               int per_token, int* dev_status, kvq_stream_t stream);
+
+/*
+ * Rotary positions, an argument of kvq_qk_norm_rope and kvq_rope_and_cache.
+ * Pair i (0 <= i < rot_dim / 2) of a token t is turned by the angle
+ *   a = positions[pair_axis[i]][t] * inv_freq[i]:
+ *   (x, y) -> scale * (x cos a - y sin a, y cos a + x sin a),
+ * where the pair is dims i and i + rot_dim / 2 or, interleaved, 2 i and 2 i +
+ * 1; dims from rot_dim on pass as they are.  The pages have no counterpart.
+ *
+ *  positions    int64 [num_axes][T], row a at positions + a *
+ *               positions_stride; any value.  One axis: the token's place in
+ *               its text.  Several: time, height and width of an image's or
+ *               video's patch, each pair following one of them.
+ *  inv_freq     float32 [rot_dim / 2], radians per position, finite.  The
+ *               angle is the exact product reduced in 64-bit fixed point: off
+ *               by at most 2^-31 of a turn for |positions| up to 2^31 and
+ *               |inv_freq| up to 1.
+ *  pair_axis    int32 [rot_dim / 2], each in [0, num_axes); NULL: all 0.
+ *  num_axes     1 to 4.
+ *  rot_dim      a multiple of 16, 16 to D.
+ *  interleaved  nonzero: pairs of neighbouring dims.
+ *  scale        multiplies the turned dims (1 for plain rotation), finite.
+ * The struct and the kvq_head_norm below are read on the host during the
+ * call; their pointers are device pointers.
+ */
+typedef struct kvq_rotary {
+  const int64_t* positions;
+  int64_t positions_stride;
+  const float* inv_freq;
+  const int32_t* pair_axis;
+  int num_axes;
+  int rot_dim;
+  int interleaved;
+  float scale;
+} kvq_rotary_t;
+
+/*
+ * Root-mean-square norm of each query and key head, before the rotation:
+ * x_d -> x_d / sqrt(sum x^2 / D + eps) * w_d.  q_weight, k_weight: bf16 [D]
+ * (either may be NULL: those heads are not normed); eps >= 0, finite.
+ */
+typedef struct kvq_head_norm {
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+} kvq_head_norm_t;
+
+/*
+ * kvq_qk_norm_rope -- head norms and rotary positions of queries and keys in
+ * one pass.  The pages have no counterpart (they take rotated keys as input).
+ *
+ *  q, k       bf16 [T][Hq][D] and [T][Hkv][D], the heads of a token
+ *             contiguous, tokens q_stride and k_stride elements apart (a slice
+ *             of a projection's output needs no copy).  Either may be NULL
+ *             with its head count 0.
+ *  q_out,     bf16, laid out alike with strides of their own; may be q and k
+ *  k_out      themselves (same strides), and must not overlap them otherwise.
+ *  norm       NULL: no norms.
+ *  rotary     NULL: no rotation.
+ *  T >= 0, Hq + Hkv >= 1, D in {64, 128, 256}.  Pointers 16-byte aligned,
+ *  strides multiples of 8 elements and at least heads * D.
+ *  Declared rounding: everything in float32 from the bf16 inputs, rounded to
+ *  bf16 once.
+ */
+kvq_status_t kvq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const kvq_head_norm_t* norm, const kvq_rotary_t* rotary, void* q_out,
+                              int64_t q_out_stride, void* k_out, int64_t k_out_stride, int T, int Hq, int Hkv, int D,
+                              int* dev_status, kvq_stream_t stream);
+
+/*
+ * kvq_rope_and_cache -- what a layer does between its projection and its
+ * attention, in one launch: head norms and rotary positions of q and k, then k
+ * and v into the paged cache and q out for attention.
+ *
+ *  q, k, v    bf16 [T][Hq][D], [T][Hkv][D], [T][Hkv][D] with token strides as
+ *             above.  q may be NULL with Hq 0.
+ *  norm, rotary  as for kvq_qk_norm_rope; v is neither normed nor turned.
+ *  slot_mapping, k_cache, v_cache, k_scale, v_scale  as for
+ *             kvq_reshape_and_cache; per_token nonzero: a cache of
+ *             kvq_reshape_and_cache_per_token (E4M3 or E5M2; the scales are
+ *             ignored and may be NULL).
+ *  q_out      bf16 [T][Hq][D], tokens q_out_stride elements apart; may be q
+ *             itself; or NULL.
+ *  q8         uint8 [T][Hq][D] contiguous, 16-byte aligned: E4M3 codes of
+ *             fl32(q / q_scale) as kvq_quantize_query; or NULL.  Both may be
+ *             given; with Hq > 0 one must be.
+ *  q_scale    float32 [1], for q8.
+ *  T >= 0, Hq >= 0, 1 <= Hkv, D in {64, 128} (and 256 for FP8 caches with
+ *  per-head scales), P == 16.  q_out, q8 and the caches must not overlap k or v.
+ *  Declared rounding: norm and rotation in float32; the float32 result is
+ *  quantized (or rounded to bf16) directly, without a rounding to bf16 before.
+ */
+kvq_status_t kvq_rope_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const kvq_head_norm_t* norm, const kvq_rotary_t* rotary,
+                                const int64_t* slot_mapping, void* k_cache, void* v_cache, const float* k_scale,
+                                const float* v_scale, void* q_out, int64_t q_out_stride, uint8_t* q8,
+                                const float* q_scale, int T, int Hq, int Hkv, int D, int P, int64_t num_blocks,
+                                kvq_dtype_t cache_dtype, int per_token, int* dev_status, kvq_stream_t stream);
+
+/*
+ * kvq_gather_cache -- the reverse of the cache writes: the tokens of the given
+ * slots back as bf16 (a cached context for an attention of the caller's own, a
+ * cache moved to another format).  The pages have no counterpart.
+ *
+ *  slot_mapping   int64 [T]: a slot may appear more than once; a negative slot
+ *                 leaves its rows as they were, as does a slot >= num_blocks *
+ *                 P, which sets KVQ_DEV_BAD_SLOT.
+ *  k_cache,       any format of kvq_reshape_and_cache or (per_token nonzero)
+ *  v_cache        kvq_reshape_and_cache_per_token.
+ *  k_scale,       float32 [Hkv] (FP8 and FP4 with per-head scales; else ignored,
+ *  v_scale        may be NULL).
+ *  k_out, v_out   bf16 [T][Hkv][D], contiguous, 16-byte aligned.
+ *  D in {64, 128} (and 256 for FP8 caches with per-head scales), P == 16.
+ *  Declared rounding: bf16(fl32(code * scale)); FP4: code times block scale is
+ *  exact, then as above; BF16: bit copies.
+ */
+kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale, void* k_out, void* v_out, int T, int Hkv,
+                              int D, int P, int64_t num_blocks, kvq_dtype_t cache_dtype, int per_token,
+                              int* dev_status, kvq_stream_t stream);
+
+/*
+ * kvq_paged_decode_attention_fp4 -- kvq_paged_decode_attention over a cache of
+ * KVQ_DTYPE_FP4_E2M1 (9/16 of an FP8 cache's bytes).
+ *
+ *  Arguments as for kvq_paged_decode_attention without the dtype and the split
+ *  count.  D in {64, 128}, P == 16, Hq % Hkv == 0, Hq / Hkv <= 8.
+ *  workspace  kvq_decode_fp4_workspace_size(...) bytes, 16-byte aligned;
+ *             contents on entry are ignored; calls sharing it must not overlap.
+ *  The attended pages of all sequences and KV heads are laid end to end and cut
+ *  into equal parts, one per CTA, so that ragged batches balance; a part's
+ *  share of a (sequence, KV head) is merged by log-sum-exps in FP32.  The plan is a
+ *  function of the lengths alone: results are deterministic.
+ *  Declared rounding: the query enters as f16(fl32(q * sigma)) as for
+ *  kvq_paged_decode_attention; K enters as code * block scale, exact in float16; scores
+ *  are FP32 sums times fl32(fl32(k_scale * sm_scale) * log2(e)) / sigma;
+ *  probabilities 2^(s2 - M + 4), M a running maximum that may lag by up to 3,
+ *  are rounded to float16, multiplied by V's block scale with another
+ *  rounding to float16 (each half a step of 2^-10; below 2^-14 steps of 2^-24),
+ *  and contracted with V's codes, exact in float16, in FP32 per page
+ *  of 16 tokens, then added into a running FP32 sum; the row sum adds them
+ *  unrounded.  The output is rounded to bf16 once, at the end.
+ */
+size_t kvq_decode_fp4_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks);
+kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache,
+                                            const float* k_scale, const float* v_scale, const int32_t* block_table,
+                                            const int32_t* seq_lens, void* out, int B, int Hq, int Hkv, int D, int P,
+                                            int max_blocks, int64_t num_blocks, float sm_scale, int window,
+                                            void* workspace, size_t workspace_bytes, int* dev_status,
+                                            kvq_stream_t stream);
 
 /*
  * kvq_paged_decode_attention_static_scratch -- kvq_paged_decode_attention

@@ -11,6 +11,9 @@ Modules
 e4m3       the E4M3 codec (decode table from the format fields; saturating
            round-to-nearest-even encode; quantize = encode(fl32(x / s))).
 e5m2       the E5M2 codec, written the same way.
+e2m1       E2M1 codes with a block scale: codec, quantization, 4-bit pages,
+           attention over their values.
+rotary     head norms and rotary positions.
 kv_cache   the paged cache write (K pages [P][D], V pages [D][P]) with
            per-head or per-token dynamic scales, query quantization, the KV
            byte formulas.
