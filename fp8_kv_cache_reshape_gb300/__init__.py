@@ -599,62 +599,70 @@ def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens
     return dst_seq_lens
 
 
-def _rows(t, heads, D, name):
-    """Tokens' heads (bf16 [T][heads][D]) with any stride between tokens:
-    that stride in elements."""
-    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} must be bf16 [T][{heads}][{D}], got {t.dtype} {list(t.shape)}")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+def _rows(t, T, D, name):
+    """Heads and token stride (in elements) of tokens' heads, bf16 [T][heads][D]
+    with any stride between tokens."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != D:
+        raise ValueError(f"{name} must be bf16 [T][heads][{D}], got {t.dtype} {list(shape)}")
+    if shape[0] != T:
+        raise ValueError(f"{name} must have {T} tokens like the others, got {shape[0]}")
+    heads = shape[1]
+    if strides[2] != 1 or (heads > 1 and strides[1] != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    return heads, strides[0] if T > 1 else heads * D
 
 
-def _device_ptr(t):
-    """_device_ptrs for a tensor whose strides are checked by its user."""
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError("libkvq takes CUDA tensors only")
-    current = torch.cuda.current_device()
-    if t.get_device() != current:
-        raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one (cuda:{current})")
-    return t.data_ptr()
+def _addresses(*tensors):
+    """Addresses of tensors on the current device, whose strides their user has
+    checked (None for None)."""
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        at = t.get_device()
+        if at != current or at < 0:
+            if at < 0:
+                raise ValueError("libkvq takes CUDA tensors only")
+            raise ValueError(f"the tensors' device (cuda:{at}) must be the current one (cuda:{current})")
+        out.append(t.data_ptr())
+    return out
+
+
+def _check_dense(t, dtype, shape, name):
+    _check_tensor(t, dtype, shape, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libkvq takes contiguous tensors only")
 
 
 def _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D):
-    """The shapes of the rotation's and norms' tensors."""
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _check_tensor(t, torch.bfloat16, (D,), name)
+    """The shapes of the rotation's and norms' tensors; (axes, stride between
+    their positions, pairs)."""
+    if q_weight is not None:
+        _check_dense(q_weight, torch.bfloat16, (D,), "q_weight")
+    if k_weight is not None:
+        _check_dense(k_weight, torch.bfloat16, (D,), "k_weight")
     if positions is None:
         if inv_freq is not None or pair_axis is not None:
             raise ValueError("inv_freq and pair_axis need positions")
-        return
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _check_tensor(positions, torch.int64, (axes, T) if positions.dim() == 2 else (T,), "positions")
-    if positions.stride(-1) != 1 and T > 1:
+        return 0, 0, 0
+    shape, strides = positions.shape, positions.stride()
+    axes = shape[0] if len(shape) == 2 else 1
+    if positions.dtype is not torch.int64 or not 1 <= len(shape) <= 2 or shape[-1] != T:
+        raise ValueError(f"positions must be int64 [{T}] or [axes][{T}], got {positions.dtype} {list(shape)}")
+    if strides[-1] != 1 and T > 1:
         raise ValueError("positions: an axis's tokens must be contiguous")
     if inv_freq is None:
         raise ValueError("positions need inv_freq")
-    _check_tensor(inv_freq, torch.float32, (inv_freq.numel(),), "inv_freq")
+    pairs = inv_freq.numel()
+    _check_dense(inv_freq, torch.float32, (pairs,), "inv_freq")
     if pair_axis is not None:
-        _check_tensor(pair_axis, torch.int32, (inv_freq.numel(),), "pair_axis")
+        _check_dense(pair_axis, torch.int32, (pairs,), "pair_axis")
     elif axes > 1:
         raise ValueError("several position axes need pair_axis")
-
-
-def _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps):
-    """kvq_head_norm and kvq_rotary of checked tensors (None: no norm, no rotation)."""
-    norm = rotary = None
-    if q_weight is not None or k_weight is not None:
-        norm = _HeadNorm(*(None if t is None else _device_ptrs(t)[0] for t in (q_weight, k_weight)), float(eps))
-    if positions is not None:
-        axes, T = positions.shape[0] if positions.dim() == 2 else 1, positions.shape[-1]
-        stride = positions.stride(0) if axes > 1 else T
-        freq, axis = _device_ptrs(inv_freq, pair_axis)
-        rotary = _Rotary(_device_ptr(positions), stride, freq, axis, axes, 2 * inv_freq.numel(), 1 if interleaved else 0,
-                         float(rope_scale))
-    return norm, rotary
+    return axes, strides[0] if axes > 1 else T, pairs
 
 
 def kvq_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_weight=None, eps=1e-6, pair_axis=None,
@@ -672,21 +680,27 @@ def kvq_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_weight=None, k_w
     if x is None:
         raise ValueError("q or k must be given")
     T, _, D = x.shape
-    heads, strides = [], []
-    for t, out, name in ((q, q_out, "q"), (k, k_out, "k")):
-        heads.append(0 if t is None else t.shape[1])
-        if t is None:
-            strides.append((0, 0))
-            continue
-        strides.append((_rows(t, heads[-1], D, name), 0 if out is None else _rows(out, heads[-1], D, name + "_out")))
-        if t.shape[0] != T or out is None or out.shape[0] != T:
-            raise ValueError(f"{name} and {name}_out must have the same tokens, and q's")
-    _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
-    norm, rotary = _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps)
-    (qs, qos), (ks, kos) = strides
-    _check(lib.kvq_qk_norm_rope(_device_ptr(q), qs, _device_ptr(k), ks, norm, rotary, _device_ptr(None if q is None else q_out),
-                                qos, _device_ptr(None if k is None else k_out), kos, T, *heads, D,
-                                None if dev_status is None else _device_ptrs(dev_status)[0], _stream(stream)),
+    Hq = qs = qos = Hkv = ks = kos = 0
+    if q is not None:
+        if q_out is None:
+            raise ValueError("q needs q_out")
+        Hq, qs = _rows(q, T, D, "q")
+        heads, qos = _rows(q_out, T, D, "q_out")
+        if heads != Hq:
+            raise ValueError("q_out must be shaped like q")
+    if k is not None:
+        if k_out is None:
+            raise ValueError("k needs k_out")
+        Hkv, ks = _rows(k, T, D, "k")
+        heads, kos = _rows(k_out, T, D, "k_out")
+        if heads != Hkv:
+            raise ValueError("k_out must be shaped like k")
+    axes, stride, pairs = _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
+    qp, kp, qop, kop, pos, freq, axis, qw, kw, status = _addresses(
+        q, k, q_out if Hq else None, k_out if Hkv else None, positions, inv_freq, pair_axis, q_weight, k_weight, dev_status)
+    norm = _HeadNorm(qw, kw, eps) if qw or kw else None
+    rotary = _Rotary(pos, stride, freq, axis, axes, 2 * pairs, 1 if interleaved else 0, rope_scale) if axes else None
+    _check(lib.kvq_qk_norm_rope(qp, qs, kp, ks, norm, rotary, qop, qos, kop, kos, T, Hq, Hkv, D, status, _stream(stream)),
            "kvq_qk_norm_rope")
     return q_out, k_out
 
@@ -699,41 +713,51 @@ def kvq_rope_and_cache(q, k, v, positions, inv_freq, slot_mapping, k_cache, v_ca
     and v into the cache (any dtype of alloc_kv_cache, per_token: dynamic
     scales) and q out as bf16 (q_out, may be q) or E4M3 codes (q8 with q_scale)
     or both, in one launch.  q may be None."""
-    T, Hkv, D = k.shape
-    ks, vs = _rows(k, Hkv, D, "k"), _rows(v, Hkv, D, "v")
-    if v.shape[0] != T:
-        raise ValueError("v must have k's tokens")
+    T, _, D = k.shape
+    Hkv, ks = _rows(k, T, D, "k")
+    heads, vs = _rows(v, T, D, "v")
+    if heads != Hkv:
+        raise ValueError("v must be shaped like k")
     Hq = qs = qos = 0
     if q is not None:
-        Hq = q.shape[1]
-        qs = _rows(q, Hq, D, "q")
-        if q.shape[0] != T:
-            raise ValueError("q must have k's tokens")
-        if q_out is None and q8 is None:
-            raise ValueError("q needs q_out or q8")
+        Hq, qs = _rows(q, T, D, "q")
         if q_out is not None:
-            qos = _rows(q_out, Hq, D, "q_out")
-            if q_out.shape[0] != T:
-                raise ValueError("q_out must have q's tokens")
+            heads, qos = _rows(q_out, T, D, "q_out")
+            if heads != Hq:
+                raise ValueError("q_out must be shaped like q")
+        elif q8 is None:
+            raise ValueError("q needs q_out or q8")
         if q8 is not None:
-            _check_tensor(q8, torch.uint8, (T, Hq, D), "q8")
+            _check_dense(q8, torch.uint8, (T, Hq, D), "q8")
             if q_scale is None or q_scale.dtype is not torch.float32 or q_scale.numel() != 1:
                 raise ValueError("q8 needs q_scale, float32 [1]")
     elif q_out is not None or q8 is not None:
         raise ValueError("q_out and q8 need q")
-    _check_tensor(slot_mapping, torch.int64, (T,), "slot_mapping")
+    _check_dense(slot_mapping, torch.int64, (T,), "slot_mapping")
     dt = _dtype_code(cache_dtype)
-    _check_scales(k_scale, v_scale, Hkv)
-    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
-    _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
-    slots, kc, vc, ksc, vsc, q8p, qsc, status = _device_ptrs(slot_mapping, k_cache, v_cache, k_scale, v_scale, q8, q_scale,
-                                                             dev_status)
-    norm, rotary = _turn(positions, inv_freq, pair_axis, interleaved, rope_scale, q_weight, k_weight, eps)
-    _check(lib.kvq_rope_and_cache(
-        _device_ptr(q), qs, _device_ptr(k), ks, _device_ptr(v), vs, norm, rotary, slots, kc, vc, ksc, vsc,
-        _device_ptr(q_out), qos, q8p, qsc, T, Hq, Hkv, D, PAGE, num_blocks, dt, 1 if per_token else 0, status,
-        _stream(stream)), "kvq_rope_and_cache")
+    num_blocks = _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, per_token, num_blocks)
+    axes, stride, pairs = _check_turn(positions, inv_freq, pair_axis, q_weight, k_weight, T, D)
+    qp, kp, vp, pos, freq, axis, qw, kw, slots, kc, vc, ksc, vsc, qop, q8p, qsc, status = _addresses(
+        q, k, v, positions, inv_freq, pair_axis, q_weight, k_weight, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out,
+        q8, q_scale, dev_status)
+    norm = _HeadNorm(qw, kw, eps) if qw or kw else None
+    rotary = _Rotary(pos, stride, freq, axis, axes, 2 * pairs, 1 if interleaved else 0, rope_scale) if axes else None
+    _check(lib.kvq_rope_and_cache(qp, qs, kp, ks, vp, vs, norm, rotary, slots, kc, vc, ksc, vsc, qop, qos, q8p, qsc, T, Hq, Hkv,
+                                  D, PAGE, num_blocks, dt, 1 if per_token else 0, status, _stream(stream)),
+           "kvq_rope_and_cache")
     return q_out if q_out is not None else q8
+
+
+def _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, per_token, num_blocks):
+    """_check_scales and _check_cache for callers that take addresses as they
+    are; returns the block count."""
+    if k_scale is not None:
+        _check_dense(k_scale, torch.float32, (Hkv,), "k_scale")
+    if v_scale is not None:
+        _check_dense(v_scale, torch.float32, (Hkv,), "v_scale")
+    if not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        raise ValueError("libkvq takes contiguous tensors only")
+    return _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
 
 
 def kvq_gather_cache(slot_mapping, k_cache, v_cache, k_out, v_out, k_scale=None, v_scale=None, num_blocks=None,
@@ -742,13 +766,12 @@ def kvq_gather_cache(slot_mapping, k_cache, v_cache, k_out, v_out, k_scale=None,
     (int64 [T]) as bf16 k_out, v_out [T][Hkv][D]; rows of negative slots stay
     as they were."""
     T, Hkv, D = k_out.shape
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        _check_tensor(t, torch.bfloat16, (T, Hkv, D), name)
-    _check_tensor(slot_mapping, torch.int64, (T,), "slot_mapping")
+    _check_dense(k_out, torch.bfloat16, (T, Hkv, D), "k_out")
+    _check_dense(v_out, torch.bfloat16, (T, Hkv, D), "v_out")
+    _check_dense(slot_mapping, torch.int64, (T,), "slot_mapping")
     dt = _dtype_code(cache_dtype)
-    _check_scales(k_scale, v_scale, Hkv)
-    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks)
-    *ptrs, status = _device_ptrs(slot_mapping, k_cache, v_cache, k_scale, v_scale, k_out, v_out, dev_status)
+    num_blocks = _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, per_token, num_blocks)
+    *ptrs, status = _addresses(slot_mapping, k_cache, v_cache, k_scale, v_scale, k_out, v_out, dev_status)
     _check(lib.kvq_gather_cache(*ptrs, T, Hkv, D, PAGE, num_blocks, dt, 1 if per_token else 0, status, _stream(stream)),
            "kvq_gather_cache")
     return k_out, v_out
@@ -766,15 +789,16 @@ def kvq_paged_decode_attention_fp4(q, k_cache, v_cache, k_scale, v_scale, block_
     B, Hq, D = q.shape
     Hkv = k_cache.shape[1]
     max_blocks = block_table.shape[1]
-    _check_tensor(q, torch.bfloat16, (B, Hq, D), "q")
-    _check_tensor(out, torch.bfloat16, (B, Hq, D), "out")
-    _check_tensor(block_table, torch.int32, (B, max_blocks), "block_table")
-    _check_tensor(seq_lens, torch.int32, (B,), "seq_lens")
-    _check_scales(k_scale, v_scale, Hkv)
-    num_blocks = _check_cache(k_cache, v_cache, Hkv, D, KVQ_DTYPE_FP4_E2M1, False, num_blocks)
+    _check_dense(q, torch.bfloat16, (B, Hq, D), "q")
+    _check_dense(out, torch.bfloat16, (B, Hq, D), "out")
+    _check_dense(block_table, torch.int32, (B, max_blocks), "block_table")
+    _check_dense(seq_lens, torch.int32, (B,), "seq_lens")
+    num_blocks = _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, KVQ_DTYPE_FP4_E2M1, False, num_blocks)
     if workspace is None:
         workspace = _workspace(kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, max_blocks), q, stream)
-    *ptrs, ws, status = _device_ptrs(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, dev_status)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace: libkvq takes contiguous tensors only")
+    *ptrs, ws, status = _addresses(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, dev_status)
     _check(lib.kvq_paged_decode_attention_fp4(
         *ptrs, B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale),
         window, ws, workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_fp4")

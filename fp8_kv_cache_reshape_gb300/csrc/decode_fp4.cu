@@ -86,19 +86,6 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report) {
 // Pages of a part: the stream in `parts` equal ones, but at least a page per warp.
 KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, (total + parts - 1) / parts); }
 
-KVQ_DEVINL void copy16(uint32_t dst, const uint8_t* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-KVQ_DEVINL void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-KVQ_DEVINL void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-KVQ_DEVINL uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
 KVQ_DEVINL uint2 lds64(uint32_t a) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
@@ -153,7 +140,7 @@ struct Attend {
     const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.Hq + h * p.g + (live ? r : 0)) * D +
                                                       c * (D / 4));
     float mx = 0.f;
-    float x[D / 32][8];
+    float2 x[D / 32][4];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       unpack8_bf16(live ? src[i] : make_uint4(0, 0, 0, 0), x[i]);
@@ -168,7 +155,7 @@ struct Attend {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16x2(x[i][2 * e] * sigma, x[i][2 * e + 1] * sigma);
+      for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16x2(x[i][e].x * sigma, x[i][e].y * sigma);
     const float cf = __fmul_rn(__fmul_rn(p.k_scale[h], p.sm_scale), kLog2e);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -139,6 +139,22 @@ KVQ_DEVINL uint64_t policy_evict_last() {
   return p;
 }
 
+// A 16-byte asynchronous copy of the executing thread, global -> shared; a thread
+// waits for its own copies, up to its last N groups of them.
+KVQ_DEVINL void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+KVQ_DEVINL void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+KVQ_DEVINL void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+KVQ_DEVINL uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+
 // A 32-bit load cached in L2 only (no L1 line is left behind).
 KVQ_DEVINL int ld_l2only_s32(const int32_t* src) {
   int v;
@@ -252,6 +268,16 @@ KVQ_DEVINL float2 ffma2(float2 a, float2 b, float2 c) {
   memcpy(&rb, &b, 8);
   memcpy(&rc, &c, 8);
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(rd) : "l"(ra), "l"(rb), "l"(rc));
+  float2 d;
+  memcpy(&d, &rd, 8);
+  return d;
+}
+// Two float32 products in one instruction.
+KVQ_DEVINL float2 fmul2(float2 a, float2 b) {
+  unsigned long long ra, rb, rd;
+  memcpy(&ra, &a, 8);
+  memcpy(&rb, &b, 8);
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
   float2 d;
   memcpy(&d, &rd, 8);
   return d;

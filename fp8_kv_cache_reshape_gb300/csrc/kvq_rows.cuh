@@ -5,9 +5,20 @@
 
 #include <cuda_fp4.h>
 
+#ifndef KVQ_TUNE
+#define KVQ_TUNE(name, value) value
+#endif
+
 #include "kvq_device.cuh"
 
 namespace kvq {
+
+// Heads a CTA walks: as many, in halves from `most`, as leave `ctas` CTAs.
+inline int heads_per_cta(int heads, int tiles, int most, int ctas) {
+  int n = most;
+  while (n > 1 && static_cast<int64_t>(tiles) * ((heads + n - 1) / n) < ctas) n /= 2;
+  return n;
+}
 
 // The formats of a cache, one kernel instantiation each.
 enum CacheFormat { kRowsOnly, kE4M3, kE5M2, kBF16, kFP4, kE4M3Token, kE5M2Token };
@@ -38,31 +49,71 @@ KVQ_DEVINL int fp4_v_scale_offset(int t, int i) {
   return (i >> 2) * 64 + ((t & 7) >> 1) * 16 + (i & 3) * 4 + (t >> 3) * 2 + (t & 1);
 }
 
-KVQ_DEVINL void unpack8_bf16(const uint4& a, float (&x)[8]) {
+// Eight dims as four pairs of neighbours, for the two-wide float32 instructions.
+KVQ_DEVINL void unpack8_bf16(const uint4& a, float2 (&x)[4]) {
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
 }
-KVQ_DEVINL uint4 pack8_bf16(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+KVQ_DEVINL uint4 pack8_bf16(const float2 (&x)[4]) {
+  return make_uint4(pack_bf16x2(x[0].x, x[0].y), pack_bf16x2(x[1].x, x[1].y), pack_bf16x2(x[2].x, x[2].y),
+                    pack_bf16x2(x[3].x, x[3].y));
+}
+// A divisor of quotients that are about to be rounded to few bits.  The code of
+// fl32(x / s) is that of x * lo and of x * hi where those two agree, for lo and hi
+// that enclose 1 / s: rounding is monotone.  Two products per value instead of a
+// division; where they disagree (x / s within 2^-20 of a midpoint between codes, one
+// value in 10^5 unless the scale is a ratio of small numbers) the eight values
+// are divided.  A power of two needs no enclosure: x * (1 / s) is x / s.  A chunk
+// of 4,096 tokens with 32 query heads quantized and 8 KV heads of 128 into an
+// E4M3 cache: 39.6 us with divisions.
+struct Divisor {
+  float s, lo, hi;
+  bool ok;  // 1 / s is a normal number
+  // rcp.approx is off by at most 2^-23, lo and hi by 2^-24 more each and each
+  // product by 2^-24: within 2^-22, so 2^-21 to either side encloses
+  KVQ_DEVINL explicit Divisor(float divisor) : s(divisor) {
+    const uint32_t u = __float_as_uint(s);
+    ok = u - 0x04000000u < 0x7A000000u - 0x04000000u;  // 2^-119 <= s < 2^117
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    const bool exact = (u & 0x7FFFFFu) == 0;
+    if (exact) r = __uint_as_float(0x7F000000u - u);  // 2^-e of 2^e
+    lo = exact ? r : r * (1.f - 0x1p-21f);
+    hi = exact ? r : r * (1.f + 0x1p-21f);
+  }
+};
+// code(fl32(x / s)) of eight values, code2 taking two at a time to the bits of `W`.
+template <int W, typename Code2>
+KVQ_DEVINL void code8(const float2 (&x)[4], const Divisor& d, Code2 code2, uint32_t (&w)[2]) {
+  constexpr int kPer = 32 / W;  // pairs per word
+  const float2 lo = make_float2(d.lo, d.lo), hi = make_float2(d.hi, d.hi);
+  uint32_t other[2] = {0, 0};
+  w[0] = w[1] = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i / kPer] |= code2(fmul2(x[i], lo)) << (W * (i % kPer));
+    other[i / kPer] |= code2(fmul2(x[i], hi)) << (W * (i % kPer));
+  }
+  if (w[0] != other[0] || w[1] != other[1] || !d.ok) {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i / kPer] |= code2(make_float2(__fdiv_rn(x[i].x, d.s), __fdiv_rn(x[i].y, d.s))) << (W * (i % kPer));
+  }
 }
 // fp8(fl32(x / s)) of eight values.
 template <bool E5>
-KVQ_DEVINL uint2 quant8_fp8(const float (&x)[8], float s) {
+KVQ_DEVINL uint2 quant8_fp8(const float2 (&x)[4], const Divisor& d) {
   constexpr auto kind = E5 ? __NV_E5M2 : __NV_E4M3;
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)), __NV_SATFINITE, kind);
-  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+  uint32_t w[2];
+  code8<16>(x, d, [](float2 v) -> uint32_t { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, kind); }, w);
+  return make_uint2(w[0], w[1]);
 }
-KVQ_DEVINL float amax8(const float (&x)[8]) {
+KVQ_DEVINL float amax8(const float2 (&x)[4]) {
   float a = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(x[i]));
+  for (int i = 0; i < 4; ++i) a = fmax3(a, fabsf(x[i].x), fabsf(x[i].y));
   return a;
 }
 KVQ_DEVINL float e4m3_value(uint8_t code) {
@@ -70,19 +121,67 @@ KVQ_DEVINL float e4m3_value(uint8_t code) {
 }
 // The E4M3 scale of a block of 16 dims, of which two neighbouring lanes hold
 // eight each, and their E2M1 codes.  s: the head's scale.
-KVQ_DEVINL uint32_t quant8_fp4(const float (&x)[8], float s, uint8_t& block_scale) {
+KVQ_DEVINL uint32_t quant8_fp4(const float2 (&x)[4], float s, uint8_t& block_scale) {
   float a = amax8(x);
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
   block_scale = f32_to_e4m3(__fdiv_rn(a, __fmul_rn(6.f, s)));
   const float step = __fmul_rn(e4m3_value(block_scale), s);
-  uint32_t w = 0;
-  if (step > 0.f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(x[2 * i], step), __fdiv_rn(x[2 * i + 1], step)),
-                                                          __NV_E2M1, cudaRoundNearest)) << (8 * i);
+  if (!(step > 0.f)) return 0;
+  uint32_t w[2];
+  code8<8>(x, Divisor(step), [](float2 v) -> uint32_t { return __nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest); }, w);
+  return w[0];
+}
+
+// 4 x 4 bytes transposed: byte j of word i to byte i of word j.
+KVQ_DEVINL void transpose4(const uint32_t (&w)[4], uint32_t (&o)[4]) {
+  const uint32_t a = __byte_perm(w[0], w[1], 0x5140), b = __byte_perm(w[2], w[3], 0x5140);
+  const uint32_t c = __byte_perm(w[0], w[1], 0x7362), d = __byte_perm(w[2], w[3], 0x7362);
+  o[0] = __byte_perm(a, b, 0x5410);
+  o[1] = __byte_perm(a, b, 0x7632);
+  o[2] = __byte_perm(c, d, 0x5410);
+  o[3] = __byte_perm(c, d, 0x7632);
+}
+
+// The tokens of a tile.  Plain tiles are 16 tokens in order.  Aligned ones
+// follow the pages: the tokens whose page, if its tokens lie in order, began with
+// one of the 16 tokens from 16 (tile - 1) on.  A run of tokens in order through
+// whole pages then has each page in one tile, wherever in a page it starts; any
+// other tokens fall to some tile too, each to one, at most 31 to a tile.
+struct TileTokens {
+  int token[32];
+  int64_t slot[32];
+  int n;
+  bool page[2];  // tokens 0 .. 15 (16 .. 31) fill one page in order
+};
+// By warp 0, before a barrier of the CTA.
+KVQ_DEVINL void find_tokens(TileTokens& s, const int64_t* slots, int T, int64_t num_slots, int tile, bool aligned, int* dev_status) {
+  const int lane = threadIdx.x & 31;
+  const int64_t token = static_cast<int64_t>(tile - (aligned ? 1 : 0)) * kPage + lane;
+  int64_t slot = -1;
+  if (token >= 0 && token < T && (aligned || lane < kPage)) slot = slots[token];
+  if (slot >= num_slots) {
+    set_status(dev_status, KVQ_DEV_BAD_SLOT);
+    slot = -1;
   }
-  return w;
+  bool mine = slot >= 0;
+  // its page's first token is token - slot % kPage, in [16 (tile - 1), 16 tile)
+  if (aligned && mine) mine = static_cast<unsigned>(lane - static_cast<int>(slot % kPage)) < kPage;
+  const unsigned have = __ballot_sync(0xffffffffu, mine);
+  if (mine) {
+    const int at = __popc(have & ((1u << lane) - 1));
+    s.token[at] = static_cast<int>(token);
+    s.slot[at] = slot;
+  }
+  __syncwarp();
+  const int n = __popc(have);
+  const int64_t first = lane < n ? s.slot[lane & kPage] : 0;
+  const bool run = lane < n && first % kPage == 0 && s.slot[lane] == first + (lane & (kPage - 1));
+  const unsigned runs = __ballot_sync(0xffffffffu, run);
+  if (lane == 0) {
+    s.n = n;
+    s.page[0] = (runs & 0xFFFFu) == 0xFFFFu;
+    s.page[1] = (runs >> 16) == 0xFFFFu;
+  }
 }
 
 }  // namespace kvq

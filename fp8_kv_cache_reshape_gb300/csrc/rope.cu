@@ -41,13 +41,22 @@ KVQ_DEVINL uint64_t turns_per_position(float inv_freq) {
   return u >> 31 ? 0 - x : x;
 }
 
-// Sine and cosine of a fraction of a turn: to the nearest quarter, then the rest.
+// Sine and cosine of a fraction of a turn: to the nearest quarter, then the
+// Taylor series of the rest, y up to pi / 4 either way.  The first terms left
+// out are y^11 / 11! < 2^-29 and y^12 / 12! < 2^-32; y is rounded twice, 2^-23.
 KVQ_DEVINL void sincos_turns(uint64_t turns, float& s, float& c) {
   const uint32_t t = static_cast<uint32_t>(turns >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const int rest = static_cast<int>(t - (quarter << 30));  // within an eighth of a turn
-  float s0, c0;
-  sincospif(static_cast<float>(rest) * 0x1p-31f, &s0, &c0);
+  const float y = static_cast<float>(rest) * (6.283185307f * 0x1p-32f), z = y * y;
+  float s0 = fmaf(z, 1.f / 362880, -1.f / 5040), c0 = fmaf(z, -1.f / 3628800, 1.f / 40320);
+  s0 = fmaf(z, s0, 1.f / 120);
+  s0 = fmaf(z, s0, -1.f / 6);
+  s0 = fmaf(y * z, s0, y);
+  c0 = fmaf(z, c0, -1.f / 720);
+  c0 = fmaf(z, c0, 1.f / 24);
+  c0 = fmaf(z, c0, -0.5f);
+  c0 = fmaf(z, c0, 1.f);
   s = quarter & 1 ? c0 : s0;
   c = quarter & 1 ? s0 : c0;
   if (quarter & 2) s = -s;
@@ -70,16 +79,18 @@ struct TokenParams {
   uint8_t* q8;
   const float* q_scale;
   int T, Hq, Hkv;
-  int tiles, q_chunk, kv_chunk, kv_chunks;  // CTAs: tiles x (kv_chunks, then chunks of q heads)
+  // CTAs: kv_tiles x kv_chunks of k's (and v's) heads, then tiles x chunks of q's
+  int kv_tiles, tiles, kv_chunk, q_chunk;
+  unsigned kv_ctas;
+  bool aligned;
   int* dev_status;
 };
 
 // The factors of a lane's eight dims (see the top of the file).
 struct Turn {
-  float a[8], b[8];
-  int from;     // lane that holds the pairs' other dims
-  bool swap;    // they are the neighbours instead
-  bool turned;  // false: b is zero, and so is what it multiplies
+  float2 a[4], b[4];
+  int from;         // lane that holds the pairs' other dims (this one, interleaved)
+  uint32_t px, py;  // which bytes of its words they are, as float32 (0x4444: none, zero)
 };
 
 template <int D>
@@ -87,29 +98,25 @@ KVQ_DEVINL Turn make_turn(const TokenParams& p, const __nv_bfloat16* weight, int
   constexpr int LPT = D / 8;
   const int j = lane % LPT;
   Turn t;
-  t.from = lane;
-  t.swap = false;
   const int rot = p.rotary.rot_dim, half = rot / 2;
-  const bool turned = t.turned = 8 * j < rot;
+  const bool turned = 8 * j < rot;
   int partner = j;
-  if (p.rotary.interleaved)
-    t.swap = true;
-  else if (turned)
-    partner = 8 * j < half ? j + half / 8 : j - half / 8;
+  if (turned && !p.rotary.interleaved) partner = 8 * j < half ? j + half / 8 : j - half / 8;
   t.from = lane - j + partner;
-  float w[8], wp[8];
+  t.px = !turned ? 0x4444 : p.rotary.interleaved ? 0x3244 : 0x1044;
+  t.py = !turned ? 0x4444 : p.rotary.interleaved ? 0x1044 : 0x3244;
+  float2 w[4], wp[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = wp[i] = 1.f;
+  for (int i = 0; i < 4; ++i) w[i] = wp[i] = make_float2(1.f, 1.f);
   if (weight) {
     unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(weight) + j), w);
     unpack8_bf16(__ldg(reinterpret_cast<const uint4*>(weight) + partner), wp);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     t.a[i] = w[i];
-    t.b[i] = 0.f;
+    t.b[i] = make_float2(0.f, 0.f);
   }
-  if (!turned) return t;
   auto angle = [&](int pair, float& s, float& c) {
     int axis = p.rotary.pair_axis ? __ldg(p.rotary.pair_axis + pair) : 0;
     if (static_cast<unsigned>(axis) >= static_cast<unsigned>(p.rotary.num_axes)) {
@@ -122,107 +129,211 @@ KVQ_DEVINL Turn make_turn(const TokenParams& p, const __nv_bfloat16* weight, int
     c *= p.rotary.scale;
   };
   if (p.rotary.interleaved) {
+    if (!turned) return t;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float s, c;
       angle(4 * j + i, s, c);
-      t.a[2 * i] = c * w[2 * i];
-      t.b[2 * i] = -s * w[2 * i + 1];
-      t.a[2 * i + 1] = c * w[2 * i + 1];
-      t.b[2 * i + 1] = s * w[2 * i];
+      t.a[i] = make_float2(c * w[i].x, c * w[i].y);
+      t.b[i] = make_float2(-s * w[i].y, s * w[i].x);
     }
   } else {
+    // this lane and its partner turn the same eight pairs: four angles each
     const bool low = 8 * j < half;
+    float2 sc[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float s, c;
-      angle((low ? 8 * j : 8 * j - half) + i, s, c);
-      t.a[i] = c * w[i];
-      t.b[i] = (low ? -s : s) * wp[i];
+    for (int i = 0; i < 4; ++i) {
+      sc[i] = make_float2(0.f, 1.f);
+      if (turned) angle(low ? 8 * j + i : 8 * j - half + 4 + i, sc[i].x, sc[i].y);
+    }
+    const float sign = low ? -1.f : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // dims 2i, 2i + 1: the lower lane has the angles of the first four
+      float2 u[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float2 mine = sc[(2 * i + e) & 3];
+        const float so = __shfl_sync(0xffffffffu, mine.x, t.from), co = __shfl_sync(0xffffffffu, mine.y, t.from);
+        u[e] = low == (i < 2) ? mine : make_float2(so, co);
+      }
+      if (!turned) continue;
+      t.a[i] = make_float2(w[i].x * u[0].y, w[i].y * u[1].y);
+      t.b[i] = make_float2(wp[i].x * u[0].x * sign, wp[i].y * u[1].x * sign);
     }
   }
   return t;
 }
 
-// Norm and rotation of a lane's eight dims; every lane of the warp takes part.
+// Norm and rotation of a lane's eight dims, `other` those of lane t.from; every
+// lane of the warp takes part.
 template <int D>
-KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, float (&o)[8]) {
+KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, const uint4& other, float2 (&o)[4]) {
   constexpr int LPT = D / 8;
-  float x[8], y[8];
+  const uint32_t w[4] = {other.x, other.y, other.z, other.w};
+  float2 x[4], y[4];
   unpack8_bf16(raw, x);
-  uint4 other;
-  other.x = __shfl_sync(0xffffffffu, raw.x, t.from);
-  other.y = __shfl_sync(0xffffffffu, raw.y, t.from);
-  other.z = __shfl_sync(0xffffffffu, raw.z, t.from);
-  other.w = __shfl_sync(0xffffffffu, raw.w, t.from);
-  unpack8_bf16(other, y);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (t.swap) y[i] = x[i ^ 1];
-    if (!t.turned) y[i] = 0.f;
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t u = w[i];
+    y[i] = make_float2(__uint_as_float(__byte_perm(u, 0, t.px)), __uint_as_float(__byte_perm(u, 0, t.py)));
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = fmaf(x[i], t.a[i], y[i] * t.b[i]);
+  for (int i = 0; i < 4; ++i) o[i] = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
   if (norm) {
-    float sum = 0.f;
+    float2 sum = fmul2(x[0], x[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
+    for (int i = 1; i < 4; ++i) sum = ffma2(x[i], x[i], sum);
+    float all = sum.x + sum.y;
 #pragma unroll
-    for (int off = 1; off < LPT; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float r = rsqrtf(fmaf(sum, 1.f / D, eps));
+    for (int off = 1; off < LPT; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+    const float r = rsqrtf(fmaf(all, 1.f / D, eps));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= r;
+    for (int i = 0; i < 4; ++i) o[i] = fmul2(o[i], make_float2(r, r));
   }
 }
 
-// One tile of 16 tokens: a thread holds dims 8 j .. 8 j + 7 of token tid / LPT.
+// Rows of a warp's tokens on their way through shared memory: a stage is the 16
+// bytes of each lane, of one row (or of a k and a v row).  The copies of all stages but one
+// are in flight, which costs no registers, and a pair's other dims are a second read.
+template <int D>
+struct Ring {
+  static constexpr int kBytes = D == 256 ? 2048 : 4096;  // of a warp (of 16 at D = 256)
+  static constexpr int kRow = 512;
+  static constexpr int kRows = kBytes / kRow, kPairs = kRows / 2;  // stages
+};
+
+// Rows in, rows (or E4M3 codes) out: 16 tokens, heads h0 .. h1 - 1.
+template <int D>
+KVQ_DEVINL void turn_rows(const TokenParams& p, uint32_t ring, bool is_q, int tile, int h0, int h1) {
+  constexpr int LPT = D / 8;
+  constexpr int kStages = Ring<D>::kRows, kStageB = Ring<D>::kRow;
+  const int lane = threadIdx.x & 31, j = threadIdx.x % LPT;
+  const int token = tile * kPage + threadIdx.x / LPT;
+  const bool live = token < p.T;
+  const int row = live ? token : p.T - 1;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>((is_q ? p.q : p.k) + row * (is_q ? p.q_stride : p.k_stride) + h0 * D + 8 * j);
+  const int n = h1 - h0;
+  auto issue = [&](int i) {
+    if (i < n) copy16(ring + i % kStages * kStageB + lane * 16, src + i * (D * 2));
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
+  const Turn turn = make_turn<D>(p, weight, row, lane);
+  __nv_bfloat16* dst = is_q ? p.q_out : p.k_out;
+  if (dst) dst += row * (is_q ? p.q_out_stride : p.k_out_stride) + h0 * D + 8 * j;
+  uint8_t* codes = is_q && p.q8 ? p.q8 + (static_cast<int64_t>(row) * p.Hq + h0) * D + 8 * j : nullptr;
+  const Divisor s(codes ? __ldg(p.q_scale) : 1.f);
+  for (int i = 0; i < n; ++i) {
+    copy_wait<kStages - 2>();
+    __syncwarp();  // the other lanes' copies too, and they are done with the stage before
+    issue(i + kStages - 1);
+    const uint32_t at = ring + i % kStages * kStageB;
+    float2 o[4];
+    turn_row<D>(turn, weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), o);
+    if (!live) continue;
+    if (dst) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(o);
+    if (codes) *reinterpret_cast<uint2*>(codes + i * D) = quant8_fp8<false>(o, s);
+  }
+}
+
+// Bytes between tokens of a V page in shared memory, before its transposition:
+// the four token rows that a page's word takes from fall into different banks.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kPage * D / 8) token_kernel(const TokenParams p) {
+constexpr int kVStride = (FMT == kFP4 ? D / 2 : FMT == kBF16 ? 2 * D : D) + 16;
+
+// A V page from its 16 token rows in shared memory.
+template <int D, int FMT>
+KVQ_DEVINL void write_v_page(const uint8_t* rows, uint8_t* vp) {
+  constexpr int S = kVStride<D, FMT>;
+  const int x = threadIdx.x;
+  if constexpr (FMT == kBF16) {
+    if (x >= D) return;
+    const int half = x & 1, d = x & ~1;  // dims d, d + 1 of eight tokens
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(rows + (8 * half + i) * S + 2 * d);
+    uint4 lo, hi;
+    lo.x = __byte_perm(w[0], w[1], 0x5410);
+    lo.y = __byte_perm(w[2], w[3], 0x5410);
+    lo.z = __byte_perm(w[4], w[5], 0x5410);
+    lo.w = __byte_perm(w[6], w[7], 0x5410);
+    hi.x = __byte_perm(w[0], w[1], 0x7632);
+    hi.y = __byte_perm(w[2], w[3], 0x7632);
+    hi.z = __byte_perm(w[4], w[5], 0x7632);
+    hi.w = __byte_perm(w[6], w[7], 0x7632);
+    *reinterpret_cast<uint4*>(vp + bf16_v_offset(d, 8 * half)) = lo;
+    *reinterpret_cast<uint4*>(vp + bf16_v_offset(d + 1, 8 * half)) = hi;
+  } else {
+    // a word is one byte of tokens 2c, 2c + 1, 2c + 8, 2c + 9, in the FP8 and the FP4 page
+    int c, col, at, step;  // four columns from `col` on, whose words lie `step` apart from `at` on
+    if constexpr (FMT == kFP4) {
+      if (x >= D / 2) return;
+      const int b = x & 3, half = (x >> 4) & 1, h = x >> 5;
+      c = (x >> 2) & 3;
+      col = 32 * h + 8 * b + 4 * half;
+      at = h * 512 + half * 256 + c * 16 + b * 4;
+      step = 64;
+    } else {
+      if (x >= D) return;
+      c = x & 3;
+      col = x & ~3;
+      at = col * kPage + c * 4;
+      step = kPage;
+    }
+    uint32_t w[4], o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(rows + (2 * c + (i & 1) + 8 * (i >> 1)) * S + col);
+    transpose4(w, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(vp + at + i * step) = o[i];
+  }
+}
+
+// k and v into the cache: a tile's tokens, heads h0 .. h1 - 1.
+template <int D, int FMT>
+KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0, int h1) {
   using F = Format<FMT>;
   constexpr int LPT = D / 8;
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int t = tid / LPT, j = tid % LPT;
-  const int tile = blockIdx.x % p.tiles, chunk = blockIdx.x / p.tiles;
-  const int token = tile * kPage + t;
-  const bool live = token < p.T;
-  const int row = live ? token : p.T - 1;  // a token to take angles of
-
-  if (chunk >= p.kv_chunks || FMT == kRowsOnly) {
-    // rows in, rows out
-    const bool is_q = chunk >= p.kv_chunks;
-    const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
-    const Turn turn = make_turn<D>(p, weight, row, lane);
-    const int per = is_q ? p.q_chunk : p.kv_chunk, heads = is_q ? p.Hq : p.Hkv;
-    const int h0 = (is_q ? chunk - p.kv_chunks : chunk) * per, h1 = min(heads, h0 + per);
-    const __nv_bfloat16* src = (is_q ? p.q : p.k) + row * (is_q ? p.q_stride : p.k_stride) + 8 * j;
-    __nv_bfloat16* dst = is_q ? p.q_out : p.k_out;
-    if (dst) dst += row * (is_q ? p.q_out_stride : p.k_out_stride) + 8 * j;
-    uint8_t* codes = is_q && p.q8 ? p.q8 + static_cast<int64_t>(row) * p.Hq * D + 8 * j : nullptr;
-    const float s = codes ? __ldg(p.q_scale) : 1.f;
-    for (int h = h0; h < h1; ++h) {
-      float o[8];
-      turn_row<D>(turn, weight != nullptr, p.eps, *reinterpret_cast<const uint4*>(src + h * D), o);
-      if (!live) continue;
-      if (dst) *reinterpret_cast<uint4*>(dst + h * D) = pack8_bf16(o);
-      if (codes) *reinterpret_cast<uint2*>(codes + h * D) = quant8_fp8<false>(o, s);
-    }
-    return;
-  }
-
-  if constexpr (FMT != kRowsOnly) {
-    const Turn turn = make_turn<D>(p, p.k_weight, row, lane);
-    const int64_t slot = live ? p.slots[token] : -1;
-    if (slot >= p.num_slots && j == 0) set_status(p.dev_status, KVQ_DEV_BAD_SLOT);
-    const bool valid = slot >= 0 && slot < p.num_slots;
+  constexpr int kStages = Ring<D>::kPairs, kStageB = Ring<D>::kRow;
+  __shared__ TileTokens tt;
+  __shared__ __align__(16) uint8_t rows[2][kPage * kVStride<D, FMT>];
+  const int lane = threadIdx.x & 31, t = threadIdx.x / LPT, j = threadIdx.x % LPT;
+  if (threadIdx.x < 32) find_tokens(tt, p.slots, p.T, p.num_slots, tile, p.aligned, p.dev_status);
+  __syncthreads();
+  const int n = tt.n;
+  for (int r = 0; r < n; r += kPage) {
+    const bool valid = r + t < n, page_run = tt.page[r / kPage];
+    const int row = tt.token[valid ? r + t : r];
+    const int64_t slot = tt.slot[valid ? r + t : r];
     const int off = static_cast<int>(slot % kPage);
-    const int h0 = chunk * p.kv_chunk, h1 = min(p.Hkv, h0 + p.kv_chunk);
+    const uint8_t* ksrc = reinterpret_cast<const uint8_t*>(p.k + row * p.k_stride + h0 * D + 8 * j);
+    const uint8_t* vsrc = reinterpret_cast<const uint8_t*>(p.v + row * p.v_stride + h0 * D + 8 * j);
+    auto issue = [&](int i) {
+      if (i < h1 - h0) {
+        const uint32_t at = ring + i % kStages * (2 * kStageB) + lane * 16;
+        copy16(at, ksrc + i * (D * 2));
+        copy16(at + kStageB, vsrc + i * (D * 2));
+      }
+      copy_commit();
+    };
+    __syncwarp();  // done with the stages of the 16 tokens before
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    const Turn turn = make_turn<D>(p, p.k_weight, row, lane);
     for (int h = h0; h < h1; ++h) {
-      const uint4 kr = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + h * D + 8 * j);
-      const uint4 vr = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + h * D + 8 * j);
-      float ko[8], vo[8];
-      turn_row<D>(turn, p.k_weight != nullptr, p.eps, kr, ko);
-      unpack8_bf16(vr, vo);
-      const int64_t page = valid ? slot / kPage * p.Hkv + h : 0;
+      uint8_t* buf = rows[(h - h0) & 1];
+      copy_wait<kStages - 2>();
+      __syncwarp();  // the other lanes' copies too, and they are done with the stage before
+      issue(h - h0 + kStages - 1);
+      const uint32_t at = ring + (h - h0) % kStages * (2 * kStageB);
+      const uint4 vraw = lds128(at + kStageB + lane * 16);
+      float2 ko[4], vo[4];
+      turn_row<D>(turn, p.k_weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), ko);
+      unpack8_bf16(vraw, vo);
+      const int64_t page = slot / kPage * p.Hkv + h;
       uint8_t* kp = p.k_cache + page * p.k_str;
       uint8_t* vp = p.v_cache + page * p.v_str;
       if constexpr (F::kFp8) {
@@ -245,44 +356,87 @@ __global__ void __launch_bounds__(kPage * D / 8) token_kernel(const TokenParams 
           ks = __ldg(p.k_scale + h);
           vs = __ldg(p.v_scale + h);
         }
-        if (!valid) continue;
-        *reinterpret_cast<uint2*>(kp + fp8_k_offset(off, j >> 1, D) + (j & 1) * 8) = quant8_fp8<F::kE5>(ko, ks);
-        const uint2 codes = quant8_fp8<F::kE5>(vo, vs);
+        const uint2 kq = quant8_fp8<F::kE5>(ko, Divisor(ks)), vq = quant8_fp8<F::kE5>(vo, Divisor(vs));
+        if (valid) {
+          *reinterpret_cast<uint2*>(kp + fp8_k_offset(off, j >> 1, D) + (j & 1) * 8) = kq;
+          if (page_run) {
+            *reinterpret_cast<uint2*>(buf + off * kVStride<D, FMT> + 8 * j) = vq;
+          } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          vp[(8 * j + i) * kPage + fp8_v_slot(off)] = static_cast<uint8_t>((i < 4 ? codes.x : codes.y) >> (8 * (i & 3)));
+            for (int i = 0; i < 8; ++i)
+              vp[(8 * j + i) * kPage + fp8_v_slot(off)] = static_cast<uint8_t>((i < 4 ? vq.x : vq.y) >> (8 * (i & 3)));
+          }
+        }
       } else if constexpr (FMT == kBF16) {
-        if (!valid) continue;
-        *reinterpret_cast<uint4*>(kp + k_chunk_offset(off, j, 2 * D)) = pack8_bf16(ko);
-        const uint32_t w[4] = {vr.x, vr.y, vr.z, vr.w};
+        if (valid) {
+          *reinterpret_cast<uint4*>(kp + k_chunk_offset(off, j, 2 * D)) = pack8_bf16(ko);
+          if (page_run) {
+            *reinterpret_cast<uint4*>(buf + off * kVStride<D, FMT> + 16 * j) = vraw;
+          } else {
+            const uint32_t w[4] = {vraw.x, vraw.y, vraw.z, vraw.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint16_t*>(vp + bf16_v_offset(8 * j + i, off)) = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint16_t*>(vp + bf16_v_offset(8 * j + i, off)) =
+                  static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+          }
+        }
       } else {
         uint8_t ks, vs;
         const uint32_t kw = quant8_fp4(ko, __ldg(p.k_scale + h), ks);
         const uint32_t vw = quant8_fp4(vo, __ldg(p.v_scale + h), vs);
-        if (!valid) continue;
-        *reinterpret_cast<uint32_t*>(kp + off * (D / 2) + 4 * j) = kw;
+        if (valid) {
+          *reinterpret_cast<uint32_t*>(kp + off * (D / 2) + 4 * j) = kw;
+          if (page_run) {
+            *reinterpret_cast<uint32_t*>(buf + off * kVStride<D, FMT> + 4 * j) = vw;
+          } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vp[fp4_v_offset(off, 4 * j + i)] = static_cast<uint8_t>(vw >> (8 * i));
-        if ((j & 1) == 0) {
-          kp[kPage * D / 2 + off * (D / 16) + j / 2] = ks;
-          vp[kPage * D / 2 + fp4_v_scale_offset(off, j / 2)] = vs;
+            for (int i = 0; i < 4; ++i) vp[fp4_v_offset(off, 4 * j + i)] = static_cast<uint8_t>(vw >> (8 * i));
+          }
+          if ((j & 1) == 0) {
+            kp[kPage * D / 2 + off * (D / 16) + j / 2] = ks;
+            vp[kPage * D / 2 + fp4_v_scale_offset(off, j / 2)] = vs;
+          }
         }
       }
+      if (page_run) {
+        // two buffers: the next head's rows go to the other one, and the one after
+        // comes behind the next barrier, which nobody passes before reading this one
+        __syncthreads();
+        write_v_page<D, FMT>(buf, vp);
+      }
     }
+    if (page_run) __syncthreads();  // the next 16 tokens start with the first buffer again
+  }
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kPage * D / 8, 768 / (2 * D)) token_kernel(const TokenParams p) {
+  __shared__ __align__(16) uint8_t ring_mem[D / 16 * Ring<D>::kBytes];
+  const uint32_t ring = smem_u32(ring_mem) + threadIdx.x / 32 * Ring<D>::kBytes;
+  if (blockIdx.x >= p.kv_ctas) {
+    const unsigned x = blockIdx.x - p.kv_ctas;
+    const int h = static_cast<int>(x / p.tiles) * p.q_chunk;
+    turn_rows<D>(p, ring, true, x % p.tiles, h, min(p.Hq, h + p.q_chunk));
+  } else {
+    const int h = static_cast<int>(blockIdx.x / p.kv_tiles) * p.kv_chunk, tile = blockIdx.x % p.kv_tiles;
+    if constexpr (FMT == kRowsOnly)
+      turn_rows<D>(p, ring, false, tile, h, min(p.Hkv, h + p.kv_chunk));
+    else
+      cache_rows<D, FMT>(p, ring, tile, h, min(p.Hkv, h + p.kv_chunk));
   }
 }
 
 template <int FMT>
 kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* where) {
   p.tiles = (p.T - 1) / kPage + 1;
-  p.kv_chunk = 1;
-  p.q_chunk = 4;
-  p.kv_chunks = (p.Hkv + p.kv_chunk - 1) / p.kv_chunk;
-  const int64_t ctas = static_cast<int64_t>(p.tiles) * (p.kv_chunks + (p.Hq + p.q_chunk - 1) / p.q_chunk);
+  p.aligned = FMT != kRowsOnly && p.T >= 256;
+  p.kv_tiles = p.tiles + (p.aligned ? 1 : 0);
+  p.kv_chunk = heads_per_cta(p.Hkv, p.kv_tiles, 8, KVQ_TUNE(kvw, 128) * sm_count() / D);
+  p.q_chunk = heads_per_cta(p.Hq, p.tiles, 32, KVQ_TUNE(qw, 2) * sm_count());
+  const int64_t kv_ctas = static_cast<int64_t>(p.kv_tiles) * ((p.Hkv + static_cast<int64_t>(p.kv_chunk) - 1) / p.kv_chunk);
+  const int64_t ctas = kv_ctas + static_cast<int64_t>(p.tiles) * ((p.Hq + static_cast<int64_t>(p.q_chunk) - 1) / p.q_chunk);
   if (ctas > 0x7FFFFFFF) return fail(KVQ_ERR_UNSUPPORTED, "%s: problem too large", where);
+  p.kv_ctas = static_cast<unsigned>(kv_ctas);
   const unsigned grid = static_cast<unsigned>(ctas);
   if (D == 64) {
     token_kernel<64, FMT><<<grid, 128, 0, s>>>(p);

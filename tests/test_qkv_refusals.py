@@ -201,14 +201,14 @@ wide = torch.zeros(T, Hq, 2 * D, dtype=bf16)
 
 @pytest.mark.parametrize("call,change,words", [
     (_rope, {"q": None, "k": None}, "q or k"), (_rope, {"q": torch.zeros(T, Hq, D)}, "q must be"), (_rope, {"k": torch.zeros(T, H, 128, dtype=bf16)}, "k must be"),
-    (_rope, {"q": wide[..., :D]}, "contiguous"), (_rope, {"q": wide[..., ::2]}, "contiguous"), (_rope, {"qo": None}, "q_out"),
-    (_rope, {"k": torch.zeros(T + 1, H, D, dtype=bf16)}, "same tokens"), (_rope, {"qo": torch.zeros(T, Hq + 1, D, dtype=bf16)}, "q_out must be"),
+    (_rope, {"q": wide[..., :D]}, "contiguous"), (_rope, {"q": wide[..., ::2]}, "contiguous"), (_rope, {"qo": None}, "needs q_out"),
+    (_rope, {"k": torch.zeros(T + 1, H, D, dtype=bf16)}, "tokens like"), (_rope, {"qo": torch.zeros(T, Hq + 1, D, dtype=bf16)}, "shaped like q"),
     (_rope, {"pos": torch.zeros(T, dtype=torch.int32)}, "positions"), (_rope, {"pos": torch.zeros(T + 1, dtype=torch.int64)}, "positions"),
     (_rope, {"pos": torch.zeros(2, T, dtype=torch.int64)}, "pair_axis"), (_rope, {"pos": torch.zeros(T, 2, dtype=torch.int64)[:, 0]}, "contiguous"),
     (_rope, {"inv": None}, "inv_freq"), (_rope, {"inv": torch.zeros(D // 2, dtype=torch.float64)}, "inv_freq"), (_rope, {"pos": None}, "need positions"),
     (_rope, {"pair_axis": torch.zeros(3, dtype=torch.int32)}, "pair_axis"), (_rope, {"q_weight": torch.zeros(D)}, "q_weight"),
     (_rope, {"k_weight": torch.zeros(D + 8, dtype=bf16)}, "k_weight"),
-    (_append, {"v": torch.zeros(T + 1, H, D, dtype=bf16)}, "v must"), (_append, {"q": torch.zeros(T + 1, Hq, D, dtype=bf16)}, "q must"),
+    (_append, {"v": torch.zeros(T + 1, H, D, dtype=bf16)}, "v must have"), (_append, {"v": torch.zeros(T, H + 1, D, dtype=bf16)}, "v must be"), (_append, {"q": torch.zeros(T + 1, Hq, D, dtype=bf16)}, "q must"),
     (_append, {"qo": None}, "q needs"), (_append, {"q": None}, "need q"), (_append, {"q8": torch.zeros(T, Hq, D)}, "q8 must"),
     (_append, {"q8": torch.zeros(T, Hq, D, dtype=torch.uint8)}, "q_scale"), (_append, {"slots": torch.zeros(T + 1, dtype=torch.int64)}, "slot_mapping"),
     (_append, {"ks": torch.ones(1)}, "k_scale"), (_append, {"cache_dtype": "bf16"}, "alloc_kv_cache"), (_append, {"per_token": True}, "alloc_kv_cache"),
