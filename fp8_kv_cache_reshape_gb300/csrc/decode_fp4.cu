@@ -12,8 +12,8 @@
 //
 // Bound: memory, 9/16 byte per element of K and V.
 //
-// Layout.  A warp takes one page (16 tokens of a KV head) at a time from a
-// ring of its own in shared memory, filled by 16-byte asynchronous copies: no
+// Layout.  A warp takes two pages (32 tokens of a KV head) at a time from two
+// stages of its own in shared memory, filled by 16-byte asynchronous copies: no
 // barrier, no producer warp, nothing between warps until a piece ends.  The
 // page format is the MMA operand order (m16n8k16, tokens as the rows of K Q^T,
 // dims as the rows of V^T P^T), so that a lane reads its whole share of a page
@@ -32,10 +32,14 @@ namespace {
 
 constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
 constexpr int kCtasPerSm = 4;
-constexpr int kMinPart = kWarps;      // pages of a part: a page per warp
+constexpr int kMinPart = 4;           // pages of a part, at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
+constexpr float kNone = -1e30f;
+// Sums of code products are below 2^27, so a smaller coefficient gives scores of zero
+// either way; one of zero would make a masked score, minus infinity, no number.
+constexpr float kLeast = 1e-30f;
 #define NEG_INF __int_as_float(0xff800000)
 
 template <int D>
@@ -43,9 +47,10 @@ struct Fp4 {
   static constexpr int kCodes = kPage * D / 2;
   static constexpr int kScales = kPage * D / 16;
   static constexpr int kPageB = kCodes + kScales;
-  static constexpr int kStageB = 2 * kPageB;           // K page, V page
-  static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kRingB = kStages * kStageB;
+  static constexpr int kPairB = 2 * kPageB;            // K page, V page
+  static constexpr int kStageB = 2 * kPairB;           // of two pages
+  static constexpr int kHalfScales = 2 * kScales * 2;  // both pages' V scales as float16
+  static constexpr int kRingB = 2 * kStageB + kHalfScales;
   static constexpr int kSmem = kWarps * kRingB;
   static constexpr int kTiles = D / 16;                // MMAs per page, of K and of V
   static constexpr int kRow = D + 8;                   // floats between the queries of a warp's output in shared memory
@@ -86,20 +91,8 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report) {
 // Pages of a part: the stream in `parts` equal ones, but at least a page per warp.
 KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, (total + parts - 1) / parts); }
 
-KVQ_DEVINL uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-KVQ_DEVINL uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
-  return v;
-}
-KVQ_DEVINL uint32_t lds8(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a));
-  return v;
+KVQ_DEVINL void sts128(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 KVQ_DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -114,12 +107,18 @@ KVQ_DEVINL void e2m1x8_to_f16x2(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
-// Bytes 0 and 2 of a word.
-KVQ_DEVINL void e2m1x4_to_f16x2(uint32_t w, uint32_t& h0, uint32_t& h2) {
+// Bytes 1 and 3 of a word.
+KVQ_DEVINL void e2m1x4_to_f16x2(uint32_t w, uint32_t& h1, uint32_t& h3) {
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, c;\n\t}"
-      : "=r"(h0), "=r"(h2)
+      "cvt.rn.f16x2.e2m1x2 %0, b;\n\tcvt.rn.f16x2.e2m1x2 %1, d;\n\t}"
+      : "=r"(h1), "=r"(h3)
       : "r"(w));
+}
+// Two E4M3 codes as f16x2.
+KVQ_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t x) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(h) : "r"(x));
+  return h;
 }
 KVQ_DEVINL uint32_t both(uint32_t h, bool high) { return __byte_perm(h, h, high ? 0x3232 : 0x1010); }
 
@@ -131,7 +130,7 @@ struct Attend {
   using F = Fp4<D>;
   uint32_t q[D / 8];  // query r, dims (D / 4) c .. + D / 4 - 1
   float coef[2];
-  float m[2], mb[2], l[2];
+  float m[2], mb[2], l[2];  // mb: m - kBase, or kNone, which any score passes
   float O[F::kTiles][4];
 
   KVQ_DEVINL void start(const Fp4Params& p, int b, int h, int lane) {
@@ -160,8 +159,9 @@ struct Attend {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       coef[i] = cf * __shfl_sync(0xffffffffu, inv_sigma, 8 * c + 4 * i);
+      if (coef[i] < kLeast) coef[i] = kLeast;
       m[i] = NEG_INF;
-      mb[i] = 0.f;
+      mb[i] = kNone;
       l[i] = 0.f;
     }
 #pragma unroll
@@ -170,121 +170,158 @@ struct Attend {
       for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
   }
 
-  // Tokens [lo, hi) of the page at shared address `page`.
-  KVQ_DEVINL void take(uint32_t page, int lo, int hi, int lane) {
+  // Two pages at shared address `stage`; tokens [lo[i], hi[i]) of page i are live
+  // (edge: not all are).  `half`: room for V's scales as float16.
+  KVQ_DEVINL void take(uint32_t stage, uint32_t half, bool edge, const int (&lo)[2], const int (&hi)[2], int lane) {
     const int r = lane >> 2, c = lane & 3;
-    const bool whole = lo <= 0 && hi >= kPage;
-    // ---- scores: rows are tokens, and each lane's dims share two scales (one at D = 64) per row
-    uint32_t kw[2][D / 32], ks[2][2];
+    // ---- V's scales, eight to a lane, as float16 for all; those of masked tokens may be anything: zero
+    {
+      constexpr int kLanes = F::kScales / 8;  // per page
+      const int pg = lane / kLanes;           // D = 64: the upper half of the lanes has none
+      if (pg < 2) {
+        uint2 w = lds64(stage + pg * F::kPairB + F::kPageB + F::kCodes + lane % kLanes * 8);
+        if (edge) {
+          uint32_t keep = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = r + 8 * i;
-      uint32_t s;
-      if constexpr (D == 128) {
-        const uint4 u = lds128(page + t * 64 + c * 16);
-        kw[i][0] = u.x;
-        kw[i][1] = u.y;
-        kw[i][2] = u.z;
-        kw[i][3] = u.w;
-        s = lds16(page + F::kCodes + t * 8 + 2 * c);
-      } else {
-        const uint2 u = lds64(page + t * 32 + c * 8);
-        kw[i][0] = u.x;
-        kw[i][1] = u.y;
-        s = lds8(page + F::kCodes + t * 4 + c);
+          for (int e = 0; e < 4; ++e) {
+            const int t = 2 * ((lane >> 1) & 3) + (e & 1) + 8 * (e >> 1);
+            if (t < (pg ? lo[1] : lo[0]) || t >= (pg ? hi[1] : hi[0])) keep &= ~(0xffu << (8 * e));
+          }
+          w.x &= keep;
+          w.y &= keep;
+        }
+        uint4 h;
+        e4m3x4_to_f16x2x2(w.x, h.x, h.y);
+        e4m3x4_to_f16x2x2(w.y, h.z, h.w);
+        sts128(half + lane * 16, h);
       }
-      uint32_t lo2, hi2;
-      e4m3x4_to_f16x2x2(s, lo2, hi2);
-      ks[i][0] = both(lo2, false);
-      ks[i][1] = both(lo2, D == 128);
     }
-    float s[2][4] = {};
+    // ---- scores: rows are tokens, and each lane's dims share two scales (one at D = 64) per row
+    float t[2][4];
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      uint32_t a[2][4];
+    for (int pg = 0; pg < 2; ++pg) {
+      const uint32_t page = stage + pg * F::kPairB;
+      uint32_t kw[2][D / 32], ks[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        e2m1x8_to_f16x2(kw[i][w], a[i]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) a[i][e] = hmul2(a[i][e], ks[i][w / 2]);
+        const int tok = r + 8 * i;
+        if constexpr (D == 128) {
+          const uint4 u = lds128(page + tok * 64 + c * 16);
+          kw[i][0] = u.x;
+          kw[i][1] = u.y;
+          kw[i][2] = u.z;
+          kw[i][3] = u.w;
+          const uint32_t s = e4m3x2_to_f16x2(lds16(page + F::kCodes + tok * 8 + 2 * c));
+          ks[i][0] = both(s, false);
+          ks[i][1] = both(s, true);
+        } else {
+          const uint2 u = lds64(page + tok * 32 + c * 8);
+          kw[i][0] = u.x;
+          kw[i][1] = u.y;
+          ks[i][0] = ks[i][1] = both(e4m3x2_to_f16x2(lds8(page + F::kCodes + tok * 4 + c)), false);
+        }
       }
-      mma_f16(s[0], a[0][0], a[1][0], a[0][1], a[1][1], q[4 * w], q[4 * w + 1], s[0]);
-      mma_f16(s[1], a[0][2], a[1][2], a[0][3], a[1][3], q[4 * w + 2], q[4 * w + 3], s[1]);
-    }
-    // s[0][0], [1]: token r, queries 2c, 2c + 1; [2], [3]: token r + 8
-    float x[4];
+      float s[2][4] = {};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = (s[0][e] + s[1][e]) * coef[e & 1];
-    if (!whole) {
+      for (int w = 0; w < D / 32; ++w) {
+        uint32_t a[2][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = r + 8 * (e >> 1);
-        if (t < lo || t >= hi) x[e] = NEG_INF;
+        for (int i = 0; i < 2; ++i) {
+          e2m1x8_to_f16x2(kw[i][w], a[i]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[i][e] = hmul2(a[i][e], ks[i][w / 2]);
+        }
+        mma_f16(s[0], a[0][0], a[1][0], a[0][1], a[1][1], q[4 * w], q[4 * w + 1], s[0]);
+        mma_f16(s[1], a[0][2], a[1][2], a[0][3], a[1][3], q[4 * w + 2], q[4 * w + 3], s[1]);
+      }
+      // [0], [1]: token r, queries 2c, 2c + 1; [2], [3]: token r + 8
+#pragma unroll
+      for (int e = 0; e < 4; ++e) t[pg][e] = s[0][e] + s[1][e];
+      if (edge) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = r + 8 * (e >> 1);
+          if (tok < lo[pg] || tok >= hi[pg]) t[pg][e] = NEG_INF;
+        }
       }
     }
     // ---- stabilizer: moved only when a score passes it by more than kLag
-    const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
-    if (__any_sync(0xffffffffu, x0 > m[0] + kLag || x1 > m[1] + kLag)) {
-      float n[2] = {x0, x1};
+    float x[2][4];
+#pragma unroll
+    for (int pg = 0; pg < 2; ++pg)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+    const float top = fmax3(fmax3(x[0][0], x[0][2], fmaxf(x[1][0], x[1][2])), x[0][1], fmax3(x[0][3], x[1][1], x[1][3]));
+    if (__any_sync(0xffffffffu, top > kLag + kBase)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
+        float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i])) * coef[i];
 #pragma unroll
-        for (int o = 4; o < 32; o <<= 1) n[i] = fmaxf(n[i], __shfl_xor_sync(0xffffffffu, n[i], o));
-        n[i] = fmaxf(n[i], m[i]);
-        const float alpha = m[i] == NEG_INF ? 0.f : ex2(m[i] - n[i]);
-        l[i] *= alpha;
+        for (int o = 4; o < 32; o <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+        n = fmaxf(n, m[i]);
+        if (n > m[i]) {  // the same in every lane of the query
+          const float alpha = ex2(m[i] - n);
+          l[i] *= alpha;
 #pragma unroll
-        for (int d = 0; d < F::kTiles; ++d) {
-          O[d][i] *= alpha;
-          O[d][2 + i] *= alpha;
+          for (int d = 0; d < F::kTiles; ++d) {
+            O[d][i] *= alpha;
+            O[d][2 + i] *= alpha;
+          }
+          m[i] = n;
+          mb[i] = n - kBase;
         }
-        m[i] = n[i];
-        mb[i] = n[i] == NEG_INF ? 0.f : n[i] - kBase;
       }
-    }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = ex2(x[e] - mb[e & 1]);
-    l[0] += x[0] + x[2];
-    l[1] += x[1] + x[3];
-    const uint32_t p0 = movmatrix_t(pack_f16x2(x[0], x[1])), p1 = movmatrix_t(pack_f16x2(x[2], x[3]));
+      for (int pg = 0; pg < 2; ++pg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+    }
+    uint32_t p[2][2];
+#pragma unroll
+    for (int pg = 0; pg < 2; ++pg) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[pg][e] = ex2(x[pg][e]);
+      l[0] += x[pg][0] + x[pg][2];
+      l[1] += x[pg][1] + x[pg][3];
+      p[pg][0] = movmatrix_t(pack_f16x2(x[pg][0], x[pg][1]));
+      p[pg][1] = movmatrix_t(pack_f16x2(x[pg][2], x[pg][3]));
+    }
     // ---- outputs: rows are 16 dims that share a token's scale, which multiplies the weights
-    const uint32_t v = page + F::kPageB;
-    uint32_t keep = 0xffffffffu;  // scale bytes of masked tokens may be anything: zero
-    if (!whole) {
+    __syncwarp();  // the scales are there
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 2 * c + (e & 1) + 8 * (e >> 1);
-        if (t < lo || t >= hi) keep &= ~(0xffu << (8 * e));
-      }
-    }
+    for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
-    for (int half = 0; half < D / 64; ++half) {
-      const uint4 codes = lds128(v + half * 512 + lane * 16);
-      const uint4 scales = lds128(v + F::kCodes + half * 64 + c * 16);
-      const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-      const uint32_t sw[4] = {scales.x, scales.y, scales.z, scales.w};
+      for (int quad = 0; quad < 2; ++quad) {
+        float f[2][4] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t s0, s1;
-        e4m3x4_to_f16x2x2(sw[i] & keep, s0, s1);
-        // bytes are tokens, nibbles dims 2r and 2r + 1: bytes 0 and 2 of `even`
-        // (`odd`) are dim 2r (2r + 1) of tokens 2c, 2c + 1 and of 2c + 8, 2c + 9
-        constexpr uint32_t kLow = 0x000F000Fu;
-        const uint32_t w4 = cw[i] >> 4, w8 = cw[i] >> 8;
-        const uint32_t even = (cw[i] & kLow) | (w4 & ~kLow), odd = (w4 & kLow) | (w8 & ~kLow);
-        uint32_t a0, a1, a2, a3;
-        e2m1x4_to_f16x2(even, a0, a2);
-        e2m1x4_to_f16x2(odd, a1, a3);
-        float f[4];
-        const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-        mma_f16(f, a0, a1, a2, a3, hmul2(p0, s0), hmul2(p1, s1), zero);
-        float(&o)[4] = O[half * 4 + i];
-        const float2 u = fadd2(make_float2(o[0], o[1]), make_float2(f[0], f[1]));
-        const float2 z = fadd2(make_float2(o[2], o[3]), make_float2(f[2], f[3]));
-        o[0] = u.x;
-        o[1] = u.y;
-        o[2] = z.x;
-        o[3] = z.y;
+        for (int pg = 0; pg < 2; ++pg) {
+          const uint2 codes = lds64(stage + pg * F::kPairB + F::kPageB + h * 512 + lane * 16 + quad * 8);
+          const uint4 scales = lds128(half + pg * (2 * F::kScales) + h * 128 + c * 32 + quad * 16);
+          const uint32_t cw[2] = {codes.x, codes.y};
+          const uint32_t sw[2][2] = {{scales.x, scales.y}, {scales.z, scales.w}};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // bytes are tokens, nibbles dims 2r and 2r + 1: bytes 1 and 3 of `even`
+            // (`odd`) become dim 2r (2r + 1) of tokens 2c, 2c + 1 and of 2c + 8, 2c + 9
+            constexpr uint32_t kHigh = 0xF000F000u;
+            const uint32_t w4 = cw[i] << 4, w8 = cw[i] << 8;
+            const uint32_t even = (w4 & kHigh) | (w8 & ~kHigh), odd = (cw[i] & kHigh) | (w4 & ~kHigh);
+            uint32_t a0, a1, a2, a3;
+            e2m1x4_to_f16x2(even, a0, a2);
+            e2m1x4_to_f16x2(odd, a1, a3);
+            mma_f16(f[i], a0, a1, a2, a3, hmul2(p[pg][0], sw[i][0]), hmul2(p[pg][1], sw[i][1]), f[i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float(&o)[4] = O[h * 4 + quad * 2 + i];
+          const float2 u = fadd2(make_float2(o[0], o[1]), make_float2(f[i][0], f[i][1]));
+          const float2 z = fadd2(make_float2(o[2], o[3]), make_float2(f[i][2], f[i][3]));
+          o[0] = u.x;
+          o[1] = u.y;
+          o[2] = z.x;
+          o[3] = z.y;
+        }
       }
     }
   }
@@ -365,45 +402,63 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
     const int n = min(end - pos, sp.n - pg0);
     const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks + sp.first + pg0;
 
-    // ---- this warp's pages: warp, warp + kWarps, ...
-    const int count = n > warp ? (n - warp + kWarps - 1) / kWarps : 0;
-    int ids = 0;         // block ids of 32 pages, one per lane
-    unsigned valid = 0;  // bit i: stage i holds a page
+    // ---- this warp's pairs of pages: pairs warp, warp + kWarps, ...
+    const int pairs = (n + 1) / 2;
+    const int count = pairs > warp ? (pairs - warp + kWarps - 1) / kWarps : 0;
+    int ids = -1;        // block ids of 16 pairs, one page per lane
+    unsigned valid = 0;  // bit 2 s + i: page i of stage s is there
     auto issue = [&](int i) {
       if (i < count) {
-        if ((i & 31) == 0) {
-          const int j = i + lane;
-          ids = j < count ? table[warp + j * kWarps] : 0;
+        if ((i & 15) == 0) {
+          const int j = i + (lane >> 1), page = 2 * (warp + j * kWarps) + (lane & 1);
+          ids = j < count && page < n ? table[page] : -1;
         }
-        const int id = __shfl_sync(0xffffffffu, ids, i & 31);
-        const int st = i % F::kStages;
-        const bool ok = static_cast<unsigned>(id) < static_cast<uint64_t>(p.num_blocks);
-        valid = ok ? valid | (1u << st) : valid & ~(1u << st);
-        if (ok) {
-          const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
-          const uint8_t* k = p.k_cache + page * p.k_str;
-          const uint8_t* v = p.v_cache + page * p.v_str;
+        const int st = i & 1;
+        valid &= ~(3u << (2 * st));
 #pragma unroll
-          for (int x = lane * 16; x < F::kStageB; x += 512)
-            copy16(ring + st * F::kStageB + x, x < F::kPageB ? k + x : v + (x - F::kPageB));
-        } else if (lane == 0) {
-          set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+        for (int pg = 0; pg < 2; ++pg) {
+          const int id = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + pg);
+          if (static_cast<unsigned>(id) < static_cast<uint64_t>(p.num_blocks)) {
+            valid |= 1u << (2 * st + pg);
+            const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
+            const uint8_t* k = p.k_cache + page * p.k_str + lane * 16;
+            const uint8_t* v = p.v_cache + page * p.v_str + lane * 16;
+            const uint32_t at = ring + st * F::kStageB + pg * F::kPairB + lane * 16;
+#pragma unroll
+            for (int x = 0; x < F::kPageB; x += 512) {
+              if (x + 512 <= F::kPageB || x + lane * 16 < F::kPageB) {
+                copy16(at + x, k + x);
+                copy16(at + F::kPageB + x, v + x);
+              }
+            }
+          } else if (lane == 0 && 2 * (warp + i * kWarps) + pg < n) {
+            set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+          }
         }
       }
       copy_commit();
     };
     at.start(p, b, h, lane);
-#pragma unroll
-    for (int i = 0; i < F::kStages - 1; ++i) issue(i);
+    issue(0);
+    issue(1);
     for (int i = 0; i < count; ++i) {
-      copy_wait<F::kStages - 2>();
-      __syncwarp();  // every lane's copies are there, and every lane is done with the stage before
-      issue(i + F::kStages - 1);
-      const int st = i % F::kStages;
-      if (valid >> st & 1) {
-        const int tok = (sp.first + pg0 + warp + i * kWarps) * kPage;
-        at.take(ring + st * F::kStageB, sp.lo - tok, sp.len - tok, lane);
+      copy_wait<1>();
+      __syncwarp();  // every lane's copies are there
+      const int st = i & 1;
+      const unsigned have = valid >> (2 * st) & 3;
+      if (have) {
+        const int tok = (sp.first + pg0 + 2 * (warp + i * kWarps)) * kPage;
+        int lo[2], hi[2];
+#pragma unroll
+        for (int pg = 0; pg < 2; ++pg) {
+          lo[pg] = sp.lo - tok - pg * kPage;
+          hi[pg] = have >> pg & 1 ? sp.len - tok - pg * kPage : 0;
+        }
+        const bool edge = lo[0] > 0 || lo[1] > 0 || hi[0] < kPage || hi[1] < kPage;
+        at.take(ring + st * F::kStageB, ring + 2 * F::kStageB, edge, lo, hi, lane);
       }
+      __syncwarp();  // every lane is done with the stage
+      issue(i + 2);
     }
     copy_wait<0>();
     __syncwarp();

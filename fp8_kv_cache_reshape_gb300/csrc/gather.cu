@@ -44,202 +44,210 @@ KVQ_DEVINL void value8_fp4(uint32_t c, uint8_t block, float s, float2 (&x)[4]) {
   }
 }
 
-// Bytes between the token rows of a page in shared memory: those that a thread
-// writes together, and the two halves of a BF16 page, fall into different banks.
+// One thread's eight dims of a token, from the pages themselves.
 template <int D, int FMT>
-constexpr int kRowStride = FMT == kBF16 ? 2 * D + 8 : (FMT == kFP4 ? D / 2 : D) + 16;
-
-// What a thread brings of a V page: four words of four (FP8, FP4) or eight
-// tokens (BF16: two 16-byte rows), and where they go.
-template <int D, int FMT>
-struct VPart {
-  static constexpr int kThreads = FMT == kFP4 ? D / 2 : D;  // that take part
-  uint32_t w[FMT == kBF16 ? 8 : 4];
-
-  KVQ_DEVINL void load(const uint8_t* vp, int x) {
-    if (x >= kThreads) return;
-    if constexpr (FMT == kBF16) {
-      const int half = x & 1, d = x & ~1;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4*>(vp + bf16_v_offset(d + i, 8 * half));
-        w[4 * i] = u.x;
-        w[4 * i + 1] = u.y;
-        w[4 * i + 2] = u.z;
-        w[4 * i + 3] = u.w;
-      }
-    } else {
-      int at, step;
-      if constexpr (FMT == kFP4) {
-        at = (x >> 5) * 512 + ((x >> 4) & 1) * 256 + ((x >> 2) & 3) * 16 + (x & 3) * 4;
-        step = 64;
-      } else {
-        at = (x & ~3) * kPage + (x & 3) * 4;
-        step = kPage;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(vp + at + i * step);
-    }
-  }
-  KVQ_DEVINL void store(uint8_t* rows, int x) const {
-    constexpr int S = kRowStride<D, FMT>;
-    if (x >= kThreads) return;
-    if constexpr (FMT == kBF16) {
-      const int half = x & 1, d = x & ~1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // tokens 8 half + 2i, + 1: dims d, d + 1
-        *reinterpret_cast<uint32_t*>(rows + (8 * half + 2 * i) * S + 2 * d) = __byte_perm(w[i], w[4 + i], 0x5410);
-        *reinterpret_cast<uint32_t*>(rows + (8 * half + 2 * i + 1) * S + 2 * d) = __byte_perm(w[i], w[4 + i], 0x7632);
-      }
-    } else {
-      const int c = FMT == kFP4 ? (x >> 2) & 3 : x & 3;
-      const int col = FMT == kFP4 ? 32 * (x >> 5) + 8 * (x & 3) + 4 * ((x >> 4) & 1) : x & ~3;
-      uint32_t o[4];
-      transpose4(w, o);  // a word's bytes are tokens 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t*>(rows + (2 * c + (i & 1) + 8 * (i >> 1)) * S + col) = o[i];
-    }
-  }
-};
-
-// What a thread brings of its own token: eight dims of K and their scales.
-template <int D, int FMT>
-struct KPart {
-  uint4 k;
-  float ks, vs;
-
-  KVQ_DEVINL void load(const GatherParams& p, const uint8_t* kp, const uint8_t* vp, int off, int j, int h) {
-    if constexpr (FMT == kBF16) {
-      k = *reinterpret_cast<const uint4*>(kp + k_chunk_offset(off, j, 2 * D));
-    } else if constexpr (FMT == kFP4) {
-      k.x = *reinterpret_cast<const uint32_t*>(kp + off * (D / 2) + 4 * j);
-      k.y = kp[kPage * D / 2 + off * (D / 16) + j / 2];
-      k.z = vp[kPage * D / 2 + fp4_v_scale_offset(off, j / 2)];
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(kp + fp8_k_offset(off, j >> 1, D) + (j & 1) * 8);
-      k.x = u.x;
-      k.y = u.y;
-    }
-    if constexpr (Format<FMT>::kToken) {
-      const float* tail = reinterpret_cast<const float*>(vp + kPage * D);
-      ks = tail[off];
-      vs = tail[kPage + off];
-    } else if constexpr (FMT != kBF16) {
-      ks = __ldg(p.k_scale + h);
-      vs = __ldg(p.v_scale + h);
-    }
-  }
-};
-
-// One thread's eight dims of V of a token, from the page itself.
-template <int D, int FMT>
-KVQ_DEVINL uint4 v_of_page(const uint8_t* vp, int off, int j) {
-  uint32_t w[4] = {0, 0, 0, 0};
+KVQ_DEVINL void one_token(const GatherParams& p, const uint8_t* kp, const uint8_t* vp, int off, int j, int h, uint4& k, uint4& v) {
+  using F = Format<FMT>;
   if constexpr (FMT == kBF16) {
+    k = *reinterpret_cast<const uint4*>(kp + k_chunk_offset(off, j, 2 * D));
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       w[i >> 1] |= static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vp + bf16_v_offset(8 * j + i, off))) << (16 * (i & 1));
-  } else if constexpr (FMT == kFP4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[0] |= static_cast<uint32_t>(vp[fp4_v_offset(off, 4 * j + i)]) << (8 * i);
+    v = make_uint4(w[0], w[1], w[2], w[3]);
   } else {
+    float2 kf[4], vf[4];
+    if constexpr (FMT == kFP4) {
+      uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i >> 2] |= static_cast<uint32_t>(vp[(8 * j + i) * kPage + fp8_v_slot(off)]) << (8 * (i & 3));
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// ... and from the page's token rows in shared memory.
-template <int D, int FMT>
-KVQ_DEVINL uint4 v_of_rows(const uint8_t* rows, int off, int j) {
-  const uint8_t* at = rows + off * kRowStride<D, FMT>;
-  uint4 v = make_uint4(0, 0, 0, 0);
-  if constexpr (FMT == kFP4) {
-    v.x = *reinterpret_cast<const uint32_t*>(at + 4 * j);
-  } else {
-    const uint2* u = reinterpret_cast<const uint2*>(at + (FMT == kBF16 ? 16 : 8) * j);
-    v.x = u[0].x;
-    v.y = u[0].y;
-    if constexpr (FMT == kBF16) {
-      v.z = u[1].x;
-      v.w = u[1].y;
+      for (int i = 0; i < 4; ++i) w |= static_cast<uint32_t>(vp[fp4_v_offset(off, 4 * j + i)]) << (8 * i);
+      value8_fp4(*reinterpret_cast<const uint32_t*>(kp + off * (D / 2) + 4 * j), kp[kPage * D / 2 + off * (D / 16) + j / 2],
+                 __ldg(p.k_scale + h), kf);
+      value8_fp4(w, vp[kPage * D / 2 + fp4_v_scale_offset(off, j / 2)], __ldg(p.v_scale + h), vf);
+    } else {
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        w[i >> 2] |= static_cast<uint32_t>(vp[(8 * j + i) * kPage + fp8_v_slot(off)]) << (8 * (i & 3));
+      const float* tail = reinterpret_cast<const float*>(vp + kPage * D);
+      value8_fp8<F::kE5>(*reinterpret_cast<const uint2*>(kp + fp8_k_offset(off, j >> 1, D) + (j & 1) * 8),
+                         F::kToken ? tail[off] : __ldg(p.k_scale + h), kf);
+      value8_fp8<F::kE5>(make_uint2(w[0], w[1]), F::kToken ? tail[kPage + off] : __ldg(p.v_scale + h), vf);
     }
+    k = pack8_bf16(kf);
+    v = pack8_bf16(vf);
   }
-  return v;
 }
 
-// A tile's tokens, a chunk of heads; a thread holds dims 8 j .. 8 j + 7 of a
-// token.  Where the tokens fill a page in order, its V part comes in whole words that are
-// transposed in registers and meet in shared memory; the next head's loads are
-// in flight meanwhile.
+// Whole pages pass through shared memory, their V part turned by transposing
+// matrix loads: a matrix's rows are eight 16-byte chunks of the page, and a lane
+// gets two rows' values of the same two (FP8, FP4) or one (BF16) tokens.  Rows
+// are chosen so that a lane's four matrices hold neighbouring dims, and chunks
+// placed so that a matrix's rows lie in different banks.
+template <int D, int FMT>
+struct Staged {
+  using F = Format<FMT>;
+  static constexpr int kKPage = static_cast<int>(k_page_bytes(FMT, D)), kVPage = static_cast<int>(v_page_bytes(FMT, D));
+  static constexpr int kStageB = kKPage + kVPage;
+  static constexpr int kStages = 4;
+  static constexpr int kThreads = kPage * D / 8;
+  [[maybe_unused]] static constexpr int kCodes = FMT == kFP4 ? kPage * D / 2 : kPage * D * (FMT == kBF16 ? 2 : 1);
+
+  // Where the V page's 16-byte chunk x goes.
+  static KVQ_DEVINL int place(int x) {
+    if constexpr (F::kFp8) {
+      return x < kCodes / 16 ? x ^ (((x >> 3) & 3) << 1) : x;  // row x is dim x
+    } else if constexpr (FMT == kBF16) {
+      return x ^ ((x >> 4) & 1) ^ (((x >> 5) & 1) << 2);  // row x / 2
+    } else {
+      return x;
+    }
+  }
+  static KVQ_DEVINL void copy(uint32_t stage, const uint8_t* kp, const uint8_t* vp) {
+#pragma unroll
+    for (int x = threadIdx.x; x < kStageB / 16; x += kThreads) {
+      if (x < kKPage / 16)
+        copy16(stage + x * 16, kp + x * 16);
+      else
+        copy16(stage + kKPage + place(x - kKPage / 16) * 16, vp + (x - kKPage / 16) * 16);
+    }
+  }
+
+  // This thread's part of a head's rows: put(token of the tile, dim, is_v, eight dims).
+  template <typename Put>
+  static KVQ_DEVINL void rows(uint32_t stage, float ks, float vs, Put put) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int i = lane & 7, m = lane >> 3, u = lane >> 2, c = lane & 3;
+    const uint32_t v = stage + kKPage;
+    uint32_t w[4];
+    if constexpr (FMT == kBF16) {
+      const int t = threadIdx.x / (D / 8), j = threadIdx.x % (D / 8);
+      put(t, 8 * j, false, lds128(stage + k_chunk_offset(t, j, 2 * D)));
+      const int base = 32 * (warp >> 1), half = warp & 1;
+      const int d = base + 8 * (i >> 1) + 2 * m + (i & 1);
+      ldsm_x4_t(v + place(2 * d + (half ^ ((d >> 2) & 1))) * 16, w);
+      put(8 * half + u, base + 8 * c, true, make_uint4(w[0], w[1], w[2], w[3]));
+    } else if constexpr (F::kFp8) {
+      constexpr int kVWarps = D / 32;  // the others take K
+      if (warp < kVWarps) {
+        const int d = 32 * warp + 8 * (i >> 1) + 2 * m + (i & 1);
+        ldsm_x4_t(v + place(d) * 16, w);
+        const int t = u & 1 ? 7 + u : u;  // slots 2u, 2u + 1 hold tokens t, t + 1
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t pick = e ? 0x7531 : 0x6420;
+          float2 x[4];
+          value8_fp8<F::kE5>(make_uint2(__byte_perm(w[0], w[1], pick), __byte_perm(w[2], w[3], pick)),
+                             F::kToken ? lds_f32(v + kCodes + (kPage + t + e) * 4) : vs, x);
+          put(t + e, 32 * warp + 8 * c, true, pack8_bf16(x));
+        }
+      } else {
+        const int y = threadIdx.x - 32 * kVWarps, j = y % (D / 8);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = y / (D / 8) + 8 * e;
+          float2 x[4];
+          value8_fp8<F::kE5>(lds64(stage + fp8_k_offset(t, j >> 1, D) + (j & 1) * 8), F::kToken ? lds_f32(v + kCodes + t * 4) : ks, x);
+          put(t, 8 * j, false, pack8_bf16(x));
+        }
+      }
+    } else {
+      constexpr int kVWarps = D / 64;
+      if (warp < kVWarps) {
+        ldsm_x4_t(v + (warp * 32 + (2 * m + (i & 1)) * 4 + (i >> 1)) * 16, w);
+        // the lane has 16 dims of tokens 2c + 8 hi, + 1; with its neighbour in hi it
+        // changes halves, so that they write 32 bytes of a row between them
+        const int b = u >> 1, hi = u & 1;
+        uint32_t code[4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9; dims 8 hi .. + 7 of the block
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t pick = e ? 0x7531 : 0x6420;
+          const uint32_t q0 = __byte_perm(w[0], w[1], pick), q1 = __byte_perm(w[2], w[3], pick);
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, hi ? q0 : q1, 4);
+          code[e] = hi ? got : q0;
+          code[2 + e] = hi ? q1 : got;
+        }
+        const uint32_t scales = lds32(v + kCodes + warp * 64 + c * 16 + b * 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float2 x[4];
+          value8_fp4(code[e], static_cast<uint8_t>(scales >> (8 * e)), vs, x);
+          put(2 * c + (e & 1) + 8 * (e >> 1), 64 * warp + 16 * b + 8 * hi, true, pack8_bf16(x));
+        }
+      } else if (warp < kVWarps + D / 32) {
+        const int y = threadIdx.x - 32 * kVWarps, j = y % (D / 8);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int t = y / (D / 8) + 8 * e;
+          float2 x[4];
+          value8_fp4(lds32(stage + t * (D / 2) + 4 * j), static_cast<uint8_t>(lds8(stage + kCodes + t * (D / 16) + j / 2)), ks, x);
+          put(t, 8 * j, false, pack8_bf16(x));
+        }
+      }
+    }
+  }
+};
+
+// A tile's tokens, a chunk of heads.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPage * D / 8) gather_kernel(const GatherParams p) {
-  using F = Format<FMT>;
+  using S = Staged<D, FMT>;
   constexpr int LPT = D / 8;
   __shared__ TileTokens tt;
-  __shared__ __align__(16) uint8_t rows[2][kPage * kRowStride<D, FMT>];
+  __shared__ __align__(128) uint8_t stages[S::kStages * S::kStageB];
+  const uint32_t ring = smem_u32(stages);
   const int x = threadIdx.x, t = x / LPT, j = x % LPT;
   const int tile = blockIdx.x % p.tiles;
-  const int h0 = blockIdx.x / p.tiles * p.chunk, h1 = min(p.Hkv, h0 + p.chunk);
+  const int h0 = blockIdx.x / p.tiles * p.chunk, n = min(p.Hkv - h0, p.chunk);
   if (x < 32) find_tokens(tt, p.slots, p.T, p.num_slots, tile, p.aligned, p.dev_status);
   __syncthreads();
-  const int n = tt.n;
-  for (int r = 0; r < n; r += kPage) {
-    const bool valid = r + t < n, page_run = tt.page[r / kPage];
-    const int token = tt.token[valid ? r + t : r];
-    const int64_t slot = tt.slot[valid ? r + t : r];
-    const int off = static_cast<int>(slot % kPage);
-    const int64_t page = slot / kPage * p.Hkv + h0;
-    const uint8_t* kp = p.k_cache + page * p.k_str;
-    const uint8_t* vp = p.v_cache + page * p.v_str;
-    KPart<D, FMT> k;
-    VPart<D, FMT> part;
-    k.load(p, kp, vp, off, j, h0);
-    if (page_run) part.load(vp, x);
-    for (int h = h0; h < h1; ++h) {
-      const KPart<D, FMT> now = k;
-      uint4 v;
-      if (page_run) {
-        uint8_t* buf = rows[(h - h0) & 1];  // the other one is read no longer when it is written again, a barrier later
-        part.store(buf, x);
-        if (h + 1 < h1) part.load(vp + p.v_str, x);
-      } else {
-        v = v_of_page<D, FMT>(vp, off, j);
-      }
-      kp += p.k_str;
-      vp += p.v_str;
-      if (h + 1 < h1) k.load(p, kp, vp, off, j, h + 1);
-      if (page_run) {
-        __syncthreads();
-        v = v_of_rows<D, FMT>(rows[(h - h0) & 1], off, j);
-      }
-      if (!valid) continue;
-      uint4 ko = now.k;
-      if constexpr (FMT != kBF16) {
-        float2 kf[4], vf[4];
-        if constexpr (FMT == kFP4) {
-          value8_fp4(now.k.x, static_cast<uint8_t>(now.k.y), now.ks, kf);
-          value8_fp4(v.x, static_cast<uint8_t>(now.k.z), now.vs, vf);
-        } else {
-          value8_fp8<F::kE5>(make_uint2(now.k.x, now.k.y), now.ks, kf);
-          value8_fp8<F::kE5>(make_uint2(v.x, v.y), now.vs, vf);
+  const int tokens = tt.n;
+  for (int r = 0; r < tokens; r += kPage) {
+    if (tt.page[r / kPage]) {
+      const int64_t page = tt.slot[r] / kPage * p.Hkv + h0;
+      const uint8_t* kp = p.k_cache + page * p.k_str;
+      const uint8_t* vp = p.v_cache + page * p.v_str;
+      auto issue = [&](int i) {
+        if (i < n) S::copy(ring + i % S::kStages * S::kStageB, kp + i * p.k_str, vp + i * p.v_str);
+        copy_commit();
+      };
+#pragma unroll
+      for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+      for (int i = 0; i < n; ++i) {
+        copy_wait<S::kStages - 2>();
+        __syncthreads();  // everybody's copies are there, and the stage before is read
+        issue(i + S::kStages - 1);
+        float ks = 1.f, vs = 1.f;
+        if (FMT != kBF16 && !Format<FMT>::kToken) {
+          ks = __ldg(p.k_scale + h0 + i);
+          vs = __ldg(p.v_scale + h0 + i);
         }
-        ko = pack8_bf16(kf);
-        v = pack8_bf16(vf);
+        S::rows(ring + i % S::kStages * S::kStageB, ks, vs, [&](int token, int d, bool is_v, const uint4& o) {
+          const int64_t at = (static_cast<int64_t>(tt.token[r + token]) * p.Hkv + h0 + i) * D + d;
+          *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + at) = o;
+        });
       }
-      const int64_t at = (static_cast<int64_t>(token) * p.Hkv + h) * D + 8 * j;
-      *reinterpret_cast<uint4*>(p.k_out + at) = ko;
-      *reinterpret_cast<uint4*>(p.v_out + at) = v;
+      __syncthreads();  // the stages are free for the next 16 tokens
+    } else if (r + t < tokens) {
+      const int64_t slot = tt.slot[r + t];
+      const int64_t page = slot / kPage * p.Hkv + h0;
+      for (int i = 0; i < n; ++i) {
+        uint4 k, v;
+        one_token<D, FMT>(p, p.k_cache + (page + i) * p.k_str, p.v_cache + (page + i) * p.v_str,
+                          static_cast<int>(slot % kPage), j, h0 + i, k, v);
+        const int64_t at = (static_cast<int64_t>(tt.token[r + t]) * p.Hkv + h0 + i) * D + 8 * j;
+        *reinterpret_cast<uint4*>(p.k_out + at) = k;
+        *reinterpret_cast<uint4*>(p.v_out + at) = v;
+      }
     }
-    if (page_run) __syncthreads();  // the next 16 tokens start with the first buffer again
   }
 }
 
 template <int FMT>
 kvq_status_t launch_gather(GatherParams& p, int D, cudaStream_t s) {
-  p.aligned = p.T >= KVQ_TUNE(galign, 64);
+  p.aligned = p.T >= 64;
   p.tiles = (p.T - 1) / kPage + 1 + (p.aligned ? 1 : 0);
-  p.chunk = heads_per_cta(p.Hkv, p.tiles, KVQ_TUNE(gmost, 8), KVQ_TUNE(gctas, 8) * sm_count());
+  p.chunk = heads_per_cta(p.Hkv, p.tiles, 4, 4 * sm_count());
   const int64_t ctas = static_cast<int64_t>(p.tiles) * ((p.Hkv + static_cast<int64_t>(p.chunk) - 1) / p.chunk);
   if (ctas > 0x7FFFFFFF) return fail(KVQ_ERR_UNSUPPORTED, "gather_cache: problem too large");
   const unsigned grid = static_cast<unsigned>(ctas);
