@@ -22,6 +22,7 @@
 // dims 2r, 2r + 1 of each 16 of V.
 #include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "kvq_host.h"
 #include "kvq_rows.cuh"
@@ -31,8 +32,9 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 3;
 constexpr int kMinPart = 4;           // pages of a part, at least
+constexpr int kHinted = 16;             // pages that hint_pages() asks for: two pairs per warp
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
@@ -78,9 +80,11 @@ struct Fp4Params {
 struct Span {
   int lo, len, first, n;
 };
-KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report) {
+// early: before the preceding kernel has completed (the value may still change, and
+// leaves no line in L1).
+KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false, bool early = false) {
   Span s;
-  const int L = p.seq_lens[b];
+  const int L = early ? ld_l2only_s32(p.seq_lens + b) : p.seq_lens[b];
   s.len = min(max(L, 0), p.max_blocks * kPage);
   if (report && s.len != L) set_status(p.dev_status, KVQ_DEV_BAD_SEQLEN);
   s.lo = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
@@ -90,6 +94,72 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report) {
 }
 // Pages of a part: the stream in `parts` equal ones, but at least a page per warp.
 KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, (total + parts - 1) / parts); }
+
+// Where a CTA's part [pos, end) of the page stream begins: in sequence b, `before`
+// pages (of one KV head) after the stream's start.  A warp finds it alone.
+struct Part {
+  int pos, end, b, before;
+};
+KVQ_DEVINL Part find_part(const Fp4Params& p, int lane, bool first_cta, bool early) {
+  const int per = (p.B + 31) / 32;
+  const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
+  int mine = 0;
+  for (int b = b0; b < b1; ++b) mine += span_of(p, b, first_cta, early).n;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (first_cta) {  // for the combine
+    int x = incl - mine;
+    for (int b = b0; b < b1; ++b) {
+      p.prefix[b] = x;
+      x += span_of(p, b).n;
+    }
+    if (lane == 0) p.prefix[p.B] = total;
+  }
+  Part r;
+  const int chunk = part_pages(total * p.Hkv, gridDim.x);
+  r.pos = blockIdx.x * chunk;
+  r.end = min(total * p.Hkv, r.pos + chunk);
+  r.b = r.before = 0;
+  if (r.pos >= r.end) return r;
+  // the lane whose sequences hold the part's first page looks for the one
+  const bool here = r.pos >= (incl - mine) * p.Hkv && r.pos < incl * p.Hkv;
+  int b = b0, x = incl - mine;
+  if (here) {
+    for (;; ++b) {
+      const int n = span_of(p, b, false, early).n;
+      if (r.pos < (x + n) * p.Hkv || b + 1 >= b1) break;  // the second: lengths that change meanwhile (early)
+      x += n;
+    }
+  }
+  const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+  r.b = __shfl_sync(0xffffffffu, b, who);
+  r.before = __shfl_sync(0xffffffffu, x, who);
+  return r;
+}
+
+// While the preceding kernel still runs: brings the first pages of a CTA's part
+// into L2.  A hint: what it reads may still change and is read again, and the
+// addresses stay inside the table and the caches whatever it holds.
+template <int D>
+KVQ_DEVINL void hint_pages(const Fp4Params& p, int lane) {
+  const Part part = find_part(p, lane, false, true);
+  if (part.pos >= part.end) return;
+  const Span sp = span_of(p, part.b, false, true);
+  if (sp.n == 0) return;
+  const int within = max(0, part.pos - part.before * p.Hkv);
+  const int h = min(within / sp.n, p.Hkv - 1), pg = within % sp.n + lane;
+  if (pg >= sp.n || pg - lane + part.pos >= part.end || lane >= kHinted) return;
+  const int id = ld_l2only_s32(p.block_table + static_cast<int64_t>(part.b) * p.max_blocks + min(sp.first + pg, p.max_blocks - 1));
+  if (static_cast<unsigned>(id) >= static_cast<uint64_t>(p.num_blocks)) return;
+  const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
+  prefetch_l2(p.k_cache + page * p.k_str, Fp4<D>::kPageB);
+  prefetch_l2(p.v_cache + page * p.v_str, Fp4<D>::kPageB);
+}
 
 KVQ_DEVINL void sts128(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -331,67 +401,26 @@ template <int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(const Fp4Params p) {
   using F = Fp4<D>;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_scan[kWarps], s_seq, s_before;
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (warp == kWarps - 1) hint_pages<D>(p, lane);
   grid_dependency_wait();
   grid_launch_dependents();
-
-  // ---- the plan: where this CTA's part of the page stream begins
-  const int per = (p.B + kWarps * 32 - 1) / (kWarps * 32);
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(p, b, blockIdx.x == 0).n;
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) incl += s_scan[w];
-    total += s_scan[w];
-  }
-  if (blockIdx.x == 0) {  // for the combine
-    int x = incl - mine;
-    for (int b = b0; b < b1; ++b) {
-      p.prefix[b] = x;
-      x += span_of(p, b, false).n;
-    }
-    if (tid == 0) p.prefix[p.B] = total;
-  }
-  const int chunk = part_pages(total * p.Hkv, gridDim.x);
-  int pos = blockIdx.x * chunk;
-  const int end = min(total * p.Hkv, pos + chunk);
+  const Part part = find_part(p, lane, blockIdx.x == 0 && warp == 0, false);
+  int pos = part.pos, b = part.b, before = part.before;
+  const int end = part.end;
   if (pos >= end) return;
-  // the thread whose sequences hold the part's first page looks for the one
-  if (pos >= (incl - mine) * p.Hkv && pos < incl * p.Hkv) {
-    int x = incl - mine, b = b0;
-    for (;; ++b) {
-      const int n = span_of(p, b, false).n;
-      if (pos < (x + n) * p.Hkv) break;
-      x += n;
-    }
-    s_seq = b;
-    s_before = x;
-  }
-  __syncthreads();
-  int b = s_seq, before = s_before;
 
   const uint32_t ring = smem_u32(smem) + warp * F::kRingB;
   float* const stage = reinterpret_cast<float*>(smem + warp * F::kRingB);
   Attend<D> at;
 
   while (pos < end) {
-    const Span sp = span_of(p, b, false);
+    const Span sp = span_of(p, b);
     if (sp.n == 0) {  // to the next sequence with pages (there is one: pos < end)
       do {
         ++b;
-        const unsigned has = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1), false).n > 0);
+        const unsigned has = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1)).n > 0);
         b += has ? __ffs(has) - 1 : 31;
         if (has) break;
       } while (true);
@@ -438,9 +467,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
       }
       copy_commit();
     };
-    at.start(p, b, h, lane);
     issue(0);
     issue(1);
+    at.start(p, b, h, lane);
     for (int i = 0; i < count; ++i) {
       copy_wait<1>();
       __syncwarp();  // every lane's copies are there
@@ -512,15 +541,22 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
   }
 }
 
-// Joins the pieces of a row: a CTA per (sequence, query head).
+// Joins the pieces of a row: a CTA per (sequence, query head).  A warp loads
+// kAtOnce pieces' log-sum-exps and outputs together, so that a row of up to NW *
+// kAtOnce pieces takes one round trip to L2, then joins them against their own
+// maximum; the warps meet in shared memory.
+constexpr int kAtOnce = 5;
 template <int D, int NW>
 __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Params p, int parts) {
-  __shared__ float s_max[NW], s_o[NW][D], s_l[NW];
+  __shared__ float s_max[NW], s_l[NW];
+  __shared__ __align__(16) float s_o[NW][D];
   constexpr int V = D / 32;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq;
   const int h = hq / p.g, qh = hq % p.g;
   grid_dependency_wait();
+  grid_launch_dependents();  // the next call's CTAs may come; they wait for this kernel's end
   const int total = p.prefix[p.B], before = p.prefix[b], n = p.prefix[b + 1] - before;
   __nv_bfloat16* out = p.out + (static_cast<int64_t>(b) * p.Hq + hq) * D;
   if (n == 0) {
@@ -531,33 +567,53 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
   const int x = before * p.Hkv + h * n;
   const int first = x / chunk, last = (x + n - 1) / chunk;
   if (first == last) return;  // written where it was computed
-  const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h;
-  const float* lse = p.lse_part + (first + pair) * p.g + qh;
-  const float* o = p.o_part + ((first + pair) * p.g + qh) * D;
+  const int64_t row = (first + static_cast<int64_t>(b) * p.Hkv + h) * p.g + qh;
   const int count = last - first + 1;
-  float M = NEG_INF;
-  for (int i = warp; i < count; i += NW) M = fmaxf(M, lse[static_cast<int64_t>(i) * p.g]);
-  const float base = M == NEG_INF ? 0.f : M;
-  float acc[V] = {}, l = 0.f;
-  for (int i = warp; i < count; i += NW) {
-    const float f = ex2(lse[static_cast<int64_t>(i) * p.g] - base);
-    l += f;
+  float m = NEG_INF, l = 0.f, acc[V] = {};
+  for (int i0 = warp; i0 < count; i0 += NW * kAtOnce) {
+    float e[kAtOnce];
+    Vec o[kAtOnce];
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = fmaf(o[static_cast<int64_t>(i) * p.g * D + lane * V + e], f, acc[e]);
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * NW;
+      const int64_t at = row + static_cast<int64_t>(min(i, count - 1)) * p.g;
+      e[k] = i < count ? p.lse_part[at] : NEG_INF;
+      o[k] = reinterpret_cast<const Vec*>(p.o_part + at * D)[lane];
+    }
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, e[k]);
+    const float base = top == NEG_INF ? 0.f : top;
+    const float alpha = ex2(m - base);
+    m = top;
+    l *= alpha;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= alpha;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const float f = ex2(e[k] - base);
+      l += f;
+      const float* ov = reinterpret_cast<const float*>(&o[k]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = fmaf(ov[v], f, acc[v]);
+    }
   }
   if (lane == 0) {
-    s_max[warp] = M;
+    s_max[warp] = m;
     s_l[warp] = l;
   }
 #pragma unroll
-  for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+  for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
   __syncthreads();
   for (int d = threadIdx.x; d < D; d += NW * 32) {
     float top = NEG_INF;
+#pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w]);
+    const float base = top == NEG_INF ? 0.f : top;
     float sum = 0.f, y = 0.f;
+#pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float f = s_max[w] == NEG_INF ? 0.f : ex2(s_max[w] - top);
+      const float f = ex2(s_max[w] - base);
       sum = fmaf(s_l[w], f, sum);
       y = fmaf(s_o[w][d], f, y);
     }
