@@ -14,13 +14,14 @@
 //
 // Layout.  A warp takes two pages (32 tokens of a KV head) at a time from two
 // stages of its own in shared memory, filled by 16-byte asynchronous copies: no
-// barrier, no producer warp, nothing between warps until a piece ends.  The
+// barrier, no producer warp, nothing between warps.  The
 // page format is the MMA operand order (m16n8k16, tokens as the rows of K Q^T,
 // dims as the rows of V^T P^T), so that a lane reads its whole share of a page
 // with 16-byte loads: lane 4 r + c holds dims 32 c .. 32 c + 31 (at head dim
 // 128) of tokens r and r + 8 of K, and tokens 2c, 2c + 1, 2c + 8, 2c + 9 of
 // dims 2r, 2r + 1 of each 16 of V.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -33,8 +34,7 @@ namespace {
 
 constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
 constexpr int kCtasPerSm = 3;
-constexpr int kMinPart = 4;           // pages of a part, at least
-constexpr int kHinted = 16;             // pages that hint_pages() asks for: two pairs per warp
+constexpr int kMinPart = 2;           // pages of a part, at least: a pair
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
@@ -49,27 +49,30 @@ struct Fp4 {
   static constexpr int kCodes = kPage * D / 2;
   static constexpr int kScales = kPage * D / 16;
   static constexpr int kPageB = kCodes + kScales;
+  static_assert(kPageB % 64 == 0, "pages lie at multiples of 64 bytes");
   static constexpr int kPairB = 2 * kPageB;            // K page, V page
   static constexpr int kStageB = 2 * kPairB;           // of two pages
+  static constexpr int kStages = 3;                    // scores taken, outputs taken, in flight
   static constexpr int kHalfScales = 2 * kScales * 2;  // both pages' V scales as float16
-  static constexpr int kRingB = 2 * kStageB + kHalfScales;
+  static constexpr int kRingB = kStages * kStageB + 2 * kHalfScales;
   static constexpr int kSmem = kWarps * kRingB;
   static constexpr int kTiles = D / 16;                // MMAs per page, of K and of V
   static constexpr int kRow = D + 8;                   // floats between the queries of a warp's output in shared memory
   static_assert(kRingB >= 8 * kRow * 4, "a warp's output takes its ring's place");
-  static_assert(kSmem <= 47 * 1024, "no more than a launch gets unasked");
+  static_assert(kCtasPerSm * (kSmem + 2048) <= 227 * 1024, "the CTAs of an SM");
 };
 
 struct Fp4Params {
   const __nv_bfloat16* q;
   const uint8_t *k_cache, *v_cache;
-  int64_t k_str, v_str;
+  int64_t str;  // bytes between pages, of both caches
   const float *k_scale, *v_scale;
   const int32_t *block_table, *seq_lens;
   __nv_bfloat16* out;
   float *o_part, *lse_part;
-  int32_t* prefix;  // [B + 1]: attended pages of the sequences before b
+  int32_t* prefix;  // [B + 1]: attended pages of the sequences before b, for the combine
   int B, Hq, Hkv, g, max_blocks;
+  int parts;  // of the page stream, a warp each
   int64_t num_blocks;
   float sm_scale;
   int window;
@@ -80,11 +83,9 @@ struct Fp4Params {
 struct Span {
   int lo, len, first, n;
 };
-// early: before the preceding kernel has completed (the value may still change, and
-// leaves no line in L1).
-KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false, bool early = false) {
+KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false) {
   Span s;
-  const int L = early ? ld_l2only_s32(p.seq_lens + b) : p.seq_lens[b];
+  const int L = p.seq_lens[b];
   s.len = min(max(L, 0), p.max_blocks * kPage);
   if (report && s.len != L) set_status(p.dev_status, KVQ_DEV_BAD_SEQLEN);
   s.lo = p.window > 0 && s.len > p.window ? s.len - p.window : 0;
@@ -92,73 +93,58 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false, bool ear
   s.n = (s.len + kPage - 1) / kPage - s.first;
   return s;
 }
-// Pages of a part: the stream in `parts` equal ones, but at least a page per warp.
-KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, (total + parts - 1) / parts); }
+// Pages of a part, an even number: the stream in `parts` equal ones.
+KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, ((total + parts - 1) / parts + 1) & ~1); }
 
-// Where a CTA's part [pos, end) of the page stream begins: in sequence b, `before`
-// pages (of one KV head) after the stream's start.  A warp finds it alone.
+// Where a warp's part [pos, end) of the page stream begins: in sequence b, `before`
+// pages (of one KV head) after the stream's start.
 struct Part {
   int pos, end, b, before;
+  int chunk, total;  // pages of a part, of the stream
 };
-KVQ_DEVINL Part find_part(const Fp4Params& p, int lane, bool first_cta, bool early) {
-  const int per = (p.B + 31) / 32;
-  const int b0 = min(p.B, lane * per), b1 = min(p.B, b0 + per);
-  int mine = 0;
-  for (int b = b0; b < b1; ++b) mine += span_of(p, b, first_cta, early).n;
-  int incl = mine;
+KVQ_DEVINL int scan_add(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  const int total = __shfl_sync(0xffffffffu, incl, 31);
-  if (first_cta) {  // for the combine
-    int x = incl - mine;
-    for (int b = b0; b < b1; ++b) {
-      p.prefix[b] = x;
-      x += span_of(p, b).n;
-    }
-    if (lane == 0) p.prefix[p.B] = total;
-  }
+  return x;
+}
+KVQ_DEVINL Part find_part(const Fp4Params& p, int index, int lane) {
+  const int n0 = lane < p.B ? span_of(p, lane, index == 0).n : 0;  // of the first 32 sequences
+  int sum = n0;
+#pragma unroll 4
+  for (int b = lane + 32; b < p.B; b += 32) sum += span_of(p, b, index == 0).n;
   Part r;
-  const int chunk = part_pages(total * p.Hkv, gridDim.x);
-  r.pos = blockIdx.x * chunk;
-  r.end = min(total * p.Hkv, r.pos + chunk);
+  r.total = __reduce_add_sync(0xffffffffu, sum) * p.Hkv;
+  r.chunk = part_pages(r.total, p.parts);
+  r.pos = index * r.chunk;
+  r.end = min(r.total, r.pos + r.chunk);
   r.b = r.before = 0;
   if (r.pos >= r.end) return r;
-  // the lane whose sequences hold the part's first page looks for the one
-  const bool here = r.pos >= (incl - mine) * p.Hkv && r.pos < incl * p.Hkv;
-  int b = b0, x = incl - mine;
-  if (here) {
-    for (;; ++b) {
-      const int n = span_of(p, b, false, early).n;
-      if (r.pos < (x + n) * p.Hkv || b + 1 >= b1) break;  // the second: lengths that change meanwhile (early)
-      x += n;
+  for (int b0 = 0, x = 0;; b0 += 32) {  // 32 sequences at a time; the one is there: pos < total
+    const int n = b0 == 0 ? n0 : b0 + lane < p.B ? span_of(p, b0 + lane).n : 0;
+    const int incl = x + scan_add(n, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, r.pos < incl * p.Hkv);
+    if (past) {
+      const int who = __ffs(past) - 1;
+      r.b = b0 + who;
+      r.before = __shfl_sync(0xffffffffu, incl - n, who);
+      return r;
     }
+    x = __shfl_sync(0xffffffffu, incl, 31);
   }
-  const int who = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-  r.b = __shfl_sync(0xffffffffu, b, who);
-  r.before = __shfl_sync(0xffffffffu, x, who);
-  return r;
 }
 
-// While the preceding kernel still runs: brings the first pages of a CTA's part
-// into L2.  A hint: what it reads may still change and is read again, and the
-// addresses stay inside the table and the caches whatever it holds.
-template <int D>
-KVQ_DEVINL void hint_pages(const Fp4Params& p, int lane) {
-  const Part part = find_part(p, lane, false, true);
-  if (part.pos >= part.end) return;
-  const Span sp = span_of(p, part.b, false, true);
-  if (sp.n == 0) return;
-  const int within = max(0, part.pos - part.before * p.Hkv);
-  const int h = min(within / sp.n, p.Hkv - 1), pg = within % sp.n + lane;
-  if (pg >= sp.n || pg - lane + part.pos >= part.end || lane >= kHinted) return;
-  const int id = ld_l2only_s32(p.block_table + static_cast<int64_t>(part.b) * p.max_blocks + min(sp.first + pg, p.max_blocks - 1));
-  if (static_cast<unsigned>(id) >= static_cast<uint64_t>(p.num_blocks)) return;
-  const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
-  prefetch_l2(p.k_cache + page * p.k_str, Fp4<D>::kPageB);
-  prefetch_l2(p.v_cache + page * p.v_str, Fp4<D>::kPageB);
+KVQ_DEVINL void write_prefix(const Fp4Params& p, int lane) {
+  int x = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int n = b0 + lane < p.B ? span_of(p, b0 + lane).n : 0;
+    const int incl = scan_add(n, lane);
+    if (b0 + lane < p.B) p.prefix[b0 + lane] = x + incl - n;
+    x += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  if (lane == 0) p.prefix[p.B] = x;
 }
 
 KVQ_DEVINL void sts128(uint32_t a, const uint4& v) {
@@ -192,6 +178,14 @@ KVQ_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t x) {
 }
 KVQ_DEVINL uint32_t both(uint32_t h, bool high) { return __byte_perm(h, h, high ? 0x3232 : 0x1010); }
 
+// What a stage in flight holds.
+struct Meta {
+  int b, h, tok;  // sequence, KV head, first token
+  int flags;      // bit i: page i is there; the piece's first and last stage; all of (b, h); 0: none
+};
+constexpr uint32_t kNowhere = 0xffffffffu;
+constexpr int kFirst = 4, kLast = 8, kWhole = 16, kStage = 32;
+
 // A warp's state for the queries of one KV head: lane 4 r + c holds the
 // stabilizers and sums of queries 2c, 2c + 1 and, per 16 dims, the outputs
 // O[.][0], O[.][1] of dim 2r and O[.][2], O[.][3] of dim 2r + 1.
@@ -199,20 +193,35 @@ template <int D>
 struct Attend {
   using F = Fp4<D>;
   uint32_t q[D / 8];  // query r, dims (D / 4) c .. + D / 4 - 1
-  float coef[2];
+  float coef[2], vs;
   float m[2], mb[2], l[2];  // mb: m - kBase, or kNone, which any score passes
   float O[F::kTiles][4];
+  uint32_t p[2][2];  // weights of the stage whose outputs are due
 
-  KVQ_DEVINL void start(const Fp4Params& p, int b, int h, int lane) {
+  // The queries as they are, and (begin) as the products take them.
+  struct Raw {
+    uint4 q[D / 32];
+    float ks, vs;
+  };
+  KVQ_DEVINL static Raw fetch(const Fp4Params& prm, int b, int h, int lane) {
     const int r = lane >> 2, c = lane & 3;
-    const bool live = r < p.g;
-    const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(b) * p.Hq + h * p.g + (live ? r : 0)) * D +
-                                                      c * (D / 4));
+    const bool live = r < prm.g;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        prm.q + (static_cast<int64_t>(b) * prm.Hq + h * prm.g + (live ? r : 0)) * D + c * (D / 4));
+    Raw raw;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) raw.q[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+    raw.ks = prm.k_scale[h];
+    raw.vs = prm.v_scale[h];
+    return raw;
+  }
+  KVQ_DEVINL void begin(const Fp4Params& prm, const Raw& raw, int lane) {
+    const int c = lane & 3;
     float mx = 0.f;
     float2 x[D / 32][4];
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      unpack8_bf16(live ? src[i] : make_uint4(0, 0, 0, 0), x[i]);
+      unpack8_bf16(raw.q[i], x[i]);
       mx = fmaxf(mx, amax8(x[i]));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -225,7 +234,8 @@ struct Attend {
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) q[4 * i + e] = pack_f16x2(x[i][e].x * sigma, x[i][e].y * sigma);
-    const float cf = __fmul_rn(__fmul_rn(p.k_scale[h], p.sm_scale), kLog2e);
+    vs = raw.vs;
+    const float cf = __fmul_rn(__fmul_rn(raw.ks, prm.sm_scale), kLog2e);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       coef[i] = cf * __shfl_sync(0xffffffffu, inv_sigma, 8 * c + 4 * i);
@@ -240,37 +250,61 @@ struct Attend {
       for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
   }
 
-  // Two pages at shared address `stage`; tokens [lo[i], hi[i]) of page i are live
-  // (edge: not all are).  `half`: room for V's scales as float16.
-  KVQ_DEVINL void take(uint32_t stage, uint32_t half, bool edge, const int (&lo)[2], const int (&hi)[2], int lane) {
+  // The piece's output, normalized: to the output where it is all of the sequence
+  // and KV head, else to the workspace with its log-sum-exp.
+  KVQ_DEVINL void finish(const Fp4Params& prm, int index, const Meta& meta, int lane) {
     const int r = lane >> 2, c = lane & 3;
-    // ---- V's scales, eight to a lane, as float16 for all; those of masked tokens may be anything: zero
-    {
-      constexpr int kLanes = F::kScales / 8;  // per page
-      const int pg = lane / kLanes;           // D = 64: the upper half of the lanes has none
-      if (pg < 2) {
-        uint2 w = lds64(stage + pg * F::kPairB + F::kPageB + F::kCodes + lane % kLanes * 8);
-        if (edge) {
-          uint32_t keep = 0xffffffffu;
+    const int64_t id = index + static_cast<int64_t>(meta.b) * prm.Hkv + meta.h;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int t = 2 * ((lane >> 1) & 3) + (e & 1) + 8 * (e >> 1);
-            if (t < (pg ? lo[1] : lo[0]) || t >= (pg ? hi[1] : hi[0])) keep &= ~(0xffu << (8 * e));
-          }
-          w.x &= keep;
-          w.y &= keep;
-        }
-        uint4 h;
-        e4m3x4_to_f16x2x2(w.x, h.x, h.y);
-        e4m3x4_to_f16x2x2(w.y, h.z, h.w);
-        sts128(half + lane * 16, h);
+    for (int i = 0; i < 2; ++i) {
+      float sum = l[i];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const bool any = sum > 0.f || sum != sum;
+      const float f = any ? vs / sum : 0.f;
+      const int qh = 2 * c + i;
+      if (qh >= prm.g) continue;
+      if (meta.flags & kWhole) {
+        __nv_bfloat16* out = prm.out + (static_cast<int64_t>(meta.b) * prm.Hq + meta.h * prm.g + qh) * D + 2 * r;
+#pragma unroll
+        for (int d = 0; d < F::kTiles; ++d)
+          *reinterpret_cast<uint32_t*>(out + 16 * d) = pack_bf16x2(any ? O[d][i] * f : 0.f, any ? O[d][2 + i] * f : 0.f);
+      } else {
+        float* out = prm.o_part + (id * prm.g + qh) * D + 2 * r;
+#pragma unroll
+        for (int d = 0; d < F::kTiles; ++d)
+          *reinterpret_cast<float2*>(out + 16 * d) = make_float2(any ? O[d][i] * f : 0.f, any ? O[d][2 + i] * f : 0.f);
+        if (r == 0) prm.lse_part[id * prm.g + qh] = any ? m[i] + log2f(sum) : NEG_INF;
       }
     }
-    // ---- scores: rows are tokens, and each lane's dims share two scales (one at D = 64) per row
-    float t[2][4];
+  }
+
+  // The state to shared memory, for the CTA's warps to join.
+  KVQ_DEVINL void show(float* o, float* sm, float* sl, int lane) {
+    const int r = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float sum = l[i];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+      if (r == 0) {
+        sm[2 * c + i] = m[i];
+        sl[2 * c + i] = sum;
+      }
+#pragma unroll
+      for (int d = 0; d < F::kTiles; ++d)
+        *reinterpret_cast<float2*>(o + (2 * c + i) * F::kRow + 16 * d + 2 * r) = make_float2(O[d][i], O[d][2 + i]);
+    }
+  }
+
+  // The stage's K against the queries: t[i][0], [1] of token r of page i, queries 2c,
+  // 2c + 1; [2], [3] of token r + 8.
+  KVQ_DEVINL void scores(uint32_t stage, float (&t)[2][4], int lane) const {
+    const int r = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int pg = 0; pg < 2; ++pg) {
       const uint32_t page = stage + pg * F::kPairB;
+      // each lane's dims share two scales (one at D = 64) per token
       uint32_t kw[2][D / 32], ks[2][2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -304,60 +338,15 @@ struct Attend {
         mma_f16(s[0], a[0][0], a[1][0], a[0][1], a[1][1], q[4 * w], q[4 * w + 1], s[0]);
         mma_f16(s[1], a[0][2], a[1][2], a[0][3], a[1][3], q[4 * w + 2], q[4 * w + 3], s[1]);
       }
-      // [0], [1]: token r, queries 2c, 2c + 1; [2], [3]: token r + 8
 #pragma unroll
       for (int e = 0; e < 4; ++e) t[pg][e] = s[0][e] + s[1][e];
-      if (edge) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int tok = r + 8 * (e >> 1);
-          if (tok < lo[pg] || tok >= hi[pg]) t[pg][e] = NEG_INF;
-        }
-      }
     }
-    // ---- stabilizer: moved only when a score passes it by more than kLag
-    float x[2][4];
-#pragma unroll
-    for (int pg = 0; pg < 2; ++pg)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
-    const float top = fmax3(fmax3(x[0][0], x[0][2], fmaxf(x[1][0], x[1][2])), x[0][1], fmax3(x[0][3], x[1][1], x[1][3]));
-    if (__any_sync(0xffffffffu, top > kLag + kBase)) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i])) * coef[i];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
-        n = fmaxf(n, m[i]);
-        if (n > m[i]) {  // the same in every lane of the query
-          const float alpha = ex2(m[i] - n);
-          l[i] *= alpha;
-#pragma unroll
-          for (int d = 0; d < F::kTiles; ++d) {
-            O[d][i] *= alpha;
-            O[d][2 + i] *= alpha;
-          }
-          m[i] = n;
-          mb[i] = n - kBase;
-        }
-      }
-#pragma unroll
-      for (int pg = 0; pg < 2; ++pg)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
-    }
-    uint32_t p[2][2];
-#pragma unroll
-    for (int pg = 0; pg < 2; ++pg) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[pg][e] = ex2(x[pg][e]);
-      l[0] += x[pg][0] + x[pg][2];
-      l[1] += x[pg][1] + x[pg][3];
-      p[pg][0] = movmatrix_t(pack_f16x2(x[pg][0], x[pg][1]));
-      p[pg][1] = movmatrix_t(pack_f16x2(x[pg][2], x[pg][3]));
-    }
-    // ---- outputs: rows are 16 dims that share a token's scale, which multiplies the weights
-    __syncwarp();  // the scales are there
+  }
+
+  // The weights p against the stage's V, whose scales are at `half`: rows are 16
+  // dims that share a token's scale, which multiplies the weights.
+  KVQ_DEVINL void outputs(uint32_t stage, uint32_t half, int lane) {
+    const int c = lane & 3;
 #pragma unroll
     for (int h = 0; h < D / 64; ++h) {
 #pragma unroll
@@ -395,180 +384,327 @@ struct Attend {
       }
     }
   }
+
+  // The stage's weights from its scores, and its V scales, eight to a lane, as float16 at
+  // `half`.  Tokens [lo[i], hi[i]) of page i are live (edge: not all are); the
+  // scales of the others may be anything and become zero.
+  KVQ_DEVINL void weigh(uint32_t stage, uint32_t half, float (&t)[2][4], bool edge, const int (&lo)[2], const int (&hi)[2],
+                        int lane) {
+    const int r = lane >> 2;
+    constexpr int kLanes = F::kScales / 8;  // per page
+    const int at = lane / kLanes;           // D = 64: the upper half of the lanes has none
+    uint2 w = make_uint2(0, 0);
+    if (at < 2) w = lds64(stage + at * F::kPairB + F::kPageB + F::kCodes + lane % kLanes * 8);
+    if (edge) {
+      uint32_t keep = 0xffffffffu;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int tok = 2 * ((lane >> 1) & 3) + (e & 1) + 8 * (e >> 1);
+        if (tok < (at ? lo[1] : lo[0]) || tok >= (at ? hi[1] : hi[0])) keep &= ~(0xffu << (8 * e));
+      }
+      w.x &= keep;
+      w.y &= keep;
+#pragma unroll
+      for (int pg = 0; pg < 2; ++pg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int tok = r + 8 * (e >> 1);
+          if (tok < lo[pg] || tok >= hi[pg]) t[pg][e] = NEG_INF;
+        }
+    }
+    uint4 hs;
+    e4m3x4_to_f16x2x2(w.x, hs.x, hs.y);
+    e4m3x4_to_f16x2x2(w.y, hs.z, hs.w);
+    if (at < 2) sts128(half + lane * 16, hs);
+    // stabilizer: moved only when a score passes it by more than kLag
+    float x[2][4];
+#pragma unroll
+    for (int pg = 0; pg < 2; ++pg)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+    const float top = fmax3(fmax3(x[0][0], x[0][2], fmaxf(x[1][0], x[1][2])), x[0][1], fmax3(x[0][3], x[1][1], x[1][3]));
+    if (__any_sync(0xffffffffu, top > kLag + kBase)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i])) * coef[i];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
+        if (n > m[i]) {  // the same in every lane of the query
+          const float alpha = ex2(m[i] - n);
+          l[i] *= alpha;
+#pragma unroll
+          for (int d = 0; d < F::kTiles; ++d) {
+            O[d][i] *= alpha;
+            O[d][2 + i] *= alpha;
+          }
+          m[i] = n;
+          mb[i] = n - kBase;
+        }
+      }
+#pragma unroll
+      for (int pg = 0; pg < 2; ++pg)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+    }
+#pragma unroll
+    for (int pg = 0; pg < 2; ++pg) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[pg][e] = ex2(x[pg][e]);
+      l[0] += x[pg][0] + x[pg][2];
+      l[1] += x[pg][1] + x[pg][3];
+      p[pg][0] = movmatrix_t(pack_f16x2(x[pg][0], x[pg][1]));
+      p[pg][1] = movmatrix_t(pack_f16x2(x[pg][2], x[pg][3]));
+    }
+  }
+};
+
+// Walks the stream's pieces ((sequence, KV head) parts) two pages at a time and
+// issues their copies; every lane of the warp takes part.
+template <int D>
+struct Feeder {
+  using F = Fp4<D>;
+  int pos, end, b, before;  // as Part
+  int h, pg, stop;          // the piece: pages [.., stop) of KV head h, pg next
+  Span sp;
+  int flags;                // of the next stage: kFirst, kWhole
+  int base, ahead;          // a lane's page: base + lane of the sequence's attended ones; block id of the one 32 on
+  uint32_t place;           // 64-byte units into the caches, or kNowhere
+
+  KVQ_DEVINL void piece(const Fp4Params& p, int lane) {
+    const int within = pos - before * p.Hkv;
+    h = within / sp.n;
+    pg = within - h * sp.n;
+    stop = min(sp.n, pg + end - pos);
+    flags = kFirst | (stop - pg == sp.n ? kWhole : 0);
+    base = pg - 32;
+    ahead = id_of(p, pg + lane);
+    // the piece's queries, which its first stage's taker reads
+    const int bytes = p.g * D * 2;
+    if (lane * 128 < bytes)
+      prefetch_l2(reinterpret_cast<const uint8_t*>(p.q + (static_cast<int64_t>(b) * p.Hq + h * p.g) * D) + lane * 128, 128);
+  }
+  KVQ_DEVINL int id_of(const Fp4Params& p, int page) const {
+    return page < stop ? p.block_table[static_cast<int64_t>(b) * p.max_blocks + sp.first + page] : -1;
+  }
+  KVQ_DEVINL void start(const Fp4Params& p, const Part& part, int lane) {
+    pos = part.pos;
+    end = part.end;
+    b = part.b;
+    before = part.before;
+    if (pos >= end) return;
+    sp = span_of(p, b);
+    piece(p, lane);
+  }
+  // The next stage's copies (none when the part is through), as one group.
+  KVQ_DEVINL void feed(const Fp4Params& p, uint32_t stage, Meta* meta, int lane) {
+    if (pos < end) {
+      const int n = min(2, stop - pg);
+      if (pg + n > base + 32) {  // the next 32 pages, whose ids have come meanwhile
+        base = pg;
+        place = static_cast<unsigned>(ahead) < static_cast<uint64_t>(p.num_blocks)
+                    ? static_cast<uint32_t>((static_cast<int64_t>(ahead) * p.Hkv + h) * p.str >> 6)
+                    : kNowhere;
+        ahead = id_of(p, pg + 32 + lane);
+      }
+      int has = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i >= n) break;
+        const uint32_t at = __shfl_sync(0xffffffffu, place, pg + i - base);
+        if (at != kNowhere) {
+          has |= 1 << i;
+          const uint8_t* k = p.k_cache + (static_cast<uint64_t>(at) << 6) + lane * 16;
+          const uint8_t* v = p.v_cache + (static_cast<uint64_t>(at) << 6) + lane * 16;
+          const uint32_t to = stage + i * F::kPairB + lane * 16;
+#pragma unroll
+          for (int x = 0; x < F::kPageB; x += 512) {
+            if (x + 512 <= F::kPageB || x + lane * 16 < F::kPageB) {
+              copy16(to + x, k + x);
+              copy16(to + F::kPageB + x, v + x);
+            }
+          }
+        } else if (lane == 0) {
+          set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
+        }
+      }
+      if (lane == 0) *meta = Meta{b, h, (sp.first + pg) * kPage, has | flags | kStage | (pg + n == stop ? kLast : 0)};
+      flags &= ~kFirst;
+      pg += n;
+      pos += n;
+      if (pg == stop && pos < end) {  // the next piece
+        if (h + 1 == p.Hkv) {         // of the next sequence with pages (there is one: pos < end)
+          before += sp.n;
+          ++b;
+          while (true) {
+            const unsigned some = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1)).n > 0);
+            if (some) {
+              b += __ffs(some) - 1;
+              break;
+            }
+            b += 32;
+          }
+          sp = span_of(p, b);
+        }
+        piece(p, lane);
+      }
+    } else if (lane == 0) {
+      meta->flags = 0;
+    }
+    copy_commit();
+  }
 };
 
 template <int D>
 __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(const Fp4Params p) {
   using F = Fp4<D>;
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Meta s_meta[kWarps][F::kStages];
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (warp == kWarps - 1) hint_pages<D>(p, lane);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int index = blockIdx.x * kWarps + warp;
   grid_dependency_wait();
   grid_launch_dependents();
-  const Part part = find_part(p, lane, blockIdx.x == 0 && warp == 0, false);
-  int pos = part.pos, b = part.b, before = part.before;
-  const int end = part.end;
-  if (pos >= end) return;
+  if (index == 0) write_prefix(p, lane);
+  const Part part = find_part(p, index, lane);
 
   const uint32_t ring = smem_u32(smem) + warp * F::kRingB;
-  float* const stage = reinterpret_cast<float*>(smem + warp * F::kRingB);
+  Meta* const meta = s_meta[warp];
+  if (part.pos >= part.end) return;
+  Feeder<D> feeder;
+  feeder.start(p, part, lane);
+  // Are all of the CTA's parts, more than one, of one (sequence, KV head)?  Then
+  // their states meet at the end: one row of partials instead of four.
+  const int c0 = (index - warp) * part.chunk, c1 = min(part.total, c0 + kWarps * part.chunk);
+  const int x0 = feeder.before * p.Hkv + feeder.h * feeder.sp.n;
+  const bool joined = c1 - c0 > part.chunk && x0 <= c0 && c1 <= x0 + feeder.sp.n;
+  Span sp = feeder.sp;
+  const typename Attend<D>::Raw raw = Attend<D>::fetch(p, feeder.b, feeder.h, lane);  // ahead of the copies
+  feeder.feed(p, ring, meta, lane);
+  feeder.feed(p, ring + F::kStageB, meta + 1, lane);
+  // Stage i's scores are taken together with stage i - 1's outputs: two independent
+  // chains of conversions and MMAs for a warp to fill its issue slots with.
   Attend<D> at;
-
-  while (pos < end) {
-    const Span sp = span_of(p, b);
-    if (sp.n == 0) {  // to the next sequence with pages (there is one: pos < end)
-      do {
-        ++b;
-        const unsigned has = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1)).n > 0);
-        b += has ? __ffs(has) - 1 : 31;
-        if (has) break;
-      } while (true);
-      continue;
+  at.begin(p, raw, lane);
+  Meta before;  // of stage i - 1
+  before.flags = 0;
+  uint32_t here = ring, prev = ring + 2 * F::kStageB;  // the stages' places
+  const uint32_t halves = ring + F::kStages * F::kStageB;
+  for (int i = 0;; ++i) {
+    copy_wait<1>();
+    __syncwarp();  // every lane's copies are there, the meta word, and the scales of stage i - 1
+    const int st = i % F::kStages;
+    const Meta m = meta[st];
+    const uint32_t half = halves + (i & 1) * F::kHalfScales, half_before = halves + (~i & 1) * F::kHalfScales;
+    float t[2][4];
+    if (before.flags != 0 && (m.flags == 0 || m.flags & kFirst)) {  // the piece before is through
+      at.outputs(prev, half_before, lane);
+      if (joined) break;
+      at.finish(p, index, before, lane);
     }
-    const int within = pos - before * p.Hkv;
-    const int h = within / sp.n, pg0 = within % sp.n;
-    const int n = min(end - pos, sp.n - pg0);
-    const int32_t* table = p.block_table + static_cast<int64_t>(b) * p.max_blocks + sp.first + pg0;
-
-    // ---- this warp's pairs of pages: pairs warp, warp + kWarps, ...
-    const int pairs = (n + 1) / 2;
-    const int count = pairs > warp ? (pairs - warp + kWarps - 1) / kWarps : 0;
-    int ids = -1;        // block ids of 16 pairs, one page per lane
-    unsigned valid = 0;  // bit 2 s + i: page i of stage s is there
-    auto issue = [&](int i) {
-      if (i < count) {
-        if ((i & 15) == 0) {
-          const int j = i + (lane >> 1), page = 2 * (warp + j * kWarps) + (lane & 1);
-          ids = j < count && page < n ? table[page] : -1;
-        }
-        const int st = i & 1;
-        valid &= ~(3u << (2 * st));
-#pragma unroll
-        for (int pg = 0; pg < 2; ++pg) {
-          const int id = __shfl_sync(0xffffffffu, ids, 2 * (i & 15) + pg);
-          if (static_cast<unsigned>(id) < static_cast<uint64_t>(p.num_blocks)) {
-            valid |= 1u << (2 * st + pg);
-            const int64_t page = static_cast<int64_t>(id) * p.Hkv + h;
-            const uint8_t* k = p.k_cache + page * p.k_str + lane * 16;
-            const uint8_t* v = p.v_cache + page * p.v_str + lane * 16;
-            const uint32_t at = ring + st * F::kStageB + pg * F::kPairB + lane * 16;
-#pragma unroll
-            for (int x = 0; x < F::kPageB; x += 512) {
-              if (x + 512 <= F::kPageB || x + lane * 16 < F::kPageB) {
-                copy16(at + x, k + x);
-                copy16(at + F::kPageB + x, v + x);
-              }
-            }
-          } else if (lane == 0 && 2 * (warp + i * kWarps) + pg < n) {
-            set_status(p.dev_status, KVQ_DEV_BAD_BLOCK);
-          }
-        }
+    if (m.flags == 0) return;
+    if (m.flags & kFirst) {
+      if (i > 0) {
+        at.begin(p, Attend<D>::fetch(p, m.b, m.h, lane), lane);
+        sp = span_of(p, m.b);
       }
-      copy_commit();
-    };
-    issue(0);
-    issue(1);
-    at.start(p, b, h, lane);
-    for (int i = 0; i < count; ++i) {
-      copy_wait<1>();
-      __syncwarp();  // every lane's copies are there
-      const int st = i & 1;
-      const unsigned have = valid >> (2 * st) & 3;
-      if (have) {
-        const int tok = (sp.first + pg0 + 2 * (warp + i * kWarps)) * kPage;
-        int lo[2], hi[2];
-#pragma unroll
-        for (int pg = 0; pg < 2; ++pg) {
-          lo[pg] = sp.lo - tok - pg * kPage;
-          hi[pg] = have >> pg & 1 ? sp.len - tok - pg * kPage : 0;
-        }
-        const bool edge = lo[0] > 0 || lo[1] > 0 || hi[0] < kPage || hi[1] < kPage;
-        at.take(ring + st * F::kStageB, ring + 2 * F::kStageB, edge, lo, hi, lane);
-      }
-      __syncwarp();  // every lane is done with the stage
-      issue(i + 2);
+      at.scores(here, t, lane);
+    } else {
+      at.scores(here, t, lane);
+      at.outputs(prev, half_before, lane);
     }
-    copy_wait<0>();
-    __syncwarp();
-
-    // ---- the piece's end: the warps' states meet
-    {
-      const int r = lane >> 2, c = lane & 3;
+    int lo[2], hi[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) at.l[i] += __shfl_xor_sync(0xffffffffu, at.l[i], o);
-        if (r == 0) {
-          s_m[warp][2 * c + i] = at.m[i];
-          s_l[warp][2 * c + i] = at.l[i];
-        }
-#pragma unroll
-        for (int d = 0; d < F::kTiles; ++d)
-          *reinterpret_cast<float2*>(stage + (2 * c + i) * F::kRow + 16 * d + 2 * r) = make_float2(at.O[d][i], at.O[d][2 + i]);
-      }
+    for (int pg = 0; pg < 2; ++pg) {
+      lo[pg] = sp.lo - m.tok - pg * kPage;
+      hi[pg] = m.flags >> pg & 1 ? sp.len - m.tok - pg * kPage : 0;
     }
-    __syncthreads();
-    const bool direct = n == sp.n;  // all of the sequence and KV head
-    const int64_t id = blockIdx.x + static_cast<int64_t>(b) * p.Hkv + h;
-    const float vs = p.v_scale[h];
-    for (int x = tid; x < p.g * D; x += kWarps * 32) {
-      const int qh = x / D, d = x % D;
-      float M = NEG_INF;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][qh]);
-      float l = 0.f, o = 0.f;
+    const bool edge = lo[0] > 0 || lo[1] > 0 || hi[0] < kPage || hi[1] < kPage;
+    at.weigh(here, half, t, edge, lo, hi, lane);
+    __syncwarp();  // every lane is done with stage i - 1
+    feeder.feed(p, prev, meta + (st + 2) % F::kStages, lane);
+    before = m;
+    const uint32_t next = 3 * ring + 3 * F::kStageB - here - prev;  // the three places add up to this
+    prev = here;
+    here = next;
+  }
+  {
+    const Meta& m = before;
+    __syncwarp();  // the stages are read, and no copies are left in flight
+    at.show(reinterpret_cast<float*>(smem + warp * F::kRingB), s_m[warp], s_l[warp], lane);
+    const int warps = (c1 - c0 + part.chunk - 1) / part.chunk;
+    named_bar_sync(1, warps * 32);
+    const int64_t id = index - warp + static_cast<int64_t>(m.b) * p.Hkv + m.h;
+    for (int x = threadIdx.x; x < p.g * (D / 2); x += warps * 32) {  // two dims
+      const int qh = x / (D / 2), d = x % (D / 2) * 2;
+      float mw[kWarps], lw[kWarps];
+      float2 ow[kWarps];
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = s_m[w][qh] == NEG_INF ? 0.f : ex2(s_m[w][qh] - M);
-        l = fmaf(s_l[w][qh], f, l);
-        if (f != 0.f) o = fmaf(reinterpret_cast<const float*>(smem + w * F::kRingB)[qh * F::kRow + d], f, o);
+        const bool is = w < warps;
+        mw[w] = is ? s_m[w][qh] : NEG_INF;
+        lw[w] = is ? s_l[w][qh] : 0.f;
+        ow[w] = is ? *reinterpret_cast<const float2*>(smem + w * F::kRingB + (qh * F::kRow + d) * 4) : make_float2(0.f, 0.f);
       }
-      o = l > 0.f || l != l ? o / l * vs : 0.f;
-      if (direct) {
-        p.out[(static_cast<int64_t>(b) * p.Hq + h * p.g + qh) * D + d] = __float2bfloat16(o);
-      } else {
-        p.o_part[(id * p.g + qh) * D + d] = o;
-        if (d == 0) p.lse_part[id * p.g + qh] = l > 0.f || l != l ? M + log2f(l) : NEG_INF;
+      float M = mw[0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mw[w]);
+      const float base = M == NEG_INF ? 0.f : M;
+      float l = 0.f;
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = ex2(mw[w] - base);
+        l = fmaf(lw[w], f, l);
+        o = ffma2(ow[w], make_float2(f, f), o);
       }
-    }
-    __syncthreads();
-    pos += n;
-    if (within + n == sp.n * p.Hkv) {
-      before += sp.n;
-      ++b;
+      const bool any = l > 0.f || l != l;
+      const float f = any ? at.vs / l : 0.f;
+      *reinterpret_cast<float2*>(p.o_part + (id * p.g + qh) * D + d) = any ? make_float2(o.x * f, o.y * f) : make_float2(0.f, 0.f);
+      if (d == 0) p.lse_part[id * p.g + qh] = any ? M + log2f(l) : NEG_INF;
     }
   }
 }
 
-// Joins the pieces of a row: a CTA per (sequence, query head).  A warp loads
+// Joins the pieces of a row: a CTA per (sequence, query head) and W dims.  A warp loads
 // kAtOnce pieces' log-sum-exps and outputs together, so that a row of up to NW *
 // kAtOnce pieces takes one round trip to L2, then joins them against their own
 // maximum; the warps meet in shared memory.
-constexpr int kAtOnce = 5;
-template <int D, int NW>
-__global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Params p, int parts) {
+constexpr int kAtOnce = 8;
+template <int D, int W, int NW>
+__global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Params p) {
   __shared__ float s_max[NW], s_l[NW];
-  __shared__ __align__(16) float s_o[NW][D];
-  constexpr int V = D / 32;
-  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ __align__(16) float s_o[NW][W];
+  constexpr int V = W / 32;
+  using Vec = typename std::conditional<V == 4, float4, typename std::conditional<V == 2, float2, float>::type>::type;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq;
+  const int b = blockIdx.x / p.Hq, hq = blockIdx.x % p.Hq, d0 = blockIdx.y * W;
   const int h = hq / p.g, qh = hq % p.g;
   grid_dependency_wait();
   grid_launch_dependents();  // the next call's CTAs may come; they wait for this kernel's end
   const int total = p.prefix[p.B], before = p.prefix[b], n = p.prefix[b + 1] - before;
-  __nv_bfloat16* out = p.out + (static_cast<int64_t>(b) * p.Hq + hq) * D;
+  __nv_bfloat16* out = p.out + (static_cast<int64_t>(b) * p.Hq + hq) * D + d0;
   if (n == 0) {
-    for (int d = threadIdx.x; d < D; d += NW * 32) out[d] = __float2bfloat16(0.f);
+    for (int d = threadIdx.x; d < W; d += NW * 32) out[d] = __float2bfloat16(0.f);
     return;
   }
-  const int chunk = part_pages(total * p.Hkv, parts);
+  const int chunk = part_pages(total * p.Hkv, p.parts);
   const int x = before * p.Hkv + h * n;
   const int first = x / chunk, last = (x + n - 1) / chunk;
   if (first == last) return;  // written where it was computed
-  const int64_t row = (first + static_cast<int64_t>(b) * p.Hkv + h) * p.g + qh;
-  const int count = last - first + 1;
+  // CTAs kWarps * [c0, c1) of parts wrote one row each, the parts before and behind
+  // them their own
+  const int all = total * p.Hkv, cta = kWarps * chunk;
+  const int c0 = (x + cta - 1) / cta;
+  int c1 = (x + n) / cta;
+  if (x + n == all && all - all / cta * cta > chunk) c1 = all / cta + 1;
+  const int lead = c1 > c0 ? kWarps * c0 - first : last - first + 1;
+  const int full = c1 > c0 ? c1 - c0 : 0;
+  const int count = c1 > c0 ? lead + full + max(0, last - kWarps * c1 + 1) : lead;
+  const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h;
+  auto row = [&](int i) -> int64_t {
+    const int part = i < lead ? first + i : i < lead + full ? kWarps * (c0 + i - lead) : kWarps * c1 + i - lead - full;
+    return (part + pair) * p.g + qh;
+  };
   float m = NEG_INF, l = 0.f, acc[V] = {};
   for (int i0 = warp; i0 < count; i0 += NW * kAtOnce) {
     float e[kAtOnce];
@@ -576,9 +712,9 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
       const int i = i0 + k * NW;
-      const int64_t at = row + static_cast<int64_t>(min(i, count - 1)) * p.g;
+      const int64_t at = row(min(i, count - 1));
       e[k] = i < count ? p.lse_part[at] : NEG_INF;
-      o[k] = reinterpret_cast<const Vec*>(p.o_part + at * D)[lane];
+      o[k] = reinterpret_cast<const Vec*>(p.o_part + at * D + d0)[lane];
     }
     float top = m;
 #pragma unroll
@@ -605,7 +741,7 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
 #pragma unroll
   for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += NW * 32) {
+  for (int d = threadIdx.x; d < W; d += NW * 32) {
     float top = NEG_INF;
 #pragma unroll
     for (int w = 0; w < NW; ++w) top = fmaxf(top, s_max[w]);
@@ -621,10 +757,11 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
   }
 }
 
-// CTAs of a call: one wave, and no more than parts of kMinPart pages.
+// Parts of a call's page stream, a warp each: one wave of CTAs, and no more than pairs
+// of pages.
 int fp4_parts(int B, int Hkv, int max_blocks) {
   const int64_t most = (static_cast<int64_t>(B) * Hkv * max_blocks + kMinPart - 1) / kMinPart;
-  return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(kCtasPerSm) * sm_count(), most));
+  return static_cast<int>(std::min<int64_t>(static_cast<int64_t>(kCtasPerSm) * sm_count() * kWarps, most));
 }
 // Rows of partials: piece (part, sequence and KV head) is row part + pair.
 int64_t fp4_rows(int B, int Hq, int Hkv, int max_blocks) {
@@ -638,12 +775,19 @@ template <int D>
 kvq_status_t launch_fp4(const Fp4Params& p, cudaStream_t s) {
   using F = Fp4<D>;
   auto kern = decode_fp4_kernel<D>;
-  const int parts = fp4_parts(p.B, p.Hkv, p.max_blocks);
+  static std::atomic<uint64_t> configured{0};  // devices whose attribute is set
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (!(configured.load() >> (dev & 63) & 1)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, F::kSmem);
+    if (e != cudaSuccess) return cuda_status(e, "paged_decode_fp4: set shared memory size");
+    configured.fetch_or(uint64_t(1) << (dev & 63));
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(parts);
+  cfg.gridDim = dim3((p.parts + kWarps - 1) / kWarps);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = F::kSmem;
   cfg.stream = s;
@@ -651,15 +795,22 @@ kvq_status_t launch_fp4(const Fp4Params& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return cuda_status(e, "paged_decode_fp4 launch");
-  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hq);
   cfg.dynamicSmemBytes = 0;
-  // warps for the pieces of a row
-  if (parts / (static_cast<int64_t>(p.B) * p.Hkv) >= 8) {
-    cfg.blockDim = dim3(16 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 16>, p, parts);
+  const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
+  // few rows have many pieces (about four of which are one row of partials): more warps, 32 dims to a CTA
+  const int64_t pieces = p.parts / (static_cast<int64_t>(p.B) * p.Hkv);
+  if (pieces >= KVQ_TUNE(cmany, 512)) {
+    cfg.gridDim = dim3(rows, D / 32);
+    cfg.blockDim = dim3(32 * 32);
+    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 32, 32>, p);
+  } else if (pieces >= KVQ_TUNE(csome, 8)) {
+    cfg.gridDim = dim3(rows);
+    cfg.blockDim = dim3(8 * 32);
+    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, D, 8>, p);
   } else {
-    cfg.blockDim = dim3(4 * 32);
-    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 4>, p, parts);
+    cfg.gridDim = dim3(rows);
+    cfg.blockDim = dim3(2 * 32);
+    e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, D, 2>, p);
   }
   return cuda_status(e, "paged_decode_fp4 combine launch");
 }
@@ -692,7 +843,7 @@ extern "C" kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void
   if (Hq / Hkv > 8) return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: GQA ratio %d > 8", Hq / Hkv);
   // positions in the stream of pages, and tokens, are 32-bit
   if (static_cast<int64_t>(max_blocks) * kPage > 0x7FFFFFFF - kPage || static_cast<int64_t>(B) * Hq > 0x7FFFFFFF ||
-      static_cast<double>(B) * Hkv * max_blocks > 0x7FFFFFFF - 65536.0)
+      static_cast<double>(B) * Hkv * max_blocks > 0x7F000000)
     return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: problem too large");
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !seq_lens || !out || !workspace)
     return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: null pointer");
@@ -702,14 +853,15 @@ extern "C" kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void
   const size_t need = kvq_decode_fp4_workspace_size(B, Hq, Hkv, D, P, max_blocks);
   if (workspace_bytes < need)
     return fail(KVQ_ERR_INVALID_ARG, "paged_decode_fp4: workspace %zu bytes < %zu needed", workspace_bytes, need);
+  const PageStrides ps = page_strides(k_cache, v_cache, k_page_bytes(kFP4, D), v_page_bytes(kFP4, D));
+  if (static_cast<double>(num_blocks) * Hkv * ps.k >= 64.0 * 0xffffffffu)  // places are 32-bit, in 64-byte units
+    return fail(KVQ_ERR_UNSUPPORTED, "paged_decode_fp4: cache larger than 256 GiB");
   const int64_t rows = fp4_rows(B, Hq, Hkv, max_blocks);
   Fp4Params p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k_cache = static_cast<const uint8_t*>(k_cache);
   p.v_cache = static_cast<const uint8_t*>(v_cache);
-  const PageStrides ps = page_strides(k_cache, v_cache, k_page_bytes(kFP4, D), v_page_bytes(kFP4, D));
-  p.k_str = ps.k;
-  p.v_str = ps.v;
+  p.str = ps.k;  // K and V pages are of one size: ps.v is the same
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.block_table = block_table;
@@ -723,6 +875,7 @@ extern "C" kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void
   p.Hkv = Hkv;
   p.g = Hq / Hkv;
   p.max_blocks = max_blocks;
+  p.parts = fp4_parts(B, Hkv, max_blocks);
   p.num_blocks = num_blocks;
   p.sm_scale = sm_scale;
   p.window = window;

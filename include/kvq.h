@@ -678,11 +678,12 @@ kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, 
  * KVQ_DTYPE_FP4_E2M1 (9/16 of an FP8 cache's bytes).
  *
  *  Arguments as for kvq_paged_decode_attention without the dtype and the split
- *  count.  D in {64, 128}, P == 16, Hq % Hkv == 0, Hq / Hkv <= 8.
+ *  count.  D in {64, 128}, P == 16, Hq % Hkv == 0, Hq / Hkv <= 8; each cache
+ *  below 256 GiB.
  *  workspace  kvq_decode_fp4_workspace_size(...) bytes, 16-byte aligned;
  *             contents on entry are ignored; calls sharing it must not overlap.
  *  The attended pages of all sequences and KV heads are laid end to end and cut
- *  into equal parts, one per CTA, so that ragged batches balance; a part's
+ *  into equal parts, one per warp, so that ragged batches balance; a part's
  *  share of a (sequence, KV head) is merged by log-sum-exps in FP32.  The plan is a
  *  function of the lengths alone: results are deterministic.
  *  Declared rounding: the query enters as f16(fl32(q * sigma)) as for

@@ -5,7 +5,7 @@ import random
 
 import pytest
 
-MIN_PART = 4
+MIN_PART = 2
 
 
 def spans(lens, window, cap):
@@ -19,9 +19,9 @@ def spans(lens, window, cap):
 
 
 def pieces(sp, heads, parts):
-    """(part, sequence, head, first page, count) as the CTAs walk them."""
+    """(part, sequence, head, first page, count) as the warps walk them."""
     total = sum(n for _, n in sp)
-    chunk = max(MIN_PART, (total * heads + parts - 1) // parts)
+    chunk = max(MIN_PART, ((total * heads + parts - 1) // parts + 1) // 2 * 2)
     prefix = [0]
     for _, n in sp:
         prefix.append(prefix[-1] + n)
@@ -45,37 +45,67 @@ def pieces(sp, heads, parts):
 def test_plan(seed):
     rng = random.Random(seed)
     B, heads, sms = rng.choice([1, 2, 7, 60]), rng.choice([1, 2, 8]), rng.choice([1, 3, 152])
-    cap = rng.choice([1, 5, 100])
+    cap = rng.choice([1, 5, 100, 1000])
     lens = [rng.choice([0, 1, 16, 17, rng.randint(0, cap * 16)]) for _ in range(B)]
     window = rng.choice([-1, -1, 1, 40, 500])
-    parts = min(4 * sms, (B * heads * cap + MIN_PART - 1) // MIN_PART)
+    parts = min(12 * sms, (B * heads * cap + MIN_PART - 1) // MIN_PART)
     rows = parts + B * heads
     sp = spans(lens, window, cap)
-    covered, ids, direct = set(), {}, set()
+    total = heads * sum(n for _, n in sp)
+    chunk = max(MIN_PART, ((total + parts - 1) // parts + 1) // 2 * 2)
+    starts, x = {}, 0
+    for b, (_, n) in enumerate(sp):
+        for h in range(heads):
+            starts[b, h] = x
+            x += n
+
+    def joined(part, b, h):
+        """A warp's view, from the piece that its part begins with."""
+        c0 = part // 4 * 4 * chunk
+        c1 = min(total, c0 + 4 * chunk)
+        return c1 - c0 > chunk and starts[b, h] <= c0 and c1 <= starts[b, h] + sp[b][1]
+
+    covered, ids, direct, verdict = set(), {}, set(), {}
     for part, b, h, pg, n in pieces(sp, heads, parts):
         for x in range(pg, pg + n):
             assert (b, h, x) not in covered
             covered.add((b, h, x))
-        if n == sp[b][1]:
+        if part not in [k[1] for k in verdict if k[0] == part // 4]:
+            verdict[part // 4, part] = joined(part, b, h)
+        if verdict[part // 4, part]:
+            at = part // 4 * 4 + b * heads + h  # written once, by all of the CTA's warps
+            assert ids.get(at, (b, h)) == (b, h)
+            ids[at] = (b, h)
+        elif n == sp[b][1]:
             direct.add((b, h))
-            continue
-        at = part + b * heads + h
-        assert at not in ids and 0 <= at < rows
-        ids[at] = (b, h)
-    assert len(covered) == heads * sum(n for _, n in sp)
+        else:
+            at = part + b * heads + h
+            assert at not in ids and 0 <= at < rows
+            ids[at] = (b, h)
+    assert len(covered) == total
+    for cta in {c for c, _ in verdict}:  # the warps of a CTA agree, and those without a part are not waited for
+        views = [v for (c, _), v in verdict.items() if c == cta]
+        assert len(set(views)) == 1
+        if views[0]:
+            assert len(views) == -(-(min(total, (cta + 1) * 4 * chunk) - cta * 4 * chunk) // chunk)
     # the combine
-    total = sum(n for _, n in sp)
-    chunk = max(MIN_PART, (total * heads + parts - 1) // parts)
-    before = 0
-    for b, (_, n) in enumerate(sp):
-        for h in range(heads if n else 0):
-            x = before * heads + h * n
-            first, last = x // chunk, (x + n - 1) // chunk
-            if first == last:
-                assert (b, h) in direct
-                continue
-            assert last < parts
-            for part in range(first, last + 1):
-                assert ids.pop(part + b * heads + h) == (b, h)
-        before += n
+    for (b, h), x in starts.items():
+        n = sp[b][1]
+        if n == 0:
+            continue
+        first, last = x // chunk, (x + n - 1) // chunk
+        if first == last:
+            assert (b, h) in direct
+            continue
+        assert last < parts
+        cta = 4 * chunk
+        c0, c1 = -(-x // cta), (x + n) // cta
+        if x + n == total and total % cta > chunk:
+            c1 = total // cta + 1
+        if c1 > c0:
+            found = [*range(first, 4 * c0), *range(4 * c0, 4 * c1, 4), *range(4 * c1, last + 1)]
+        else:
+            found = list(range(first, last + 1))
+        for part in found:
+            assert ids.pop(part + b * heads + h) == (b, h)
     assert not ids

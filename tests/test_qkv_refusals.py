@@ -127,8 +127,8 @@ def test_fp4_workspace_size(lib):
     f = lib.kvq_decode_fp4_workspace_size
     f.restype, f.argtypes = sz, [i] * 6
     assert f(0, 8, 2, 128, 16, 4) == f(4, 8, 3, 128, 16, 4) == f(4, 8, 2, 96, 16, 4) == f(4, 8, 2, 128, 8, 4) == 0
-    # 4 sequences of 2 KV heads and 4 pages: 8 parts of 4 pages; rows of D + 1 floats, and the pages before each sequence
-    assert f(4, 8, 2, 128, 16, 4) == ((8 + 8) * 4 * 129 + 5) * 4 + 12
+    # 4 sequences of 2 KV heads and 4 pages: 16 parts of 2 pages; rows of D + 1 floats, and the pages before each sequence
+    assert f(4, 8, 2, 128, 16, 4) == ((16 + 8) * 4 * 129 + 5) * 4 + 12
 
 
 def test_other_calls_refuse_the_4_bit_cache(k):
