@@ -617,22 +617,17 @@ def _addresses(*tensors):
     """Addresses of tensors on the current device, whose strides their user has
     checked (None for None)."""
     current = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
-    out = []
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        at = t.get_device()
-        if at != current or at < 0:
-            if at < 0:
+        if t is not None and (current < 0 or t.get_device() != current):
+            if t.get_device() < 0:
                 raise ValueError("libkvq takes CUDA tensors only")
-            raise ValueError(f"the tensors' device (cuda:{at}) must be the current one (cuda:{current})")
-        out.append(t.data_ptr())
-    return out
+            raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one (cuda:{current})")
+    return [None if t is None else t.data_ptr() for t in tensors]
 
 
 def _check_dense(t, dtype, shape, name):
-    _check_tensor(t, dtype, shape, name)
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: libkvq takes contiguous tensors only")
 

@@ -91,7 +91,8 @@ struct Staged {
   static constexpr int kStageB = kKPage + kVPage;
   static constexpr int kStages = 4;
   static constexpr int kThreads = kPage * D / 8;
-  [[maybe_unused]] static constexpr int kCodes = FMT == kFP4 ? kPage * D / 2 : kPage * D * (FMT == kBF16 ? 2 : 1);
+  static constexpr int kCodes = FMT == kFP4 ? kPage * D / 2 : kPage * D * (FMT == kBF16 ? 2 : 1);
+  static_assert(kCodes % 512 == 0 && kStageB % 16 == 0, "whole 16-byte chunks, and whole groups of those that change places");
 
   // Where the V page's 16-byte chunk x goes.
   static KVQ_DEVINL int place(int x) {
@@ -190,7 +191,7 @@ struct Staged {
 
 // A tile's tokens, a chunk of heads.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kPage * D / 8) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kPage * D / 8, 1536 / (2 * D)) gather_kernel(const GatherParams p) {
   using S = Staged<D, FMT>;
   constexpr int LPT = D / 8;
   __shared__ TileTokens tt;

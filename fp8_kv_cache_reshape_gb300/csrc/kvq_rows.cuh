@@ -119,12 +119,18 @@ KVQ_DEVINL float amax8(const float2 (&x)[4]) {
 KVQ_DEVINL float e4m3_value(uint8_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
 }
+// e4m3(fl32(x / s)) of one value.
+KVQ_DEVINL uint32_t quant1_e4m3(float x, const Divisor& d) {
+  const uint32_t w = __nv_cvt_float2_to_fp8x2(make_float2(x * d.lo, x * d.hi), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t lo = w & 0xFF;
+  return lo == w >> 8 && d.ok ? lo : f32_to_e4m3(__fdiv_rn(x, d.s));
+}
 // The E4M3 scale of a block of 16 dims, of which two neighbouring lanes hold
-// eight each, and their E2M1 codes.  s: the head's scale.
-KVQ_DEVINL uint32_t quant8_fp4(const float2 (&x)[4], float s, uint8_t& block_scale) {
+// eight each, and their E2M1 codes.  s: the head's scale, six: Divisor(fl32(6 s)).
+KVQ_DEVINL uint32_t quant8_fp4(const float2 (&x)[4], float s, const Divisor& six, uint8_t& block_scale) {
   float a = amax8(x);
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  block_scale = f32_to_e4m3(__fdiv_rn(a, __fmul_rn(6.f, s)));
+  block_scale = static_cast<uint8_t>(quant1_e4m3(a, six));
   const float step = __fmul_rn(e4m3_value(block_scale), s);
   if (!(step > 0.f)) return 0;
   uint32_t w[2];

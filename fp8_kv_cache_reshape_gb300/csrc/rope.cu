@@ -293,7 +293,8 @@ KVQ_DEVINL void write_v_page(const uint8_t* rows, uint8_t* vp) {
 }
 
 // k and v into the cache: a tile's tokens, heads h0 .. h1 - 1.
-template <int D, int FMT>
+// TURN: k is normed or turned.
+template <int D, int FMT, bool TURN>
 KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0, int h1) {
   using F = Format<FMT>;
   constexpr int LPT = D / 8;
@@ -322,7 +323,8 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
     __syncwarp();  // done with the stages of the 16 tokens before
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
-    const Turn turn = make_turn<D>(p, p.k_weight, row, lane);
+    Turn turn;
+    if constexpr (TURN) turn = make_turn<D>(p, p.k_weight, row, lane);
     for (int h = h0; h < h1; ++h) {
       uint8_t* buf = rows[(h - h0) & 1];
       copy_wait<kStages - 2>();
@@ -331,7 +333,10 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       const uint32_t at = ring + (h - h0) % kStages * (2 * kStageB);
       const uint4 vraw = lds128(at + kStageB + lane * 16);
       float2 ko[4], vo[4];
-      turn_row<D>(turn, p.k_weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), ko);
+      if constexpr (TURN)
+        turn_row<D>(turn, p.k_weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), ko);
+      else
+        unpack8_bf16(lds128(at + lane * 16), ko);
       unpack8_bf16(vraw, vo);
       const int64_t page = slot / kPage * p.Hkv + h;
       uint8_t* kp = p.k_cache + page * p.k_str;
@@ -382,8 +387,9 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
         }
       } else {
         uint8_t ks, vs;
-        const uint32_t kw = quant8_fp4(ko, __ldg(p.k_scale + h), ks);
-        const uint32_t vw = quant8_fp4(vo, __ldg(p.v_scale + h), vs);
+        const float sk = __ldg(p.k_scale + h), sv = __ldg(p.v_scale + h);
+        const uint32_t kw = quant8_fp4(ko, sk, Divisor(__fmul_rn(6.f, sk)), ks);
+        const uint32_t vw = quant8_fp4(vo, sv, Divisor(__fmul_rn(6.f, sv)), vs);
         if (valid) {
           *reinterpret_cast<uint32_t*>(kp + off * (D / 2) + 4 * j) = kw;
           if (page_run) {
@@ -409,7 +415,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
   }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool TURN = true>
 __global__ void __launch_bounds__(kPage * D / 8, 768 / (2 * D)) token_kernel(const TokenParams p) {
   __shared__ __align__(16) uint8_t ring_mem[D / 16 * Ring<D>::kBytes];
   const uint32_t ring = smem_u32(ring_mem) + threadIdx.x / 32 * Ring<D>::kBytes;
@@ -422,11 +428,11 @@ __global__ void __launch_bounds__(kPage * D / 8, 768 / (2 * D)) token_kernel(con
     if constexpr (FMT == kRowsOnly)
       turn_rows<D>(p, ring, false, tile, h, min(p.Hkv, h + p.kv_chunk));
     else
-      cache_rows<D, FMT>(p, ring, tile, h, min(p.Hkv, h + p.kv_chunk));
+      cache_rows<D, FMT, TURN>(p, ring, tile, h, min(p.Hkv, h + p.kv_chunk));
   }
 }
 
-template <int FMT>
+template <int FMT, bool TURN = true>
 kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* where) {
   p.tiles = (p.T - 1) / kPage + 1;
   p.aligned = FMT != kRowsOnly && p.T >= 256;
@@ -439,9 +445,9 @@ kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* wh
   p.kv_ctas = static_cast<unsigned>(kv_ctas);
   const unsigned grid = static_cast<unsigned>(ctas);
   if (D == 64) {
-    token_kernel<64, FMT><<<grid, 128, 0, s>>>(p);
+    token_kernel<64, FMT, TURN><<<grid, 128, 0, s>>>(p);
   } else if (D == 128) {
-    token_kernel<128, FMT><<<grid, 256, 0, s>>>(p);
+    token_kernel<128, FMT, TURN><<<grid, 256, 0, s>>>(p);
   } else if constexpr (FMT == kRowsOnly || FMT == kE4M3 || FMT == kE5M2) {
     token_kernel<256, FMT><<<grid, 512, 0, s>>>(p);
   }
@@ -516,7 +522,7 @@ kvq_status_t write_fp4(const void* k, const void* v, const int64_t* slot_mapping
   p.Hkv = Hkv;
   const kvq_status_t st =
       take_cache(p, slot_mapping, k_cache, v_cache, k_scale, v_scale, kFP4, D, num_blocks, dev_status, "reshape_and_cache");
-  return st != KVQ_OK ? st : launch_tokens<kFP4>(p, D, s, "reshape_and_cache");
+  return st != KVQ_OK ? st : launch_tokens<kFP4, false>(p, D, s, "reshape_and_cache");
 }
 
 }  // namespace kvq
