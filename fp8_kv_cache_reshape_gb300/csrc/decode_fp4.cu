@@ -799,11 +799,11 @@ kvq_status_t launch_fp4(const Fp4Params& p, cudaStream_t s) {
   const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
   // few rows have many pieces (about four of which are one row of partials): more warps, 32 dims to a CTA
   const int64_t pieces = p.parts / (static_cast<int64_t>(p.B) * p.Hkv);
-  if (pieces >= KVQ_TUNE(cmany, 512)) {
+  if (pieces >= 512) {
     cfg.gridDim = dim3(rows, D / 32);
     cfg.blockDim = dim3(32 * 32);
     e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, 32, 32>, p);
-  } else if (pieces >= KVQ_TUNE(csome, 8)) {
+  } else if (pieces >= 8) {
     cfg.gridDim = dim3(rows);
     cfg.blockDim = dim3(8 * 32);
     e = cudaLaunchKernelEx(&cfg, decode_fp4_combine_kernel<D, D, 8>, p);

@@ -5,9 +5,6 @@
 
 #include <cuda_fp4.h>
 
-#ifndef KVQ_TUNE
-#define KVQ_TUNE(name, value) value
-#endif
 
 #include "kvq_device.cuh"
 

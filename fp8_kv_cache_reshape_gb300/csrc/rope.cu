@@ -115,7 +115,7 @@ KVQ_DEVINL Turn make_turn(const TokenParams& p, const __nv_bfloat16* weight, int
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     t.a[i] = w[i];
-    t.b[i] = make_float2(0.f, 0.f);
+    t.b[i] = make_float2(-0.f, -0.f);  // x * 1 + 0 * -0 is x, a negative zero too
   }
   auto angle = [&](int pair, float& s, float& c) {
     int axis = p.rotary.pair_axis ? __ldg(p.rotary.pair_axis + pair) : 0;
@@ -437,8 +437,8 @@ kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* wh
   p.tiles = (p.T - 1) / kPage + 1;
   p.aligned = FMT != kRowsOnly && p.T >= 256;
   p.kv_tiles = p.tiles + (p.aligned ? 1 : 0);
-  p.kv_chunk = heads_per_cta(p.Hkv, p.kv_tiles, 8, KVQ_TUNE(kvw, 128) * sm_count() / D);
-  p.q_chunk = heads_per_cta(p.Hq, p.tiles, 32, KVQ_TUNE(qw, 2) * sm_count());
+  p.kv_chunk = heads_per_cta(p.Hkv, p.kv_tiles, 8, 128 * sm_count() / D);
+  p.q_chunk = heads_per_cta(p.Hq, p.tiles, 32, 2 * sm_count());
   const int64_t kv_ctas = static_cast<int64_t>(p.kv_tiles) * ((p.Hkv + static_cast<int64_t>(p.kv_chunk) - 1) / p.kv_chunk);
   const int64_t ctas = kv_ctas + static_cast<int64_t>(p.tiles) * ((p.Hq + static_cast<int64_t>(p.q_chunk) - 1) / p.q_chunk);
   if (ctas > 0x7FFFFFFF) return fail(KVQ_ERR_UNSUPPORTED, "%s: problem too large", where);
@@ -480,8 +480,8 @@ kvq_status_t take_turn(TokenParams& p, const kvq_head_norm_t* norm, const kvq_ro
         !aligned(rotary->pair_axis, 4))
       return fail(KVQ_ERR_INVALID_ARG, "%s: rotary tables null or misaligned", where);
     if (!(std::fabs(rotary->scale) <= FLT_MAX)) return fail(KVQ_ERR_INVALID_ARG, "%s: bad rotary scale", where);
-    if (rotary->num_axes > 1 && rotary->positions_stride < p.T)
-      return fail(KVQ_ERR_INVALID_ARG, "%s: positions_stride < T", where);
+    if (rotary->num_axes > 1 && rotary->positions_stride != 0 && rotary->positions_stride < p.T)
+      return fail(KVQ_ERR_INVALID_ARG, "%s: positions_stride must be 0 or at least T", where);
     p.rotary = *rotary;
   }
   return KVQ_OK;

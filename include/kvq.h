@@ -562,9 +562,10 @@ kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_stride, void
  * 1; dims from rot_dim on pass as they are.  The pages have no counterpart.
  *
  *  positions    int64 [num_axes][T], row a at positions + a *
- *               positions_stride; any value.  One axis: the token's place in
- *               its text.  Several: time, height and width of an image's or
- *               video's patch, each pair following one of them.
+ *               positions_stride (at least T, or 0: one row for all axes); any
+ *               value.  One axis: the token's place in its text.  Several: time,
+ *               height and width of an image's or video's patch, each pair
+ *               following one of them.
  *  inv_freq     float32 [rot_dim / 2], radians per position, finite.  The
  *               angle is the exact product reduced in 64-bit fixed point: off
  *               by at most 2^-31 of a turn for |positions| up to 2^31 and

@@ -184,6 +184,34 @@ def test_graphs_that_share_a_workspace_and_a_side_stream():
         assert torch.equal(eager, outs[0])
 
 
+def test_memory_given_back_by_another_stream_is_left_alone():
+    """A call without a workspace on a side stream, while the current stream still writes memory that it has given back."""
+    k = _k()
+    args, ref, tol, kw = _case([2000, 31, 700], 2, 4, 128)
+    alone, _ = _run(args, kw)
+    size = k.kvq_decode_fp4_workspace_size(3, 8, 2, 128, args[5].shape[1])
+    side, big, out = torch.cuda.Stream(), torch.ones(4096, 4096, device="cuda"), torch.zeros_like(alone)
+    torch.cuda.synchronize()
+    given_back = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        big @ big
+    for _ in range(300):
+        given_back.fill_(0xFF)
+    del given_back
+    k.kvq_paged_decode_attention_fp4(*args, out, stream=side, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out, alone)
+
+
+@pytest.mark.parametrize("lengths,heads,group", [([20000], 1, 8), ([30000, 5], 8, 4), ([4096] * 3, 4, 2)])
+def test_long(lengths, heads, group):
+    """Many pieces to a row, whole CTAs of one sequence and KV head, and parts that end in others."""
+    args, ref, tol, kw = _case(lengths, heads, group, 128)
+    out, st = _run(args, kw)
+    assert st == 0
+    assert_within(out, ref, tol)
+
+
 def test_offsets_beyond_32_bits():
     """A cache of more than 4 GiB per tensor, its last pages used."""
     k = _k()

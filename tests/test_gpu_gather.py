@@ -46,8 +46,8 @@ def _check(k, slots, caches, scales, want, **kw):
 
 
 @pytest.mark.parametrize("dtype,per_token", [(FP8, False), (FP8_E5M2, False), (FP8, True), (FP8_E5M2, True), (BF16, False)])
-@pytest.mark.parametrize("dim,heads,paired", [(64, 3, False), (128, 2, True)])
-@pytest.mark.parametrize("n", [1, 16, 100, 555])
+@pytest.mark.parametrize("dim,heads,paired,n", [(64, 3, False, 1), (64, 3, False, 16), (128, 2, True, 100), (128, 2, True, 555), (64, 5, True, 10000),
+                                                (128, 6, False, 10000)])
 def test_formats(dtype, per_token, dim, heads, paired, n):
     from oracle import e4m3, e5m2
     pool = Pool(-(-n // P) + 4, heads, dim, dtype, 3, per_token)
@@ -70,8 +70,7 @@ def test_formats(dtype, per_token, dim, heads, paired, n):
     _check(_k(), slots, pool.device(paired), pool.device_scales(), want, cache_dtype=dtype, per_token=per_token)
 
 
-@pytest.mark.parametrize("dim,heads,paired", [(64, 3, True), (128, 2, False)])
-@pytest.mark.parametrize("n", [1, 16, 100, 555])
+@pytest.mark.parametrize("dim,heads,paired,n", [(64, 3, True, 1), (64, 3, True, 16), (128, 2, False, 100), (128, 2, False, 555), (64, 5, False, 10000)])
 def test_fp4(dim, heads, paired, n):
     pool = Pool4(-(-n // P) + 4, heads, dim, 3)
     table = pool.table([n])

@@ -100,6 +100,25 @@ def test_far_positions(pos):
     _rows_ok(out, *_expected(qh, dict(positions=np.array(pos), inv_freq=inv), None, False, 1.0))
 
 
+@pytest.mark.parametrize("T,Hq,H,D", [(5000, 35, 9, 64), (2600, 33, 10, 128)])
+def test_norm_rope_many_heads_to_a_cta(T, Hq, H, D):
+    (q, kk, _), (qh, kh, _) = _inputs(T, Hq, H, D)
+    dev, more, host, w = _turn(T, D // 2, 2, True, D, 100000)
+    qo, ko = (torch.full(x.shape, 9.0, dtype=torch.bfloat16, device="cuda") for x in (q, kk))
+    _k().kvq_qk_norm_rope(q, kk, **dev, q_out=qo, k_out=ko, **more)
+    _rows_ok(qo, *_expected(qh, host, w[0], False, 1.0))
+    _rows_ok(ko, *_expected(kh, host, w[1], False, 1.0))
+
+
+def test_one_row_of_positions_for_all_axes():
+    (q, kk, _), _ = _inputs(40, 2, 1, 64)
+    pos, inv = torch.randint(0, 9999, (40,)).cuda(), torch.rand(32).cuda()
+    outs = [torch.zeros_like(q) for _ in range(2)]
+    _k().kvq_qk_norm_rope(q, None, pos, inv, outs[0], None)
+    _k().kvq_qk_norm_rope(q, None, pos.expand(3, 40), inv, outs[1], None, pair_axis=(torch.arange(32) % 3).int().cuda())
+    assert torch.equal(*outs)
+
+
 def test_zero_rows_and_values_beyond_float32_squares():
     q = torch.zeros(3, 1, 64, dtype=torch.bfloat16, device="cuda")
     q[1, 0, 5] = 1e18
@@ -217,6 +236,12 @@ def test_rope_and_cache(T, Hq, H, D, rot, axes, norm, interleaved, kind, fmt, pe
     _check_append(T, Hq, H, D, rot, axes, norm, interleaved, kind, fmt, per_token, paired)
 
 
+@pytest.mark.parametrize("fmt,per_token", FORMATS)
+@pytest.mark.parametrize("T,H,D,kind", [(5000, 5, 64, "sequences"), (2600, 10, 128, "middle"), (2600, 3, 128, "any")])
+def test_rope_and_cache_many_heads_to_a_cta(T, H, D, kind, fmt, per_token):
+    _check_append(T, 2 * H, H, D, D, 1, True, False, kind, fmt, per_token, False)
+
+
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("kind", ["middle", "steps"])
 def test_rope_and_cache_head_dim_256(fmt, kind):
@@ -315,6 +340,36 @@ def test_without_norm_or_rotation_the_bytes_are_those_of_the_plain_write():
         else:
             k.kvq_reshape_and_cache(kk.contiguous(), v.contiguous(), sd, *b, *scales, cache_dtype=name)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]), fmt
+
+
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -7, 3.0, 0.011, 1e-38, 2.0 ** -126, 1e-44, 2.0 ** 120, 3e38])
+def test_quotients_are_those_of_a_division(scale):
+    """Scales that give many ties, that are powers of two, and beyond those that the enclosure covers: the bytes of the plain write."""
+    k = _k()
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(64, 2, 64, generator=gen).bfloat16()
+    x[:20] = (x[:20].float() * min(scale, 1e36)).bfloat16()
+    x[20:24] = torch.arange(4 * 2 * 64).view(4, 2, 64).bfloat16()
+    x[24] = 0
+    x = x.cuda()
+    slots = torch.arange(5, 69).cuda()
+    s = torch.full((2,), scale, device="cuda")
+    for name in ("fp8_e4m3", "fp8_e5m2"):
+        a, b = (k.alloc_kv_cache(6, 2, 64, name, fill=0) for _ in range(2))
+        k.kvq_rope_and_cache(None, x, x, None, None, slots, *a, s, s, cache_dtype=name)
+        k.kvq_reshape_and_cache(x, x, slots, *b, s, s, cache_dtype=name)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    q8, want = (torch.zeros(64, 2, 64, dtype=torch.uint8, device="cuda") for _ in range(2))
+    k.kvq_rope_and_cache(x, x, x, None, None, slots, *a, s, s, q8=q8, q_scale=s[:1], cache_dtype=name)
+    k.kvq_quantize_query(x, want, s[:1])
+    assert torch.equal(q8, want)
+    kd, vd = k.alloc_kv_cache(6, 2, 64, "fp4", fill=0)
+    k.kvq_reshape_and_cache(x, x, slots, kd, vd, s, s, cache_dtype="fp4")
+    codes, sb, vc, vsb = e2m1.from_pages(kd.cpu().numpy(), vd.cpu().numpy(), 64)
+    at, off = np.arange(5, 69) // P, np.arange(5, 69) % P
+    want = e2m1.quantize(x.float().cpu().numpy(), np.float32(scale))
+    for got, ref in ((codes, want[0]), (sb, want[1]), (vc, want[0]), (vsb, want[1])):
+        assert np.array_equal(got[at, :, off], ref)
 
 
 def test_fp4_write_against_the_oracle():

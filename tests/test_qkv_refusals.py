@@ -238,3 +238,26 @@ def test_fp4_allocation(k):
     for bad in ({"per_token": True}, {"head_dim": 256}):
         with pytest.raises(ValueError):
             k.alloc_kv_cache(**{**dict(num_blocks=7, kv_heads=2, head_dim=128, cache_dtype="fp4", device="cpu"), **bad})
+
+
+class _OnGpu:
+    def __init__(self, index):
+        self.index = index
+
+    def get_device(self):
+        return self.index
+
+    def data_ptr(self):
+        return 16 * self.index
+
+
+def test_tensors_of_another_device_are_refused(k, monkeypatch):
+    """Any of them, whatever its place in the call."""
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    assert k._addresses(None, _OnGpu(1), _OnGpu(1)) == [None, 16, 16]
+    for bad in ((_OnGpu(0),), (_OnGpu(1), None, _OnGpu(0))):
+        with pytest.raises(ValueError, match=r"cuda:0\) must be the current one \(cuda:1\)"):
+            k._addresses(*bad)
+    with pytest.raises(ValueError, match="CUDA tensors only"):
+        k._addresses(_OnGpu(1), torch.zeros(1))
