@@ -10,16 +10,23 @@
 // moves to the other operand, P, one multiplication for two weights instead of one
 // for every two of V's 16 x 16 values.
 //
-// Bound: memory, 9/16 byte per element of K and V.
+// Bound: memory, 9/16 byte per element of K and V, and close behind it the issue
+// slots (58% full; ALU pipe 48%: half of it the conversions, an instruction for
+// two codes).  Over longer contexts a call grows by 28 us per 128K tokens of 8 KV
+// heads of 128, 5.4 TB/s; with the scores alone, or the outputs alone, it grows by 22,
+// the copies' own time.  One request of 128K: 38 us, 4.0 TB/s with its fixed
+// part of about 10; eight of 20K: 48 us, 4.0 TB/s.
 //
-// Layout.  A warp takes two pages (32 tokens of a KV head) at a time from two
-// stages of its own in shared memory, filled by 16-byte asynchronous copies: no
-// barrier, no producer warp, nothing between warps.  The
-// page format is the MMA operand order (m16n8k16, tokens as the rows of K Q^T,
-// dims as the rows of V^T P^T), so that a lane reads its whole share of a page
-// with 16-byte loads: lane 4 r + c holds dims 32 c .. 32 c + 31 (at head dim
-// 128) of tokens r and r + 8 of K, and tokens 2c, 2c + 1, 2c + 8, 2c + 9 of
-// dims 2r, 2r + 1 of each 16 of V.
+// Layout.  A warp takes two pages (32 tokens of a KV head) at a time from stages
+// of its own in shared memory, filled by 16-byte asynchronous copies: no barrier,
+// no producer warp, nothing between warps but the joining at the end.  The page
+// format is the MMA operand order (m16n8k16, tokens as the rows of K Q^T, dims as the
+// rows of V^T P^T), so that a lane reads its share of a page with wide loads: lane 4 r + c
+// holds dims 32 c .. 32 c + 31 (at head dim 128) of tokens r and r + 8 of K, and
+// tokens 2c, 2c + 1, 2c + 8, 2c + 9 of dims 2r, 2r + 1 of each 16 of V.
+//
+// The page stream.  All sequences' and KV heads' attended pages end to end, cut
+// into one part per warp; a part's share of a (sequence, KV head) is a piece.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -33,7 +40,7 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 3;         // 168 registers a thread (four, with 128 and spills: 128K 42.2 against 40.2 us)
 constexpr int kMinPart = 2;           // pages of a part, at least: a pair
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
@@ -97,7 +104,9 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false) {
 KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, ((total + parts - 1) / parts + 1) & ~1); }
 
 // Where a warp's part [pos, end) of the page stream begins: in sequence b, `before`
-// pages (of one KV head) after the stream's start.
+// pages (of one KV head) after the stream's start.  Lengths that another stream
+// changes while the call runs give wrong results, but every loop here ends, every
+// address stays inside its table, and the warps of a CTA agree on who waits for whom.
 struct Part {
   int pos, end, b, before;
   int chunk, total;  // pages of a part, of the stream
@@ -122,7 +131,7 @@ KVQ_DEVINL Part find_part(const Fp4Params& p, int index, int lane) {
   r.end = min(r.total, r.pos + r.chunk);
   r.b = r.before = 0;
   if (r.pos >= r.end) return r;
-  for (int b0 = 0, x = 0;; b0 += 32) {  // 32 sequences at a time; the one is there: pos < total
+  for (int b0 = 0, x = 0; b0 < p.B; b0 += 32) {  // 32 sequences at a time
     const int n = b0 == 0 ? n0 : b0 + lane < p.B ? span_of(p, b0 + lane).n : 0;
     const int incl = x + scan_add(n, lane);
     const unsigned past = __ballot_sync(0xffffffffu, r.pos < incl * p.Hkv);
@@ -134,6 +143,8 @@ KVQ_DEVINL Part find_part(const Fp4Params& p, int index, int lane) {
     }
     x = __shfl_sync(0xffffffffu, incl, 31);
   }
+  r.end = r.pos;  // not there: lengths that changed meanwhile
+  return r;
 }
 
 KVQ_DEVINL void write_prefix(const Fp4Params& p, int lane) {
@@ -472,7 +483,11 @@ struct Feeder {
 
   KVQ_DEVINL void piece(const Fp4Params& p, int lane) {
     const int within = pos - before * p.Hkv;
-    h = within / sp.n;
+    h = sp.n > 0 && within >= 0 ? within / sp.n : p.Hkv;
+    if (h >= p.Hkv) {  // lengths that changed meanwhile
+      pos = end;
+      return;
+    }
     pg = within - h * sp.n;
     stop = min(sp.n, pg + end - pos);
     flags = kFirst | (stop - pg == sp.n ? kWhole : 0);
@@ -491,9 +506,9 @@ struct Feeder {
     end = part.end;
     b = part.b;
     before = part.before;
-    if (pos >= end) return;
+    h = 0;
     sp = span_of(p, b);
-    piece(p, lane);
+    if (pos < end) piece(p, lane);
   }
   // The next stage's copies (none when the part is through), as one group.
   KVQ_DEVINL void feed(const Fp4Params& p, uint32_t stage, Meta* meta, int lane) {
@@ -532,18 +547,17 @@ struct Feeder {
       pg += n;
       pos += n;
       if (pg == stop && pos < end) {  // the next piece
-        if (h + 1 == p.Hkv) {         // of the next sequence with pages (there is one: pos < end)
+        if (h + 1 == p.Hkv) {         // of the next sequence with pages
           before += sp.n;
-          ++b;
-          while (true) {
+          sp.n = 0;
+          for (++b; b < p.B; b += 32) {
             const unsigned some = __ballot_sync(0xffffffffu, b + lane < p.B && span_of(p, min(b + lane, p.B - 1)).n > 0);
             if (some) {
               b += __ffs(some) - 1;
+              sp = span_of(p, b);
               break;
             }
-            b += 32;
           }
-          sp = span_of(p, b);
         }
         piece(p, lane);
       }
@@ -560,6 +574,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Meta s_meta[kWarps][F::kStages];
   __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+  __shared__ int s_view[kWarps];   // each warp's: no part, a part of its own, one of those that may be joined
+  __shared__ int s_first[kWarps];  // the (sequence, KV head) that it begins with
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int index = blockIdx.x * kWarps + warp;
   grid_dependency_wait();
@@ -569,16 +585,24 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
 
   const uint32_t ring = smem_u32(smem) + warp * F::kRingB;
   Meta* const meta = s_meta[warp];
-  if (part.pos >= part.end) return;
   Feeder<D> feeder;
   feeder.start(p, part, lane);
   // Are all of the CTA's parts, more than one, of one (sequence, KV head)?  Then
-  // their states meet at the end: one row of partials instead of four.
+  // their states meet at the end: one row of partials instead of four.  The warps
+  // tell each other, so that all of them go by the same answer.
   const int c0 = (index - warp) * part.chunk, c1 = min(part.total, c0 + kWarps * part.chunk);
   const int x0 = feeder.before * p.Hkv + feeder.h * feeder.sp.n;
-  const bool joined = c1 - c0 > part.chunk && x0 <= c0 && c1 <= x0 + feeder.sp.n;
+  const bool some = part.pos < part.end;
+  if (lane == 0) s_view[warp] = !some ? 0 : c1 - c0 > part.chunk && x0 <= c0 && c1 <= x0 + feeder.sp.n ? 2 : 1;
+  __syncthreads();
+  if (!some) return;
+  bool joined = true;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) joined = joined && s_view[w] != 1;
+  const int part_b = feeder.b, part_h = min(feeder.h, p.Hkv - 1);
+  if (lane == 0) s_first[warp] = part_b * p.Hkv + part_h;
   Span sp = feeder.sp;
-  const typename Attend<D>::Raw raw = Attend<D>::fetch(p, feeder.b, feeder.h, lane);  // ahead of the copies
+  const typename Attend<D>::Raw raw = Attend<D>::fetch(p, part_b, part_h, lane);  // ahead of the copies
   feeder.feed(p, ring, meta, lane);
   feeder.feed(p, ring + F::kStageB, meta + 1, lane);
   // Stage i's scores are taken together with stage i - 1's outputs: two independent
@@ -601,7 +625,10 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
       if (joined) break;
       at.finish(p, index, before, lane);
     }
-    if (m.flags == 0) return;
+    if (m.flags == 0) {
+      if (joined) break;  // a part without a stage: lengths that changed meanwhile
+      return;
+    }
     if (m.flags & kFirst) {
       if (i > 0) {
         at.begin(p, Attend<D>::fetch(p, m.b, m.h, lane), lane);
@@ -628,12 +655,14 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
     here = next;
   }
   {
-    const Meta& m = before;
+    copy_wait<0>();
     __syncwarp();  // the stages are read, and no copies are left in flight
     at.show(reinterpret_cast<float*>(smem + warp * F::kRingB), s_m[warp], s_l[warp], lane);
-    const int warps = (c1 - c0 + part.chunk - 1) / part.chunk;
+    int warps = 0;  // with a part: the first ones
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) warps += s_view[w] != 0;
     named_bar_sync(1, warps * 32);
-    const int64_t id = index - warp + static_cast<int64_t>(m.b) * p.Hkv + m.h;
+    const int64_t id = index - warp + static_cast<int64_t>(s_first[warp]);
     for (int x = threadIdx.x; x < p.g * (D / 2); x += warps * 32) {  // two dims
       const int qh = x / (D / 2), d = x % (D / 2) * 2;
       float mw[kWarps], lw[kWarps];

@@ -1,7 +1,10 @@
 // kvq_gather_cache: cached tokens back as bf16 rows.
 //
 // value = bf16(fl32(code * scale)).  Bound: memory (codes in, two bytes per
-// element out).
+// element out): 32,763 tokens of 8 KV heads of 128 from an E4M3 cache in 34 us,
+// 5.9 TB/s of the measured copy rate of 6.8 (66 us with each token's V bytes read one by
+// one, 51 us as whole words with the next head's in registers); 16,000 from a 4-bit
+// cache in 18.5 us, 4.5 TB/s, where conversions share the limit.
 #include "kvq_host.h"
 #include "kvq_rows.cuh"
 
@@ -189,7 +192,8 @@ struct Staged {
   }
 };
 
-// A tile's tokens, a chunk of heads.
+// A tile's tokens, a chunk of heads.  Six CTAs of 256 threads an SM (40
+// registers): with five 35.5 us for the 32,763 tokens, with eight, spilling, 41.
 template <int D, int FMT>
 __global__ void __launch_bounds__(kPage * D / 8, 1536 / (2 * D)) gather_kernel(const GatherParams p) {
   using S = Staged<D, FMT>;
@@ -246,8 +250,9 @@ __global__ void __launch_bounds__(kPage * D / 8, 1536 / (2 * D)) gather_kernel(c
 
 template <int FMT>
 kvq_status_t launch_gather(GatherParams& p, int D, cudaStream_t s) {
-  p.aligned = p.T >= 64;
+  p.aligned = p.T >= 64;  // no difference below, nor for tokens each of another page
   p.tiles = (p.T - 1) / kPage + 1 + (p.aligned ? 1 : 0);
+  // heads to a CTA: 4 where that leaves work for every SM (8 of them: 35.8 us for the 32,763 tokens)
   p.chunk = heads_per_cta(p.Hkv, p.tiles, 4, 4 * sm_count());
   const int64_t ctas = static_cast<int64_t>(p.tiles) * ((p.Hkv + static_cast<int64_t>(p.chunk) - 1) / p.chunk);
   if (ctas > 0x7FFFFFFF) return fail(KVQ_ERR_UNSUPPORTED, "gather_cache: problem too large");

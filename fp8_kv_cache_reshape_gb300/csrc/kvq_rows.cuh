@@ -5,7 +5,6 @@
 
 #include <cuda_fp4.h>
 
-
 #include "kvq_device.cuh"
 
 namespace kvq {
@@ -61,9 +60,9 @@ KVQ_DEVINL uint4 pack8_bf16(const float2 (&x)[4]) {
 // that enclose 1 / s: rounding is monotone.  Two products per value instead of a
 // division; where they disagree (x / s within 2^-20 of a midpoint between codes, one
 // value in 10^5 unless the scale is a ratio of small numbers) the eight values
-// are divided.  A power of two needs no enclosure: x * (1 / s) is x / s.  A chunk
-// of 4,096 tokens with 32 query heads quantized and 8 KV heads of 128 into an
-// E4M3 cache: 39.6 us with divisions.
+// are divided.  A power of two needs no enclosure: x * (1 / s) is x / s.  4,096
+// tokens with 32 query heads quantized and 8 KV heads of 128 into an E4M3 cache:
+// 39.6 us with divisions, 28.6 so.
 struct Divisor {
   float s, lo, hi;
   bool ok;  // 1 / s is a normal number

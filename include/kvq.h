@@ -1,6 +1,6 @@
 /*
  * kvq.h -- C ABI of libkvq: FP8 (E4M3) KV-cache quantization and attention
- * over a paged FP8 (or BF16) KV cache, for NVIDIA GB300 (sm_103a).
+ * over a paged FP8 (or BF16, or 4-bit) KV cache, for NVIDIA GB300 (sm_103a).
  *
  * The operations follow the statement of the method on these pages:
  *  [vLLM]   "The state of FP8 KV-cache and attention quantization in vLLM"
