@@ -259,7 +259,10 @@ def kvq_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_
     dt = _dtype_code(cache_dtype)
     num_blocks = _num_blocks(k_cache, v_cache, Hkv, _page_bytes(D, dt))
     if dt == KVQ_DTYPE_FP4_E2M1:
-        _check_cache(k_cache, v_cache, Hkv, D, dt, False, num_blocks)
+        for t, name in ((k, "k"), (v, "v")):
+            _check_dense(t, torch.bfloat16, (T, Hkv, D), name)
+        _check_dense(slot_mapping, torch.int64, (T,), "slot_mapping")
+        _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, False, num_blocks)
     _check(lib.kvq_reshape_and_cache(_ptr(k), _ptr(v), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
                                      _ptr(k_scale), _ptr(v_scale), T, Hkv, D, PAGE, num_blocks, dt,
                                      _ptr(dev_status), _stream(stream)), "kvq_reshape_and_cache")

@@ -74,6 +74,15 @@ def test_more_sequences_than_threads_of_a_cta():
     assert_within(out, ref, tol)
 
 
+@pytest.mark.parametrize("lengths,dim", [([70, 0, 5], 128), ([1], 64), ([333] * 9, 64)])
+def test_a_table_much_wider_than_the_sequences(lengths, dim):
+    """Parts without pages, and CTAs without parts."""
+    args, ref, tol, kw = _case(lengths, 3, 2, dim, width=1500)
+    out, st = _run(args, kw)
+    assert st == 0
+    assert_within(out, ref, tol)
+
+
 def test_many_short_sequences():
     lengths = [1 + (37 * b) % 75 for b in range(400)]
     args, ref, tol, kw = _case(lengths, 2, 4, 64)

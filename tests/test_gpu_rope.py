@@ -330,6 +330,7 @@ def test_without_norm_or_rotation_the_bytes_are_those_of_the_plain_write():
     for fmt, per_token in FORMATS:
         name = {"e4m3": "fp8_e4m3", "e5m2": "fp8_e5m2"}.get(fmt, fmt)
         (_, kk, v), _ = _inputs(77, 1, 3, 128, seed=4)
+        kk[5], v[6, 1], kk[30, 2], v[30] = 0, 0, 0, 0  # tokens of zeros
         slots, blocks = _slots(77, "middle")
         sd = torch.from_numpy(slots).cuda()
         scales = () if per_token or fmt == "bf16" else (torch.full((3,), 0.011, device="cuda"), torch.full((3,), 0.017, device="cuda"))
@@ -413,6 +414,25 @@ def test_bad_slots(fmt, per_token):
     scales = {} if per_token or fmt == "bf16" else dict(k_scale=one, v_scale=one)
     k.kvq_rope_and_cache(None, kk, v, None, None, slots, kd, vd, **scales, cache_dtype=name, per_token=per_token, dev_status=st)
     assert int(st) == k.KVQ_DEV_BAD_SLOT and torch.all(kd == 1) and torch.all(vd == 1)
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_queries_in_place_beside_their_keys(T):
+    """In the projection's own memory, whose k and v go to the cache: the bits of a call with an output of its own."""
+    k = _k()
+    dev, more, _, _ = _turn(T, 128, 1, True, 128, 9999)
+    slots, blocks = _slots(T, "middle")
+    sd, s = torch.from_numpy(slots).cuda(), torch.full((2,), 0.01, device="cuda")
+    found = []
+    for own in (True, False):
+        (q, kk, v), _ = _inputs(T, 6, 2, 128, seed=2)
+        before = (kk.clone(), v.clone())
+        cache = k.alloc_kv_cache(blocks, 2, 128, fill=0)
+        out = torch.empty(T, 6, 128, dtype=torch.bfloat16, device="cuda") if own else q
+        k.kvq_rope_and_cache(q, kk, v, **dev, slot_mapping=sd, k_cache=cache[0], v_cache=cache[1], k_scale=s, v_scale=s, q_out=out, **more)
+        assert torch.equal(kk, before[0]) and torch.equal(v, before[1])
+        found.append((out.contiguous(), *cache))
+    assert all(torch.equal(a, b) for a, b in zip(*found))
 
 
 def test_no_tokens():

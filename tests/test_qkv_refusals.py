@@ -218,7 +218,10 @@ wide = torch.zeros(T, Hq, 2 * D, dtype=bf16)
     (_decode, {"q": torch.zeros(T, Hq, D)}, "q must"), (_decode, {"bt": torch.zeros(T, 2, dtype=torch.int64)}, "block_table"),
     (_decode, {"sl": torch.zeros(T + 1, dtype=torch.int32)}, "seq_lens"), (_decode, {"vs": torch.ones(H + 1)}, "v_scale"),
     (_decode, {"k4": torch.zeros(NB, H, 16 * D, dtype=torch.uint8)}, "alloc_kv_cache"), (_decode, {"num_blocks": NB + 1}, "num_blocks"),
-    (_decode, {"qo": torch.zeros(T, Hq, D)}, "out must"), (_write, {"k4": torch.zeros(NB, H, 16 * D, dtype=torch.uint8)}, "alloc_kv_cache")])
+    (_decode, {"qo": torch.zeros(T, Hq, D)}, "out must"), (_write, {"k4": torch.zeros(NB, H, 16 * D, dtype=torch.uint8)}, "alloc_kv_cache"),
+    (_write, {"v": torch.zeros(T - 1, H, D, dtype=bf16)}, "v must"), (_write, {"slots": torch.zeros(T - 1, dtype=torch.int64)}, "slot_mapping"),
+    (_write, {"ks": torch.ones(H + 1)}, "k_scale"), (_gather, {"ko": torch.zeros(H, T, D, dtype=bf16).transpose(0, 1)}, "contiguous"),
+    (_decode, {"q": torch.zeros(T, D, Hq, dtype=bf16).transpose(1, 2)}, "contiguous")])
 def test_binding_refuses(k, call, change, words):
     with pytest.raises(ValueError, match=words):
         call(k, **change)
