@@ -79,32 +79,58 @@ struct Divisor {
     hi = exact ? r : r * (1.f + 0x1p-21f);
   }
 };
-// code(fl32(x / s)) of eight values, code2 taking two at a time to the bits of `W`.
-template <int W, typename Code2>
-KVQ_DEVINL void code8(const float2 (&x)[4], const Divisor& d, Code2 code2, uint32_t (&w)[2]) {
-  constexpr int kPer = 32 / W;  // pairs per word
-  const float2 lo = make_float2(d.lo, d.lo), hi = make_float2(d.hi, d.hi);
-  uint32_t other[2] = {0, 0};
-  w[0] = w[1] = 0;
+// Four values' FP8 codes, eight values' E2M1 codes, nearest even, saturating.
+template <bool E5>
+KVQ_DEVINL uint32_t fp8x4(float2 a, float2 b) {
+  uint32_t w;
+  if constexpr (E5)
+    asm("{\n\t.reg .b16 u, v;\n\tcvt.rn.satfinite.e5m2x2.f32 u, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 v, %4, %3;\n\t"
+        "mov.b32 %0, {u, v};\n\t}" : "=r"(w) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  else
+    asm("{\n\t.reg .b16 u, v;\n\tcvt.rn.satfinite.e4m3x2.f32 u, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 v, %4, %3;\n\t"
+        "mov.b32 %0, {u, v};\n\t}" : "=r"(w) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return w;
+}
+KVQ_DEVINL uint32_t e2m1x8(const float2 (&x)[4]) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
+  return w;
+}
+KVQ_DEVINL void scale8(const float2 (&x)[4], float f, float2 (&y)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i / kPer] |= code2(fmul2(x[i], lo)) << (W * (i % kPer));
-    other[i / kPer] |= code2(fmul2(x[i], hi)) << (W * (i % kPer));
-  }
-  if (w[0] != other[0] || w[1] != other[1] || !d.ok) {
-    w[0] = w[1] = 0;
+  for (int i = 0; i < 4; ++i) y[i] = fmul2(x[i], make_float2(f, f));
+}
+KVQ_DEVINL void divide8(const float2 (&x)[4], float s, float2 (&y)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i / kPer] |= code2(make_float2(__fdiv_rn(x[i].x, d.s), __fdiv_rn(x[i].y, d.s))) << (W * (i % kPer));
-  }
+  for (int i = 0; i < 4; ++i) y[i] = make_float2(__fdiv_rn(x[i].x, s), __fdiv_rn(x[i].y, s));
 }
 // fp8(fl32(x / s)) of eight values.
 template <bool E5>
 KVQ_DEVINL uint2 quant8_fp8(const float2 (&x)[4], const Divisor& d) {
-  constexpr auto kind = E5 ? __NV_E5M2 : __NV_E4M3;
-  uint32_t w[2];
-  code8<16>(x, d, [](float2 v) -> uint32_t { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, kind); }, w);
-  return make_uint2(w[0], w[1]);
+  float2 lo[4], hi[4];
+  scale8(x, d.lo, lo);
+  scale8(x, d.hi, hi);
+  uint2 w = make_uint2(fp8x4<E5>(lo[0], lo[1]), fp8x4<E5>(lo[2], lo[3]));
+  if (w.x != fp8x4<E5>(hi[0], hi[1]) || w.y != fp8x4<E5>(hi[2], hi[3]) || !d.ok) {
+    divide8(x, d.s, lo);
+    w = make_uint2(fp8x4<E5>(lo[0], lo[1]), fp8x4<E5>(lo[2], lo[3]));
+  }
+  return w;
+}
+// e2m1(fl32(x / s)) of eight values.
+KVQ_DEVINL uint32_t quant8_e2m1(const float2 (&x)[4], const Divisor& d) {
+  float2 lo[4], hi[4];
+  scale8(x, d.lo, lo);
+  scale8(x, d.hi, hi);
+  uint32_t w = e2m1x8(lo);
+  if (w != e2m1x8(hi) || !d.ok) {
+    divide8(x, d.s, lo);
+    w = e2m1x8(lo);
+  }
+  return w;
 }
 KVQ_DEVINL float amax8(const float2 (&x)[4]) {
   float a = 0.f;
@@ -129,9 +155,7 @@ KVQ_DEVINL uint32_t quant8_fp4(const float2 (&x)[4], float s, const Divisor& six
   block_scale = static_cast<uint8_t>(quant1_e4m3(a, six));
   const float step = __fmul_rn(e4m3_value(block_scale), s);
   if (!(step > 0.f)) return 0;
-  uint32_t w[2];
-  code8<8>(x, Divisor(step), [](float2 v) -> uint32_t { return __nv_cvt_float2_to_fp4x2(v, __NV_E2M1, cudaRoundNearest); }, w);
-  return w[0];
+  return quant8_e2m1(x, Divisor(step));
 }
 
 // 4 x 4 bytes transposed: byte j of word i to byte i of word j.

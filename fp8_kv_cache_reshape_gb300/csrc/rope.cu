@@ -37,10 +37,11 @@ constexpr uint64_t kInvTwoPi = 0xA2F9836E4E441529ull;
 KVQ_DEVINL uint64_t turns_per_position(float inv_freq) {
   const uint32_t u = __float_as_uint(inv_freq);
   const int e = static_cast<int>((u >> 23) & 0xFF);
-  const uint64_t m = e ? (u & 0x7FFFFFu) | 0x800000u : u & 0x7FFFFFu;
+  const uint32_t m = e ? (u & 0x7FFFFFu) | 0x800000u : u & 0x7FFFFFu;
   // inv_freq = m 2^(e - 150) (e = 1 for subnormals), so the fraction is
   // (m kInvTwoPi / 2^24) 2^(e - 128)
-  const uint64_t f = __umul64hi(m << 40, kInvTwoPi);
+  const uint64_t f = (static_cast<uint64_t>(m) * static_cast<uint32_t>(kInvTwoPi >> 32) << 8) +
+                     (static_cast<uint64_t>(m) * static_cast<uint32_t>(kInvTwoPi) >> 24);
   const int shift = (e ? e : 1) - 128;
   const uint64_t x = shift <= -64 ? 0 : shift < 0 ? f >> -shift : shift < 64 ? f << shift : 0;
   return u >> 31 ? 0 - x : x;
@@ -330,6 +331,9 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
     __syncwarp();  // done with the stages of the 16 tokens before
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
+    const int64_t page = slot / kPage * p.Hkv + h0;
+    uint8_t* kp = p.k_cache + page * p.k_str;
+    uint8_t* vp = p.v_cache + page * p.v_str;
     Turn turn;
     if constexpr (TURN) turn = make_turn<D>(p, p.k_weight, row, lane);
     for (int h = h0; h < h1; ++h) {
@@ -345,9 +349,6 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       else
         unpack8_bf16(lds128(at + lane * 16), ko);
       unpack8_bf16(vraw, vo);
-      const int64_t page = slot / kPage * p.Hkv + h;
-      uint8_t* kp = p.k_cache + page * p.k_str;
-      uint8_t* vp = p.v_cache + page * p.v_str;
       if constexpr (F::kFp8) {
         float ks, vs;
         if constexpr (F::kToken) {
@@ -417,6 +418,8 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
         __syncthreads();
         write_v_page<D, FMT>(buf, vp);
       }
+      kp += p.k_str;
+      vp += p.v_str;
     }
     if (page_run) __syncthreads();  // the next 16 tokens start with the first buffer again
   }
