@@ -257,12 +257,16 @@ def kvq_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, k_scale=None, v_
     """Quantize (or copy) new tokens k, v (bf16 [T][Hkv][D]) into the cache."""
     T, Hkv, D = k.shape
     dt = _dtype_code(cache_dtype)
-    num_blocks = _num_blocks(k_cache, v_cache, Hkv, _page_bytes(D, dt))
     if dt == KVQ_DTYPE_FP4_E2M1:
-        for t, name in ((k, "k"), (v, "v")):
-            _check_dense(t, torch.bfloat16, (T, Hkv, D), name)
+        _check_dense(k, torch.bfloat16, (T, Hkv, D), "k")
+        _check_dense(v, torch.bfloat16, (T, Hkv, D), "v")
         _check_dense(slot_mapping, torch.int64, (T,), "slot_mapping")
-        _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, False, num_blocks)
+        num_blocks = _check_dense_cache(k_cache, v_cache, k_scale, v_scale, Hkv, D, dt, False, None)
+        *ptrs, status = _addresses(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, dev_status)
+        _check(lib.kvq_reshape_and_cache(*ptrs, T, Hkv, D, PAGE, num_blocks, dt, status, _stream(stream)),
+               "kvq_reshape_and_cache")
+        return
+    num_blocks = _num_blocks(k_cache, v_cache, Hkv, _page_bytes(D, dt))
     _check(lib.kvq_reshape_and_cache(_ptr(k), _ptr(v), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache),
                                      _ptr(k_scale), _ptr(v_scale), T, Hkv, D, PAGE, num_blocks, dt,
                                      _ptr(dev_status), _stream(stream)), "kvq_reshape_and_cache")
@@ -605,27 +609,34 @@ def kvq_evict_tokens(weights, k_cache, v_cache, block_table, seq_lens, keep_lens
 def _rows(t, T, D, name):
     """Heads and token stride (in elements) of tokens' heads, bf16 [T][heads][D]
     with any stride between tokens."""
-    shape, strides = t.shape, t.stride()
-    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != D:
-        raise ValueError(f"{name} must be bf16 [T][heads][{D}], got {t.dtype} {list(shape)}")
-    if shape[0] != T:
-        raise ValueError(f"{name} must have {T} tokens like the others, got {shape[0]}")
-    heads = shape[1]
-    if strides[2] != 1 or (heads > 1 and strides[1] != D):
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bf16 [T][heads][{D}], got {t.dtype} {list(t.shape)}")
+    tokens, heads, dim = t.shape
+    stride, head_stride, dim_stride = t.stride()
+    if dim != D:
+        raise ValueError(f"{name} must be bf16 [T][heads][{D}], got {t.dtype} {list(t.shape)}")
+    if tokens != T:
+        raise ValueError(f"{name} must have {T} tokens like the others, got {tokens}")
+    if dim_stride != 1 or (heads > 1 and head_stride != D):
         raise ValueError(f"{name}: a token's heads must be contiguous")
-    return heads, strides[0] if T > 1 else heads * D
+    return heads, stride if T > 1 else heads * D
 
 
 def _addresses(*tensors):
     """Addresses of tensors on the current device, whose strides their user has
     checked (None for None)."""
-    current = torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+    current = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    out = []
     for t in tensors:
-        if t is not None and (current < 0 or t.get_device() != current):
-            if t.get_device() < 0:
-                raise ValueError("libkvq takes CUDA tensors only")
+        if t is None:
+            out.append(None)
+        elif t.get_device() == current:
+            out.append(t.data_ptr())
+        elif t.get_device() < 0:
+            raise ValueError("libkvq takes CUDA tensors only")
+        else:
             raise ValueError(f"the tensors' device (cuda:{t.get_device()}) must be the current one (cuda:{current})")
-    return [None if t is None else t.data_ptr() for t in tensors]
+    return out
 
 
 def _check_dense(t, dtype, shape, name):
