@@ -244,6 +244,11 @@ def _is_paired(k_cache, v_cache, kpage):
     return v_cache.data_ptr() == k_cache.data_ptr() + kpage
 
 
+def _is_one_page(k_cache, v_cache, kpage, vpage):
+    """Separate tensors of one page each, which may lie side by side: the same bytes as a pair."""
+    return k_cache.nbytes == kpage and v_cache.nbytes == vpage
+
+
 def _num_blocks(k_cache, v_cache, Hkv, kpage):
     """Blocks of a cache from its K tensor: [num_blocks][Hkv][...] (separate
     or paired), or flat separate pages."""
@@ -276,7 +281,7 @@ def _check_per_token_cache(k_cache, v_cache, Hkv, D):
     kpage, vpage = PAGE * D, PAGE * D + SCALE_TAIL_BYTES
     if _is_paired(k_cache, v_cache, kpage):
         nb = k_cache.shape[0]
-        ok = k_cache.numel() == nb * Hkv * (kpage + vpage)
+        ok = k_cache.numel() == nb * Hkv * (kpage + vpage) or nb * Hkv == 1 and _is_one_page(k_cache, v_cache, kpage, vpage)
     else:
         nb = k_cache.numel() // (Hkv * kpage)
         ok = k_cache.numel() == nb * Hkv * kpage and v_cache.numel() == nb * Hkv * vpage
@@ -467,7 +472,7 @@ def _check_cache(k_cache, v_cache, Hkv, D, dt, per_token, num_blocks):
     vpage = kpage + (SCALE_TAIL_BYTES if per_token else 0)
     nb = k_cache.shape[0]
     if v_cache.data_ptr() == k_cache.data_ptr() + kpage:
-        ok = k_cache.nbytes == nb * Hkv * (kpage + vpage)
+        ok = k_cache.nbytes == nb * Hkv * (kpage + vpage) or nb * Hkv == 1 and _is_one_page(k_cache, v_cache, kpage, vpage)
     else:
         ok = k_cache.nbytes == nb * Hkv * kpage and v_cache.nbytes == nb * Hkv * vpage
     if not ok:

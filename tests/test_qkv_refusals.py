@@ -264,3 +264,18 @@ def test_tensors_of_another_device_are_refused(k, monkeypatch):
             k._addresses(*bad)
     with pytest.raises(ValueError, match="CUDA tensors only"):
         k._addresses(_OnGpu(1), torch.zeros(1))
+
+
+@pytest.mark.parametrize("dt,D,per_token", [(0, 64, False), (0, 64, True), (1, 128, False), (3, 128, False)])
+def test_separate_tensors_of_one_page_may_lie_side_by_side(k, dt, D, per_token):
+    """As an allocator may place them; with more pages the same addresses would be read as pairs."""
+    kpage = k._page_bytes(D, dt)
+    vpage = kpage + (k.SCALE_TAIL_BYTES if per_token else 0)
+    buf = torch.zeros(2 * (kpage + vpage), dtype=torch.uint8)
+    kc, vc = buf[:kpage].view(1, 1, -1), buf[kpage:kpage + vpage].view(1, 1, -1)
+    assert k._check_cache(kc, vc, 1, D, dt, per_token, None) == 1
+    if per_token:
+        assert k._check_per_token_cache(kc, vc, 1, D) == 1
+    two = (buf[:2 * kpage].view(2, 1, -1), buf[kpage:kpage + 2 * vpage].view(2, 1, -1))
+    with pytest.raises(ValueError):
+        k._check_cache(*two, 1, D, dt, per_token, None)
