@@ -24,6 +24,7 @@ struct Format {
   static constexpr bool kFp8 = FMT == kE4M3 || FMT == kE5M2 || FMT == kE4M3Token || FMT == kE5M2Token;
   static constexpr bool kE5 = FMT == kE5M2 || FMT == kE5M2Token;
   static constexpr bool kToken = FMT == kE4M3Token || FMT == kE5M2Token;
+  static constexpr bool kHeadScale = FMT == kE4M3 || FMT == kE5M2 || FMT == kFP4;
   static constexpr float kMax = kE5 ? 57344.f : 448.f;
 };
 
@@ -65,18 +66,24 @@ KVQ_DEVINL uint4 pack8_bf16(const float2 (&x)[4]) {
 // 39.6 us with divisions, 28.6 so.
 struct Divisor {
   float s, lo, hi;
-  bool ok;  // 1 / s is a normal number
+  KVQ_DEVINL Divisor(float divisor, float2 bounds) : s(divisor), lo(bounds.x), hi(bounds.y) {}
   // rcp.approx is off by at most 2^-23, lo and hi by 2^-24 more each and each
   // product by 2^-24: within 2^-22, so 2^-21 to either side encloses
   KVQ_DEVINL explicit Divisor(float divisor) : s(divisor) {
     const uint32_t u = __float_as_uint(s);
-    ok = u - 0x04000000u < 0x7A000000u - 0x04000000u;  // 2^-119 <= s < 2^117
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
     const bool exact = (u & 0x7FFFFFu) == 0;
     if (exact) r = __uint_as_float(0x7F000000u - u);  // 2^-e of 2^e
     lo = exact ? r : r * (1.f - 0x1p-21f);
     hi = exact ? r : r * (1.f + 0x1p-21f);
+    if (u - 0x04000000u >= 0x7A000000u - 0x04000000u) {
+      // not 2^-119 <= s < 2^117: no normal 1 / s.  Products whose codes differ (0 and
+      // NaN of 0, 0 and infinity of others), but for NaN and, in E2M1, where NaN is 6, for
+      // infinity, whose quotients have those codes too
+      lo = 0.f;
+      hi = __uint_as_float(0x7F800000u);
+    }
   }
 };
 // Four values' FP8 codes, eight values' E2M1 codes, nearest even, saturating.
@@ -114,7 +121,7 @@ KVQ_DEVINL uint2 quant8_fp8(const float2 (&x)[4], const Divisor& d) {
   scale8(x, d.lo, lo);
   scale8(x, d.hi, hi);
   uint2 w = make_uint2(fp8x4<E5>(lo[0], lo[1]), fp8x4<E5>(lo[2], lo[3]));
-  if (w.x != fp8x4<E5>(hi[0], hi[1]) || w.y != fp8x4<E5>(hi[2], hi[3]) || !d.ok) {
+  if (w.x != fp8x4<E5>(hi[0], hi[1]) || w.y != fp8x4<E5>(hi[2], hi[3])) {
     divide8(x, d.s, lo);
     w = make_uint2(fp8x4<E5>(lo[0], lo[1]), fp8x4<E5>(lo[2], lo[3]));
   }
@@ -126,17 +133,11 @@ KVQ_DEVINL uint32_t quant8_e2m1(const float2 (&x)[4], const Divisor& d) {
   scale8(x, d.lo, lo);
   scale8(x, d.hi, hi);
   uint32_t w = e2m1x8(lo);
-  if (w != e2m1x8(hi) || !d.ok) {
+  if (w != e2m1x8(hi)) {
     divide8(x, d.s, lo);
     w = e2m1x8(lo);
   }
   return w;
-}
-KVQ_DEVINL float amax8(const float2 (&x)[4]) {
-  float a = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a = fmax3(a, fabsf(x[i].x), fabsf(x[i].y));
-  return a;
 }
 KVQ_DEVINL float e4m3_value(uint8_t code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
@@ -145,13 +146,27 @@ KVQ_DEVINL float e4m3_value(uint8_t code) {
 KVQ_DEVINL uint32_t quant1_e4m3(float x, const Divisor& d) {
   const uint32_t w = __nv_cvt_float2_to_fp8x2(make_float2(x * d.lo, x * d.hi), __NV_SATFINITE, __NV_E4M3);
   const uint32_t lo = w & 0xFF;
-  return lo == w >> 8 && d.ok ? lo : f32_to_e4m3(__fdiv_rn(x, d.s));
+  return lo == w >> 8 ? lo : f32_to_e4m3(__fdiv_rn(x, d.s));
+}
+KVQ_DEVINL float amax8(const float2 (&x)[4]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = fmax3(a, fabsf(x[i].x), fabsf(x[i].y));
+  return a;
+}
+// The same, but NaN where one of them is: E2M1 has no code for it, the block's scale has.
+KVQ_DEVINL float amax8_nan(const float2 (&x)[4]) {
+  float a = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(fabsf(x[i].x)), "f"(fabsf(x[i].y)));
+  return a;
 }
 // The E4M3 scale of a block of 16 dims, of which two neighbouring lanes hold
 // eight each, and their E2M1 codes.  s: the head's scale, six: Divisor(fl32(6 s)).
 KVQ_DEVINL uint32_t quant8_fp4(const float2 (&x)[4], float s, const Divisor& six, uint8_t& block_scale) {
-  float a = amax8(x);
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  float a = amax8_nan(x);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(__shfl_xor_sync(0xffffffffu, a, 1)));
   block_scale = static_cast<uint8_t>(quant1_e4m3(a, six));
   const float step = __fmul_rn(e4m3_value(block_scale), s);
   if (!(step > 0.f)) return 0;

@@ -19,7 +19,7 @@
 // normed and turned along three axes: 58 us, 5.8 TB/s of the measured copy
 // rate of 6.8, the issue slots two thirds full.  4,096 tokens into an E4M3 cache,
 // queries quantized: 20 us, 3.8 TB/s, where the ALU pipe (conversions, selections of bytes) is
-// 55% busy.  A step of 64 tokens: 5.8 us, latency.
+// 55% busy.  A step of 64 tokens: 5.5 us, latency.
 #include <cfloat>
 #include <cmath>
 
@@ -300,6 +300,8 @@ KVQ_DEVINL void write_v_page(const uint8_t* rows, uint8_t* vp) {
   }
 }
 
+constexpr int kMaxKvChunk = 8;  // heads of a cache CTA
+
 // k and v into the cache: a tile's tokens, heads h0 .. h1 - 1.
 // TURN: k is normed or turned.
 template <int D, int FMT, bool TURN>
@@ -309,8 +311,19 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
   constexpr int kStages = Ring<D>::kPairs, kStageB = Ring<D>::kRow;
   __shared__ TileTokens tt;
   __shared__ __align__(16) uint8_t rows[2][kPage * kVStride<D, FMT>];
+  // lo and hi of the divisors of each head's k and v, once instead of in every lane
+  // for every row (32,768 tokens into E4M3: 49.6 us without, 46.7 so)
+  __shared__ float4 bounds[kMaxKvChunk];
   const int lane = threadIdx.x & 31, t = threadIdx.x / LPT, j = threadIdx.x % LPT;
   if (threadIdx.x < 32) find_tokens(tt, p.slots, p.T, p.num_slots, tile, p.aligned, p.dev_status);
+  if constexpr (F::kHeadScale) {
+    const int h = h0 + static_cast<int>(threadIdx.x) - 32;
+    if (h >= h0 && h < h1) {
+      constexpr float f = FMT == kFP4 ? 6.f : 1.f;
+      const Divisor kd(__fmul_rn(f, __ldg(p.k_scale + h))), vd(__fmul_rn(f, __ldg(p.v_scale + h)));
+      bounds[h - h0] = make_float4(kd.lo, kd.hi, vd.lo, vd.hi);
+    }
+  }
   __syncthreads();
   const int n = tt.n;
   for (int r = 0; r < n; r += kPage) {
@@ -350,7 +363,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
         unpack8_bf16(lds128(at + lane * 16), ko);
       unpack8_bf16(vraw, vo);
       if constexpr (F::kFp8) {
-        float ks, vs;
+        uint2 kq, vq;
         if constexpr (F::kToken) {
           float ka = amax8(ko), va = amax8(vo);
 #pragma unroll
@@ -358,18 +371,20 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
             ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
             va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
           }
-          ks = ka > 0.f ? __fdiv_rn(ka, F::kMax) : 1.f;  // an all-zero token keeps scale 1
-          vs = va > 0.f ? __fdiv_rn(va, F::kMax) : 1.f;
+          const float ks = ka > 0.f ? __fdiv_rn(ka, F::kMax) : 1.f;  // an all-zero token keeps scale 1
+          const float vs = va > 0.f ? __fdiv_rn(va, F::kMax) : 1.f;
           if (valid && j == 0) {
             float* tail = reinterpret_cast<float*>(vp + kPage * D);
             tail[off] = ks;
             tail[kPage + off] = vs;
           }
+          kq = quant8_fp8<F::kE5>(ko, Divisor(ks));
+          vq = quant8_fp8<F::kE5>(vo, Divisor(vs));
         } else {
-          ks = __ldg(p.k_scale + h);
-          vs = __ldg(p.v_scale + h);
+          const float4 b = bounds[h - h0];
+          kq = quant8_fp8<F::kE5>(ko, Divisor(__ldg(p.k_scale + h), make_float2(b.x, b.y)));
+          vq = quant8_fp8<F::kE5>(vo, Divisor(__ldg(p.v_scale + h), make_float2(b.z, b.w)));
         }
-        const uint2 kq = quant8_fp8<F::kE5>(ko, Divisor(ks)), vq = quant8_fp8<F::kE5>(vo, Divisor(vs));
         if (valid) {
           *reinterpret_cast<uint2*>(kp + fp8_k_offset(off, j >> 1, D) + (j & 1) * 8) = kq;
           if (page_run) {
@@ -396,8 +411,9 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       } else {
         uint8_t ks, vs;
         const float sk = __ldg(p.k_scale + h), sv = __ldg(p.v_scale + h);
-        const uint32_t kw = quant8_fp4(ko, sk, Divisor(__fmul_rn(6.f, sk)), ks);
-        const uint32_t vw = quant8_fp4(vo, sv, Divisor(__fmul_rn(6.f, sv)), vs);
+        const float4 b = bounds[h - h0];
+        const uint32_t kw = quant8_fp4(ko, sk, Divisor(__fmul_rn(6.f, sk), make_float2(b.x, b.y)), ks);
+        const uint32_t vw = quant8_fp4(vo, sv, Divisor(__fmul_rn(6.f, sv), make_float2(b.z, b.w)), vs);
         if (valid) {
           *reinterpret_cast<uint32_t*>(kp + off * (D / 2) + 4 * j) = kw;
           if (page_run) {
@@ -447,6 +463,8 @@ __global__ void __launch_bounds__(kPage * D / 8, 768 / (2 * D)) token_kernel(con
 // CTA of the cache's rows for each, and two of the queries' (4,096 tokens: 19.9 us;
 // 21.9 with twice as many of the first, 20.3 and 20.5 with half and twice as many of the second;
 // 1,777 tokens of head dim 64: 10.2 us, 12.4 and 12.1 with half and twice the first).
+// Without queries as many of the cache's CTAs as run at once, three to an SM (3,500
+// tokens, 4 bits: 7.4 us with 440 CTAs, 8.5 with 220; 4,096 tokens: 10.8 with 514, 9.2 with 257).
 // Aligned tiles pay from a few hundred tokens in order on (256 tokens of one
 // prompt 7.2 us against 8.2, 1,024: 17.5 against 21.2) and cost steps of many sequences a
 // little (256: 10.8 against 9.5, 1,024: 25.9 against 24.9).
@@ -455,7 +473,7 @@ kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* wh
   p.tiles = (p.T - 1) / kPage + 1;
   p.aligned = FMT != kRowsOnly && p.T >= 256;
   p.kv_tiles = p.tiles + (p.aligned ? 1 : 0);
-  p.kv_chunk = heads_per_cta(p.Hkv, p.kv_tiles, 8, 128 * sm_count() / D);
+  p.kv_chunk = heads_per_cta(p.Hkv, p.kv_tiles, kMaxKvChunk, p.Hq ? 128 * sm_count() / D : 192 * sm_count() / D + 1);
   p.q_chunk = heads_per_cta(p.Hq, p.tiles, 32, 2 * sm_count());
   const int64_t kv_ctas = static_cast<int64_t>(p.kv_tiles) * ((p.Hkv + static_cast<int64_t>(p.kv_chunk) - 1) / p.kv_chunk);
   const int64_t ctas = kv_ctas + static_cast<int64_t>(p.tiles) * ((p.Hq + static_cast<int64_t>(p.q_chunk) - 1) / p.q_chunk);

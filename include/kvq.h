@@ -184,7 +184,8 @@ const char* kvq_last_error_string(void);
  *  num_blocks >= 1.  For BF16 the values are copied bit for bit.  FP4: per
  *  token and block of 16 dims, b = e4m3(fl32(max |x| / fl32(6 s))), saturating,
  *  and code = e2m1(fl32(x / fl32(b s))), nearest even, saturating to +-6 (codes
- *  0 where b rounds to 0); the value held is code * b * s.  FP8:
+ *  0 where b rounds to 0; a NaN makes its block's b NaN); the value held is
+ *  code * b * s.  FP8:
  *  code = encode(fl32(x / s[h])), one float32 division, then one
  *  round-to-nearest-even conversion saturating at the format's largest
  *  finite value (448 for E4M3, 57344 for E5M2).

@@ -64,6 +64,30 @@ def test_window(window, dim):
     assert_within(out, ref, tol)
 
 
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("lengths", [[1, 40], [9000, 333]])
+def test_a_nan_block_shows_and_stays_where_it_is(lengths, dim):
+    """What the write makes of a NaN: its key's scores, and so the head's outputs, and its value's 16 dims."""
+    heads, group = 2, 3
+    pool = Pool4(sum(-(-n // P) for n in lengths) + 3, heads, dim, 5)
+    table = pool.table(lengths)
+    qd, q = pool.query(2, group)
+    sm = 1 / np.sqrt(dim)
+    ref, tol = pool.attend(q, table, lengths, sm)
+    last = lengths[0] - 1
+    pool.ks[table[0, last // P], 0, last % P, 1] = 0x7F
+    pool.vs[table[0, 0], 1, 0, 2] = 0x7F
+    args = (qd, *pool.device(), *pool.scales(), i32(table), i32(lengths))
+    out, st = _run(args, dict(sm_scale=sm, window=-1))
+    assert st == 0
+    odd = torch.zeros(out.shape, dtype=torch.bool)
+    odd[0, :group] = True
+    odd[0, group:, 32:48] = True
+    assert torch.equal(out.isnan().cpu(), odd)
+    ref[odd.numpy()] = 0
+    assert_within(out.nan_to_num(0.0), ref, tol)
+
+
 def test_more_sequences_than_threads_of_a_cta():
     """Most of them empty, the rest at both ends."""
     lengths = [0] * 300

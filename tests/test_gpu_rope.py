@@ -373,6 +373,35 @@ def test_quotients_are_those_of_a_division(scale):
         assert np.array_equal(got[at, :, off], ref)
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.011, 2.0 ** -126, 1e-44, 3e38])
+def test_quotients_of_infinities_nan_and_zeros(scale):
+    """The bytes of the plain write, whose values are divided; 4 bits: the oracle's."""
+    k = _k()
+    x = torch.zeros(16, 1, 64, dtype=torch.bfloat16)
+    odd = torch.tensor([float("inf"), float("-inf"), 0.0, -0.0, 1.0, -2.5, 3e38, 1e-38])
+    for t in range(16):
+        x[t, 0] = odd.repeat(8).roll(t).bfloat16()
+    x[12, 0, :8] = float("inf")
+    x[13, 0, :8] = -0.0
+    slots = torch.arange(16).cuda()
+    s = torch.full((1,), scale, device="cuda")
+    x[14, 0, ::3] = float("nan")
+    x[15, 0, :8] = float("nan")
+    kd, vd = k.alloc_kv_cache(1, 1, 64, "fp4", fill=0)
+    k.kvq_reshape_and_cache(x.cuda(), x.cuda(), slots, kd, vd, s, s, cache_dtype="fp4")
+    with np.errstate(all="ignore"):
+        want = e2m1.quantize(x.float().numpy(), np.float32(scale))
+    codes, sb, vc, vsb = e2m1.from_pages(kd.cpu().numpy(), vd.cpu().numpy(), 64)
+    for got, ref in ((codes, want[0]), (sb, want[1]), (vc, want[0]), (vsb, want[1])):
+        assert np.array_equal(got[0].transpose(1, 0, 2), ref)
+    x = x.cuda()
+    for name in ("fp8_e4m3", "fp8_e5m2"):
+        a, b = (k.alloc_kv_cache(1, 1, 64, name, fill=0) for _ in range(2))
+        k.kvq_rope_and_cache(None, x, x, None, None, slots, *a, s, s, cache_dtype=name)
+        k.kvq_reshape_and_cache(x, x, slots, *b, s, s, cache_dtype=name)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
 def test_fp4_write_against_the_oracle():
     """kvq_reshape_and_cache: every byte, zero blocks and saturation among them."""
     k = _k()
