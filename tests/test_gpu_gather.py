@@ -204,3 +204,24 @@ def test_a_layer_step_over_a_4_bit_cache(dim, group, axes, captured):
         for got, ref in ((ko, kh), (vo, vh)):
             top = np.abs(ref.reshape(n + steps, H, -1, 16)).max(-1).repeat(16, -1)
             assert np.all(np.abs(got.double().cpu().numpy() - ref) <= (1 / 6 + 2.0 ** -4) * (1 + 2.0 ** -4) * top + 2.0 ** -7 * top)
+
+
+@pytest.mark.parametrize("fmt", ["fp8_e4m3", "fp8_e5m2", "bf16", "fp4"])
+def test_nan_comes_back_as_nan(fmt):
+    """Of 4 bits the whole block of 16 dims, of the others the value."""
+    k = _k()
+    x = torch.ones(20, 2, 128, dtype=torch.bfloat16)
+    x[3, 1, 37] = x[19, 0, 127] = float("nan")
+    x = x.cuda()
+    slots = torch.arange(7, 27).cuda()
+    s = None if fmt == "bf16" else torch.ones(2, device="cuda")
+    kc, vc = k.alloc_kv_cache(2, 2, 128, fmt, fill=0)
+    k.kvq_reshape_and_cache(x, x, slots, kc, vc, s, s, cache_dtype=fmt)
+    ko, vo = torch.empty_like(x), torch.empty_like(x)
+    k.kvq_gather_cache(slots, kc, vc, ko, vo, s, s, cache_dtype=fmt)
+    want, one = x.isnan(), 1.0
+    if fmt == "fp4":
+        one = 33 / 32  # the block scale is 1/6 in E4M3: 11/64; 64/11 is 6 in E2M1
+        want = want.unflatten(-1, (-1, 16)).any(-1, keepdim=True).expand(-1, -1, -1, 16).flatten(-2)
+    for y in (ko, vo):
+        assert torch.equal(y.isnan(), want) and bool((y[~want] == one).all())
