@@ -171,19 +171,57 @@ KVQ_DEVINL Turn make_turn(const TokenParams& p, const __nv_bfloat16* weight, int
   return t;
 }
 
-// Norm and rotation of a lane's eight dims, `other` those of lane t.from; every
-// lane of the warp takes part.
+// The norm's factor of a row for turn_row, where float32 has not the plain way's
+// squares or products: x and y scaled by it on return.  The row's maximum is brought to
+// [1, 2), as a power of two, but eps with it no further than 2^100, where it outweighs
+// the rest.  Every lane of the warp takes part.
 template <int D>
-KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, const uint4& other, float2 (&o)[4]) {
+KVQ_DEVINL void norm_scaled(float eps, float2 (&x)[4], float2 (&y)[4]) {
   constexpr int LPT = D / 8;
+  float top = amax8(x);
+#pragma unroll
+  for (int off = 1; off < LPT; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  int k = 127 - static_cast<int>(__float_as_uint(top) >> 23);
+  if (eps > 0.f) k = min(k, (227 - static_cast<int>(__float_as_uint(eps) >> 23)) >> 1);
+  // 2^k in two steps: -128 to 127 is beyond one float32 factor
+  const float f = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
+  const float g = __uint_as_float(static_cast<uint32_t>(127 + k - (k >> 1)) << 23);
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = fmul2(fmul2(x[i], make_float2(f, f)), make_float2(g, g));
+    y[i] = fmul2(fmul2(y[i], make_float2(f, f)), make_float2(g, g));
+    sum = ffma2(x[i], x[i], sum);
+  }
+  float all = sum.x + sum.y;
+#pragma unroll
+  for (int off = 1; off < LPT; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
+  const float r = rsqrtf(fmaf(all, 1.f / D, eps * f * f * g * g));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = fmul2(x[i], make_float2(r, r));
+    y[i] = fmul2(y[i], make_float2(r, r));
+  }
+}
+
+// A lane's eight dims x and their pairs' others y, from the warp's stage.
+KVQ_DEVINL void load_row(const Turn& t, uint32_t stage, int lane, float2 (&x)[4], float2 (&y)[4]) {
+  const uint4 raw = lds128(stage + lane * 16), other = lds128(stage + t.from * 16);
   const uint32_t w[4] = {other.x, other.y, other.z, other.w};
-  float2 x[4], y[4];
   unpack8_bf16(raw, x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t u = w[i];
     y[i] = make_float2(__uint_as_float(__byte_perm(u, 0, t.px)), __uint_as_float(__byte_perm(u, 0, t.py)));
   }
+}
+
+// Norm and rotation of a lane's eight dims; every lane of the warp takes part.
+template <int D>
+KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, uint32_t stage, int lane, float2 (&o)[4]) {
+  constexpr int LPT = D / 8;
+  float2 x[4], y[4];
+  load_row(t, stage, lane, x, y);
 #pragma unroll
   for (int i = 0; i < 4; ++i) o[i] = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
   if (norm) {
@@ -193,9 +231,23 @@ KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, 
     float all = sum.x + sum.y;
 #pragma unroll
     for (int off = 1; off < LPT; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    const float r = rsqrtf(fmaf(all, 1.f / D, eps));
+    const float mean = fmaf(all, 1.f / D, eps), r = rsqrtf(mean);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = fmul2(o[i], make_float2(r, r));
+    // Squares that float32 has not, or products before r that it has not or not in full:
+    // from a mean of 2^-40 on, what a subnormal product loses is below 2^-129 of the result.
+    // Only such values take the other result; a warp without any pays for the comparisons
+    // and a vote (16,383 tokens: 58.0 us without them, 58.9 so).
+    const bool plain = mean >= 0x1p-40f && mean <= 0x1p100f && amax8_nan(o) <= FLT_MAX;
+    if (__any_sync(0xffffffffu, !plain)) {
+      load_row(t, stage, lane, x, y);  // again: holding them spills
+      norm_scaled<D>(eps, x, y);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 u = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
+        if (!plain) o[i] = u;
+      }
+    }
   }
 }
 
@@ -240,7 +292,7 @@ KVQ_DEVINL void turn_rows(const TokenParams& p, uint32_t ring, bool is_q, int ti
     issue(i + kStages - 1);
     const uint32_t at = ring + i % kStages * kStageB;
     float2 o[4];
-    turn_row<D>(turn, weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), o);
+    turn_row<D>(turn, weight != nullptr, p.eps, at, lane, o);
     if (!live) continue;
     if (dst) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(o);
     if (codes) *reinterpret_cast<uint2*>(codes + i * D) = quant8_fp8<false>(o, s);
@@ -358,7 +410,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       const uint4 vraw = lds128(at + kStageB + lane * 16);
       float2 ko[4], vo[4];
       if constexpr (TURN)
-        turn_row<D>(turn, p.k_weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), ko);
+        turn_row<D>(turn, p.k_weight != nullptr, p.eps, at, lane, ko);
       else
         unpack8_bf16(lds128(at + lane * 16), ko);
       unpack8_bf16(vraw, vo);

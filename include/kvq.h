@@ -592,8 +592,9 @@ typedef struct kvq_rotary {
 
 /*
  * Root-mean-square norm of each query and key head, before the rotation:
- * x_d -> x_d / sqrt(sum x^2 / D + eps) * w_d.  q_weight, k_weight: bf16 [D]
- * (either may be NULL: those heads are not normed); eps >= 0, finite.
+ * x_d -> x_d / sqrt(sum x^2 / D + eps) * w_d, also where float32 holds no sum
+ * of the squares.  q_weight, k_weight: bf16 [D] (either may be NULL: those
+ * heads are not normed); eps >= 0, finite; with eps 0 a head of zeros is NaN.
  */
 typedef struct kvq_head_norm {
   const void* q_weight;
