@@ -493,8 +493,10 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
   }
 }
 
+// Three CTAs of 256 threads an SM (80 registers) where there is a cache to write, four (64)
+// for rows alone (16,383 tokens: 58.8 us, with three 61.3).
 template <int D, int FMT, bool TURN = true>
-__global__ void __launch_bounds__(kPage * D / 8, 768 / (2 * D)) token_kernel(const TokenParams p) {
+__global__ void __launch_bounds__(kPage * D / 8, (FMT == kRowsOnly ? 1024 : 768) / (2 * D)) token_kernel(const TokenParams p) {
   __shared__ __align__(16) uint8_t ring_mem[D / 16 * Ring<D>::kBytes];
   const uint32_t ring = smem_u32(ring_mem) + threadIdx.x / 32 * Ring<D>::kBytes;
   if (blockIdx.x >= p.kv_ctas) {
