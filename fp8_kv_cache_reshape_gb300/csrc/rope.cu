@@ -49,12 +49,15 @@ KVQ_DEVINL uint64_t turns_per_position(float inv_freq) {
 
 // Sine and cosine of a fraction of a turn: to the nearest quarter, then the
 // Taylor series of the rest, y up to pi / 4 either way.  The first terms left
-// out are y^11 / 11! < 2^-29 and y^12 / 12! < 2^-32; y is rounded twice, 2^-23.
+// out are y^11 / 11! < 2^-29 and y^12 / 12! < 2^-32; y is rounded three times, 2^-22
+// of it however small it is: the rest keeps all of its bits, in two signed halves.
 KVQ_DEVINL void sincos_turns(uint64_t turns, float& s, float& c) {
-  const uint32_t t = static_cast<uint32_t>(turns >> 32);
+  const uint32_t t = static_cast<uint32_t>((turns + 0x80000000u) >> 32);
+  const int low = static_cast<int>(static_cast<uint32_t>(turns));
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const int rest = static_cast<int>(t - (quarter << 30));  // within an eighth of a turn
-  const float y = static_cast<float>(rest) * (6.283185307f * 0x1p-32f), z = y * y;
+  const float turn = 6.283185307f;
+  const float y = fmaf(static_cast<float>(rest), turn * 0x1p-32f, static_cast<float>(low) * (turn * 0x1p-64f)), z = y * y;
   float s0 = fmaf(z, 1.f / 362880, -1.f / 5040), c0 = fmaf(z, -1.f / 3628800, 1.f / 40320);
   s0 = fmaf(z, s0, 1.f / 120);
   s0 = fmaf(z, s0, -1.f / 6);
