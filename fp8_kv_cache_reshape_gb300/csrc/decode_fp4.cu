@@ -45,7 +45,9 @@ constexpr int kMinPart = 2;           // pages of a part, at least: a pair
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
-constexpr float kNone = -1e30f;
+// The stabilizer before the first score: any score passes it, by an amount whose product
+// with a coefficient of kLeast or more passes kLag.
+constexpr float kNone = -FLT_MAX;
 // Sums of code products are below 2^27, so a smaller coefficient gives scores of zero
 // either way; one of zero would make a masked score, minus infinity, no number.
 constexpr float kLeast = 1e-30f;
@@ -205,7 +207,7 @@ struct Attend {
   using F = Fp4<D>;
   uint32_t q[D / 8];  // query r, dims (D / 4) c .. + D / 4 - 1
   float coef[2], vs;
-  float m[2], mb[2], l[2];  // mb: m - kBase, or kNone, which any score passes
+  float m[2], l[2];  // the stabilizer is m * coef: differences of scores are taken before the product, which rounds them
   float O[F::kTiles][4];
   uint32_t p[2][2];  // weights of the stage whose outputs are due
 
@@ -251,8 +253,7 @@ struct Attend {
     for (int i = 0; i < 2; ++i) {
       coef[i] = cf * __shfl_sync(0xffffffffu, inv_sigma, 8 * c + 4 * i);
       if (coef[i] < kLeast) coef[i] = kLeast;
-      m[i] = NEG_INF;
-      mb[i] = kNone;
+      m[i] = kNone;
       l[i] = 0.f;
     }
 #pragma unroll
@@ -260,6 +261,8 @@ struct Attend {
 #pragma unroll
       for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
   }
+
+  KVQ_DEVINL float stabilizer(int i) const { return m[i] == kNone ? NEG_INF : m[i] * coef[i]; }
 
   // The piece's output, normalized: to the output where it is all of the sequence
   // and KV head, else to the workspace with its log-sum-exp.
@@ -285,7 +288,7 @@ struct Attend {
 #pragma unroll
         for (int d = 0; d < F::kTiles; ++d)
           *reinterpret_cast<float2*>(out + 16 * d) = make_float2(any ? O[d][i] * f : 0.f, any ? O[d][2 + i] * f : 0.f);
-        if (r == 0) prm.lse_part[id * prm.g + qh] = any ? m[i] + log2f(sum) : NEG_INF;
+        if (r == 0) prm.lse_part[id * prm.g + qh] = any ? stabilizer(i) + log2f(sum) : NEG_INF;
       }
     }
   }
@@ -299,7 +302,7 @@ struct Attend {
 #pragma unroll
       for (int k = 4; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
       if (r == 0) {
-        sm[2 * c + i] = m[i];
+        sm[2 * c + i] = stabilizer(i);
         sl[2 * c + i] = sum;
       }
 #pragma unroll
@@ -429,19 +432,27 @@ struct Attend {
     if (at < 2) sts128(half + lane * 16, hs);
     // stabilizer: moved only when a score passes it by more than kLag
     float x[2][4];
+    auto exponents = [&] {
+      const float2 minus = make_float2(-m[0], -m[1]), by = make_float2(coef[0], coef[1]), base = make_float2(kBase, kBase);
 #pragma unroll
-    for (int pg = 0; pg < 2; ++pg)
+      for (int pg = 0; pg < 2; ++pg)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+        for (int e = 0; e < 4; e += 2) {
+          const float2 y = ffma2(fadd2(make_float2(t[pg][e], t[pg][e + 1]), minus), by, base);
+          x[pg][e] = y.x;
+          x[pg][e + 1] = y.y;
+        }
+    };
+    exponents();
     const float top = fmax3(fmax3(x[0][0], x[0][2], fmaxf(x[1][0], x[1][2])), x[0][1], fmax3(x[0][3], x[1][1], x[1][3]));
     if (__any_sync(0xffffffffu, top > kLag + kBase)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i])) * coef[i];
+        float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i]));
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) n = fmaxf(n, __shfl_xor_sync(0xffffffffu, n, o));
         if (n > m[i]) {  // the same in every lane of the query
-          const float alpha = ex2(m[i] - n);
+          const float alpha = ex2((m[i] - n) * coef[i]);
           l[i] *= alpha;
 #pragma unroll
           for (int d = 0; d < F::kTiles; ++d) {
@@ -449,13 +460,9 @@ struct Attend {
             O[d][2 + i] *= alpha;
           }
           m[i] = n;
-          mb[i] = n - kBase;
         }
       }
-#pragma unroll
-      for (int pg = 0; pg < 2; ++pg)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[pg][e] = fmaf(t[pg][e], coef[e & 1], -mb[e & 1]);
+      exponents();
     }
 #pragma unroll
     for (int pg = 0; pg < 2; ++pg) {

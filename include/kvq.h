@@ -693,9 +693,9 @@ kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, 
  *  function of the lengths alone: results are deterministic.
  *  Declared rounding: the query enters as f16(fl32(q * sigma)) as for
  *  kvq_paged_decode_attention; K enters as code * block scale, exact in float16; scores
- *  are FP32 sums times fl32(fl32(k_scale * sm_scale) * log2(e)) / sigma;
- *  probabilities 2^(s2 - M + 4), M a running maximum that may lag by up to 3,
- *  are rounded to float16, multiplied by V's block scale with another
+ *  are FP32 sums t times c = fl32(fl32(k_scale * sm_scale) * log2(e)) / sigma;
+ *  probabilities 2^((t - M) c + 4), M a running maximum that may lag by up to
+ *  3 / c, are rounded to float16, multiplied by V's block scale with another
  *  rounding to float16 (each half a step of 2^-10; below 2^-14 steps of 2^-24),
  *  and contracted with V's codes, exact in float16, in FP32 per page
  *  of 16 tokens, then added into a running FP32 sum; the row sum adds them
