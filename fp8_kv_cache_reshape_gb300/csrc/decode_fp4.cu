@@ -44,7 +44,11 @@ constexpr int kCtasPerSm = 3;         // 168 registers a thread (four, with 128 
 constexpr int kMinPart = 2;           // pages of a part, at least: a pair
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
-constexpr float kBase = 4.f;          // weights are 2^(s2 - M + kBase) <= 2^7: times 448 within float16
+// Weights are 2^(s2 - M + base): below 2^16 / 2 ^ (exponent of V's largest block scale), so
+// that their products with block scales stay within float16, and as large as that allows,
+// so that they stay out of its subnormal numbers: 12 for scales below 2, 4 for those from 256 on.
+constexpr float kBase = 12.f;
+constexpr int kUnit = 7;  // exponent field of scales in [1, 2)
 // The stabilizer before the first score: any score passes it, by an amount whose product
 // with a coefficient of kLeast or more passes kLag.
 constexpr float kNone = -FLT_MAX;
@@ -209,6 +213,8 @@ struct Attend {
   float coef[2], vs;
   float m[2], l[2];  // the stabilizer is m * coef: differences of scores are taken before the product, which rounds them
   float O[F::kTiles][4];
+  float base;
+  uint32_t room;     // four bytes, each from the first code that base has no room for to its sign bit
   uint32_t p[2][2];  // weights of the stage whose outputs are due
 
   // The queries as they are, and (begin) as the products take them.
@@ -260,6 +266,18 @@ struct Attend {
     for (int i = 0; i < F::kTiles; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) O[i][e] = 0.f;
+    base = kBase;
+    room = (0x78 - 8 * kUnit) * 0x01010101u;
+  }
+
+  // All sums times f.
+  KVQ_DEVINL void scale_sums(float f) {
+    l[0] *= f;
+    l[1] *= f;
+#pragma unroll
+    for (int d = 0; d < F::kTiles; ++d)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[d][e] *= f;
   }
 
   KVQ_DEVINL float stabilizer(int i) const { return m[i] == kNone ? NEG_INF : m[i] * coef[i]; }
@@ -288,7 +306,7 @@ struct Attend {
 #pragma unroll
         for (int d = 0; d < F::kTiles; ++d)
           *reinterpret_cast<float2*>(out + 16 * d) = make_float2(any ? O[d][i] * f : 0.f, any ? O[d][2 + i] * f : 0.f);
-        if (r == 0) prm.lse_part[id * prm.g + qh] = any ? stabilizer(i) + log2f(sum) : NEG_INF;
+        if (r == 0) prm.lse_part[id * prm.g + qh] = any ? stabilizer(i) + (log2f(sum) - base) : NEG_INF;
       }
     }
   }
@@ -296,6 +314,7 @@ struct Attend {
   // The state to shared memory, for the CTA's warps to join.
   KVQ_DEVINL void show(float* o, float* sm, float* sl, int lane) {
     const int r = lane >> 2, c = lane & 3;
+    scale_sums(ex2(-base));  // the warps' may differ
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       float sum = l[i];
@@ -430,22 +449,33 @@ struct Attend {
     e4m3x4_to_f16x2x2(w.x, hs.x, hs.y);
     e4m3x4_to_f16x2x2(w.y, hs.z, hs.w);
     if (at < 2) sts128(half + lane * 16, hs);
+    constexpr uint32_t kSign = 0x80808080u;
+    const bool larger = (((w.x & ~kSign) + room) | ((w.y & ~kSign) + room)) & kSign;
     // stabilizer: moved only when a score passes it by more than kLag
     float x[2][4];
     auto exponents = [&] {
-      const float2 minus = make_float2(-m[0], -m[1]), by = make_float2(coef[0], coef[1]), base = make_float2(kBase, kBase);
+      const float2 minus = make_float2(-m[0], -m[1]), by = make_float2(coef[0], coef[1]), plus = make_float2(base, base);
 #pragma unroll
       for (int pg = 0; pg < 2; ++pg)
 #pragma unroll
         for (int e = 0; e < 4; e += 2) {
-          const float2 y = ffma2(fadd2(make_float2(t[pg][e], t[pg][e + 1]), minus), by, base);
+          const float2 y = ffma2(fadd2(make_float2(t[pg][e], t[pg][e + 1]), minus), by, plus);
           x[pg][e] = y.x;
           x[pg][e + 1] = y.y;
         }
     };
     exponents();
     const float top = fmax3(fmax3(x[0][0], x[0][2], fmaxf(x[1][0], x[1][2])), x[0][1], fmax3(x[0][3], x[1][1], x[1][3]));
-    if (__any_sync(0xffffffffu, top > kLag + kBase)) {
+    if (__any_sync(0xffffffffu, top > kLag + base || larger)) {
+      const uint32_t most = __vmaxu4(w.x & ~kSign, w.y & ~kSign);
+      const uint32_t byte = max(max(most & 0xFF, most >> 8 & 0xFF), max(most >> 16 & 0xFF, most >> 24));
+      const int unit = static_cast<int>(__reduce_max_sync(0xffffffffu, byte) >> 3);
+      const float lower = kBase + static_cast<float>(kUnit - unit);
+      if (lower < base) {
+        scale_sums(ex2(lower - base));
+        base = lower;
+        room = (0x78 - 8 * unit) * 0x01010101u;
+      }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float n = fmaxf(fmaxf(t[0][i], t[0][2 + i]), fmaxf(t[1][i], t[1][2 + i]));

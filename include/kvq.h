@@ -694,9 +694,11 @@ kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, 
  *  Declared rounding: the query enters as f16(fl32(q * sigma)) as for
  *  kvq_paged_decode_attention; K enters as code * block scale, exact in float16; scores
  *  are FP32 sums t times c = fl32(fl32(k_scale * sm_scale) * log2(e)) / sigma;
- *  probabilities 2^((t - M) c + 4), M a running maximum that may lag by up to
- *  3 / c, are rounded to float16, multiplied by V's block scale with another
- *  rounding to float16 (each half a step of 2^-10; below 2^-14 steps of 2^-24),
+ *  probabilities 2^((t - M) c + b), M a running maximum that may lag by up to
+ *  3 / c and b 12 while V's block scales are below 2 and as much lower as their
+ *  largest exponent so far is above 0, are rounded to float16, multiplied by V's
+ *  block scale with another rounding to float16 (each half a step of 2^-10;
+ *  below 2^-14 steps of 2^-24),
  *  and contracted with V's codes, exact in float16, in FP32 per page
  *  of 16 tokens, then added into a running FP32 sum; the row sum adds them
  *  unrounded.  The output is rounded to bf16 once, at the end.

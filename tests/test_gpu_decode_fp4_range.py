@@ -1,4 +1,5 @@
-"""The 4-bit decode where scores are large."""
+"""The 4-bit decode where the block scales of V are far below or far apart from
+one another, and where scores are large."""
 import numpy as np
 import pytest
 import torch
@@ -43,6 +44,46 @@ def _expected(pool, row, n, q, sm):
         tol[rows] = 2.0 ** -8 * np.abs(out[rows]) + (2 * 2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -133
         tol[rows] += 2.0 ** (-25 - 12 + field - 7) * (np.abs(v).sum(0) + n * 6 * float(pool.v_scale[h]))
     return out, tol
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [0.01, 0.05, 1.0, 300.0])
+def test_a_first_token_that_draws_most_and_a_long_flat_tail(size, dim):
+    """Head scales of 1, so that block scales are those of the data: subnormal ones at 0.01.  The first token has
+    no part in every other dim, whose output is the tail's.  The sequences share their pages, as many as it takes for
+    pieces of thousands of tokens."""
+    n, heads, batch = 16_003, 2, 512
+    pool, table = _pool(n, heads, dim, 1.0, 1.0)
+    rng = np.random.default_rng(1)
+    k, v = np.zeros((n, heads, dim), np.float32), np.empty((n, heads, dim), np.float32)
+    k[0, :, 0] = 10.0  # 14.4 in base 2 above the others
+    v[:] = size * np.where(np.arange(dim) % 4 < 2, 1, -1) * rng.uniform(0.7, 1.0, (n, heads, dim))
+    v[0, :, ::2] = 0
+    _write(pool, table[0], k, v)
+    q = torch.zeros(1, 4 * heads, dim, dtype=torch.bfloat16)
+    q[0, :, 0] = torch.tensor([1.0, 0.95, 0.9, 0.8] * heads)
+    ref, tol = _expected(pool, table[0], n, q[0].double().numpy(), 1.0)
+    args = (q.expand(batch, -1, -1).contiguous().cuda(), *pool.device(), *pool.scales(), i32(np.repeat(table, batch, 0)), i32([n] * batch))
+    out, st = _run(args, dict(sm_scale=1.0))
+    assert st == 0
+    assert_within(out, ref[None], tol[None])
+
+
+@pytest.mark.parametrize("dim,heads,batch,n", [(64, 2, 64, 4001), (128, 1, 60, 4099), (128, 1, 1, 62_005), (64, 1, 1, 1500), (64, 8, 300, 45)])
+@pytest.mark.parametrize("first,last", [(1e-3, 2000.0), (2000.0, 1e-3), (5e-3, 5e-3)])
+def test_block_scales_that_grow_and_shrink(dim, heads, batch, n, first, last):
+    """Parts of several stages, pieces of one, CTAs that join theirs: the sequences share their pages."""
+    pool, table = _pool(n, heads, dim, 0.7, 1.0, seed=3)
+    rng = np.random.default_rng(4)
+    size = np.exp(np.linspace(np.log(first), np.log(last), n))[:, None, None]
+    _write(pool, table[0], rng.standard_normal((n, heads, dim)).astype(np.float32),
+           (size * rng.standard_normal((n, heads, dim))).astype(np.float32))
+    q = torch.from_numpy(rng.standard_normal((1, heads * 3, dim))).bfloat16()
+    ref, tol = _expected(pool, table[0], n, q[0].double().numpy(), dim ** -0.5)
+    args = (q.expand(batch, -1, -1).contiguous().cuda(), *pool.device(), *pool.scales(), i32(np.repeat(table, batch, 0)), i32([n] * batch))
+    out, st = _run(args, {})
+    assert st == 0
+    assert_within(out, ref[None], tol[None])
 
 
 @pytest.mark.parametrize("score", [1e7, -1e7, 1e9, -1e9, 1e20, -1e31])
