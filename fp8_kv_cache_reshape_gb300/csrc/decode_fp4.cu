@@ -283,7 +283,8 @@ struct Attend {
   KVQ_DEVINL float stabilizer(int i) const { return m[i] == kNone ? NEG_INF : m[i] * coef[i]; }
 
   // The piece's output, normalized: to the output where it is all of the sequence
-  // and KV head, else to the workspace with its log-sum-exp.
+  // and KV head, else to the workspace with its log-sum-exp, and without V's head scale: the
+  // sum of partials has the values' range then, however large or small that is.
   KVQ_DEVINL void finish(const Fp4Params& prm, int index, const Meta& meta, int lane) {
     const int r = lane >> 2, c = lane & 3;
     const int64_t id = index + static_cast<int64_t>(meta.b) * prm.Hkv + meta.h;
@@ -293,14 +294,16 @@ struct Attend {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       const bool any = sum > 0.f || sum != sum;
-      const float f = any ? vs / sum : 0.f;
+      const float f = any ? 1.f / sum : 0.f;
       const int qh = 2 * c + i;
       if (qh >= prm.g) continue;
       if (meta.flags & kWhole) {
         __nv_bfloat16* out = prm.out + (static_cast<int64_t>(meta.b) * prm.Hq + meta.h * prm.g + qh) * D + 2 * r;
 #pragma unroll
-        for (int d = 0; d < F::kTiles; ++d)
-          *reinterpret_cast<uint32_t*>(out + 16 * d) = pack_bf16x2(any ? O[d][i] * f : 0.f, any ? O[d][2 + i] * f : 0.f);
+        for (int d = 0; d < F::kTiles; ++d) {
+          const float2 y = fmul2(fmul2(make_float2(O[d][i], O[d][2 + i]), make_float2(f, f)), make_float2(vs, vs));
+          *reinterpret_cast<uint32_t*>(out + 16 * d) = any ? pack_bf16x2(y.x, y.y) : 0;
+        }
       } else {
         float* out = prm.o_part + (id * prm.g + qh) * D + 2 * r;
 #pragma unroll
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
         o = ffma2(ow[w], make_float2(f, f), o);
       }
       const bool any = l > 0.f || l != l;
-      const float f = any ? at.vs / l : 0.f;
+      const float f = any ? 1.f / l : 0.f;
       *reinterpret_cast<float2*>(p.o_part + (id * p.g + qh) * D + d) = any ? make_float2(o.x * f, o.y * f) : make_float2(0.f, 0.f);
       if (d == 0) p.lse_part[id * p.g + qh] = any ? M + log2f(l) : NEG_INF;
     }
@@ -757,6 +760,7 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
   const int x = before * p.Hkv + h * n;
   const int first = x / chunk, last = (x + n - 1) / chunk;
   if (first == last) return;  // written where it was computed
+  const float vs = p.v_scale[h];
   // CTAs kWarps * [c0, c1) of parts wrote one row each, the parts before and behind
   // them their own
   const int all = total * p.Hkv, cta = kWarps * chunk;
@@ -819,7 +823,7 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
       sum = fmaf(s_l[w], f, sum);
       y = fmaf(s_o[w][d], f, y);
     }
-    out[d] = __float2bfloat16(sum > 0.f || sum != sum ? y / sum : 0.f);
+    out[d] = __float2bfloat16(sum > 0.f || sum != sum ? y / sum * vs : 0.f);
   }
 }
 

@@ -1,5 +1,5 @@
-"""The 4-bit decode where the block scales of V are far below or far apart from
-one another, and where scores are large."""
+"""The 4-bit decode where the scales of V are far below or far apart from one
+another, and where scores are large."""
 import numpy as np
 import pytest
 import torch
@@ -100,5 +100,20 @@ def test_large_scores_that_are_equal(score, n):
     q[0, :, 0] = score / 1000
     ref, tol = _expected(pool, table[0], n, q[0].double().numpy(), 1.0)
     out, st = _run((q.cuda(), *pool.device(), *pool.scales(), i32(table), i32([n])), dict(sm_scale=1.0))
+    assert st == 0
+    assert_within(out[0], ref, tol)
+
+
+@pytest.mark.parametrize("scale", [1e-37, 1e-33, 1e-20, 1e20, 1e34, 1.2e35])
+@pytest.mark.parametrize("n,dim", [(20, 64), (40_000, 128)])
+def test_head_scales_of_any_size(scale, n, dim):
+    """One piece, and many that are joined: values of 500 head scales, up to 2,688."""
+    pool, table = _pool(n, 1, dim, 0.01, scale, seed=9)
+    rng = np.random.default_rng(10)
+    v = 500 * (1 + 0.2 * rng.standard_normal((n, 1, dim))) * float(np.float32(scale))
+    _write(pool, table[0], rng.standard_normal((n, 1, dim)).astype(np.float32), v.astype(np.float32))
+    q = torch.from_numpy(rng.standard_normal((1, 4, dim))).bfloat16()
+    ref, tol = _expected(pool, table[0], n, q[0].double().numpy(), dim ** -0.5)
+    out, st = _run((q.cuda(), *pool.device(), *pool.scales(), i32(table), i32([n])), {})
     assert st == 0
     assert_within(out[0], ref, tol)
