@@ -1,5 +1,5 @@
 """The 4-bit decode where the scales of V are far below or far apart from one
-another, and where scores are large."""
+another, where scores are large, and where rows have many pieces."""
 import numpy as np
 import pytest
 import torch
@@ -117,3 +117,37 @@ def test_head_scales_of_any_size(scale, n, dim):
     out, st = _run((q.cuda(), *pool.device(), *pool.scales(), i32(table), i32([n])), {})
     assert st == 0
     assert_within(out[0], ref, tol)
+
+
+@pytest.mark.parametrize("dim,heads,lengths", [
+    (64, 1, [61_000]), (128, 1, [61_000]),        # 32 warps join a row: more pieces than a round's 256
+    (64, 4, [15_500]), (128, 2, [12, 16_000]),    # 8 warps: more than 64
+    (64, 1, [21_000] + [9] * 239), (128, 2, [5] * 119 + [21_000])])  # 2 warps: more than 16
+def test_rows_of_more_pieces_than_a_round_joins(dim, heads, lengths):
+    pool = Pool4(sum(-(-n // P) for n in lengths) + 3, heads, dim, 7)
+    table = pool.table(lengths)
+    qd, q = pool.query(len(lengths), 2)
+    ref, tol = pool.attend(q, table, lengths, dim ** -0.5)
+    args = (qd, *pool.device(), *pool.scales(), i32(table), i32(lengths))
+    out, st = _run(args, {})
+    assert st == 0
+    assert_within(out, ref, tol)
+    again, _ = _run(args, {})
+    assert torch.equal(out, again)
+
+
+def test_the_same_lengths_under_tables_of_several_widths():
+    """The joining's form goes by the table's width: each of them within the bound, and each the same every time."""
+    lengths = [190, 33]
+    pool = Pool4(20, 1, 64, 8)
+    table = pool.table(lengths)
+    qd, q = pool.query(2, 4)
+    ref, tol = pool.attend(q, table, lengths, 0.125)
+    for width in (12, 40, 1100):
+        wide = np.zeros((2, width), np.int32)
+        wide[:, :12] = table
+        args = (qd, *pool.device(), *pool.scales(), i32(wide), i32(lengths))
+        out, st = _run(args, {})
+        assert st == 0
+        assert_within(out, ref, tol)
+        assert torch.equal(out, _run(args, {})[0])
