@@ -1411,8 +1411,8 @@ __global__ void __launch_bounds__(NW * 32) decode_weights_kernel(const __grid_co
 int decode_pages(int P, int max_blocks, int window) {
   int pages = max_blocks;
   if (window > 0) {
-    const int w = (window + P - 1) / P + 1;
-    if (w < pages) pages = w;
+    const int64_t w = (static_cast<int64_t>(window) + P - 1) / P + 1;
+    if (w < pages) pages = static_cast<int>(w);
   }
   return pages < 1 ? 1 : pages;
 }
