@@ -308,12 +308,17 @@ def kvq_quantize_query(q, q8, q_scale, stream=None):
            "kvq_quantize_query")
 
 
+def _window(window):
+    """A window as a C int, which ctypes would make of any integer's last 32 bits."""
+    return max(-2, min(window, 2**31 - 1))
+
+
 def kvq_decode_num_splits(B, Hkv, max_blocks, window=-1, num_splits=0, head_dim=128):
-    return lib.kvq_decode_num_splits(B, Hkv, head_dim, PAGE, max_blocks, window, num_splits)
+    return lib.kvq_decode_num_splits(B, Hkv, head_dim, PAGE, max_blocks, _window(window), num_splits)
 
 
 def kvq_decode_workspace_size(B, Hq, Hkv, D, max_blocks, window=-1, num_splits=0):
-    return lib.kvq_decode_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, window, num_splits)
+    return lib.kvq_decode_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, _window(window), num_splits)
 
 
 def _workspace(need, like, stream):
@@ -348,7 +353,7 @@ def kvq_paged_decode_attention(q, k_cache, v_cache, k_scale, v_scale, block_tabl
     if workspace is None:
         workspace = _workspace(need, q, stream)
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(block_table),
-            _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), window, dt,
+            _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), _window(window), dt,
             num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status), _stream(stream))
     if accumulation is None:
         _check(lib.kvq_paged_decode_attention(*args), "kvq_paged_decode_attention")
@@ -382,7 +387,7 @@ def kvq_paged_decode_attention_append(q, k_new, v_new, slot_new, k_cache, v_cach
     _check(lib.kvq_paged_decode_attention_append(
         _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_new), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
         _ptr(v_scale), _ptr(block_table), _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
-        float(sm_scale), window, _dtype_code(cache_dtype), num_splits, _ptr(workspace), workspace.numel(),
+        float(sm_scale), _window(window), _dtype_code(cache_dtype), num_splits, _ptr(workspace), workspace.numel(),
         _ptr(dev_status), _stream(stream)), "kvq_paged_decode_attention_append")
     return out
 
@@ -403,7 +408,7 @@ def kvq_paged_decode_attention_per_token(q, k_cache, v_cache, block_table, seq_l
         workspace = _workspace(need, q, stream)
     _check(lib.kvq_paged_decode_attention_per_token(
         _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-        _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), window,
+        _ptr(seq_lens), _ptr(out), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, float(sm_scale), _window(window),
         _dtype_code(cache_dtype), num_splits, _ptr(workspace), workspace.numel(), _ptr(dev_status),
         _stream(stream)), "kvq_paged_decode_attention_per_token")
     return out
@@ -547,7 +552,7 @@ def kvq_paged_decode_attention_shared_prefix(q, k_cache, v_cache, k_scale, v_sca
 
 
 def kvq_decode_weights_workspace_size(B, Hq, Hkv, D, max_blocks, window=-1, num_splits=0):
-    return lib.kvq_decode_weights_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, window, num_splits)
+    return lib.kvq_decode_weights_workspace_size(B, Hq, Hkv, D, PAGE, max_blocks, _window(window), num_splits)
 
 
 def kvq_paged_decode_attention_weights(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, weights,
@@ -575,7 +580,7 @@ def kvq_paged_decode_attention_weights(q, k_cache, v_cache, k_scale, v_scale, bl
                                      dev_status)
     _check(lib.kvq_paged_decode_attention_weights(
         *ptrs, weights.shape[-1], float(decay), B, Hq, Hkv, D, PAGE, max_blocks, num_blocks,
-        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), window, dt, 1 if per_token else 0, num_splits, ws,
+        1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale), _window(window), dt, 1 if per_token else 0, num_splits, ws,
         workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_weights")
     return out
 
@@ -815,5 +820,5 @@ def kvq_paged_decode_attention_fp4(q, k_cache, v_cache, k_scale, v_scale, block_
     *ptrs, ws, status = _addresses(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, workspace, dev_status)
     _check(lib.kvq_paged_decode_attention_fp4(
         *ptrs, B, Hq, Hkv, D, PAGE, max_blocks, num_blocks, 1.0 / math.sqrt(D) if sm_scale is None else float(sm_scale),
-        window, ws, workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_fp4")
+        _window(window), ws, workspace.nbytes, status, _stream(stream)), "kvq_paged_decode_attention_fp4")
     return out
