@@ -208,8 +208,8 @@ __global__ void __launch_bounds__(kPage * D / 8, 1536 / (2 * D)) gather_kernel(c
   __syncthreads();
   const int tokens = tt.n;
   for (int r = 0; r < tokens; r += kPage) {
-    if (tt.page[r / kPage]) {
-      const int64_t page = tt.slot[r] / kPage * p.Hkv + h0;
+    if (r == 0 && tt.page) {
+      const int64_t page = tt.slot[0] / kPage * p.Hkv + h0;
       const uint8_t* kp = p.k_cache + page * p.k_str;
       const uint8_t* vp = p.v_cache + page * p.v_str;
       auto issue = [&](int i) {
@@ -228,11 +228,10 @@ __global__ void __launch_bounds__(kPage * D / 8, 1536 / (2 * D)) gather_kernel(c
           vs = __ldg(p.v_scale + h0 + i);
         }
         S::rows(ring + i % S::kStages * S::kStageB, ks, vs, [&](int token, int d, bool is_v, const uint4& o) {
-          const int64_t at = (static_cast<int64_t>(tt.token[r + token]) * p.Hkv + h0 + i) * D + d;
+          const int64_t at = (static_cast<int64_t>(tt.token[token]) * p.Hkv + h0 + i) * D + d;
           *reinterpret_cast<uint4*>((is_v ? p.v_out : p.k_out) + at) = o;
         });
       }
-      __syncthreads();  // the stages are free for the next 16 tokens
     } else if (r + t < tokens) {
       const int64_t slot = tt.slot[r + t];
       const int64_t page = slot / kPage * p.Hkv + h0;

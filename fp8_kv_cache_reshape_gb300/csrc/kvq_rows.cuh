@@ -187,12 +187,13 @@ KVQ_DEVINL void transpose4(const uint32_t (&w)[4], uint32_t (&o)[4]) {
 // follow the pages: the tokens whose page, if its tokens lie in order, began with
 // one of the 16 tokens from 16 (tile - 1) on.  A run of tokens in order through
 // whole pages then has each page in one tile, wherever in a page it starts; any
-// other tokens fall to some tile too, each to one, at most 31 to a tile.
+// other tokens fall to some tile too, each to one, at most 31 to a tile.  A page
+// whose tile begins with other tokens is not taken as a whole.
 struct TileTokens {
   int token[32];
   int64_t slot[32];
   int n;
-  bool page[2];  // tokens 0 .. 15 (16 .. 31) fill one page in order
+  bool page;  // tokens 0 .. 15 fill one page in order (16 on never do: they are 15 at most)
 };
 // By warp 0, before a barrier of the CTA.
 KVQ_DEVINL void find_tokens(TileTokens& s, const int64_t* slots, int T, int64_t num_slots, int tile, bool aligned, int* dev_status) {
@@ -215,13 +216,12 @@ KVQ_DEVINL void find_tokens(TileTokens& s, const int64_t* slots, int T, int64_t 
   }
   __syncwarp();
   const int n = __popc(have);
-  const int64_t first = lane < n ? s.slot[lane & kPage] : 0;
-  const bool run = lane < n && first % kPage == 0 && s.slot[lane] == first + (lane & (kPage - 1));
+  const int64_t first = n ? s.slot[0] : 0;
+  const bool run = lane < n && first % kPage == 0 && s.slot[lane] == first + lane;
   const unsigned runs = __ballot_sync(0xffffffffu, run);
   if (lane == 0) {
     s.n = n;
-    s.page[0] = (runs & 0xFFFFu) == 0xFFFFu;
-    s.page[1] = (runs >> 16) == 0xFFFFu;
+    s.page = (runs & 0xFFFFu) == 0xFFFFu;
   }
 }
 

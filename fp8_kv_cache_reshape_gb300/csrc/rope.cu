@@ -382,7 +382,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
   __syncthreads();
   const int n = tt.n;
   for (int r = 0; r < n; r += kPage) {
-    const bool valid = r + t < n, page_run = tt.page[r / kPage];
+    const bool valid = r + t < n, page_run = r == 0 && tt.page;
     const int row = tt.token[valid ? r + t : r];
     const int64_t slot = tt.slot[valid ? r + t : r];
     const int off = static_cast<int>(slot % kPage);
@@ -492,7 +492,6 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       kp += p.k_str;
       vp += p.v_str;
     }
-    if (page_run) __syncthreads();  // the next 16 tokens start with the first buffer again
   }
 }
 
