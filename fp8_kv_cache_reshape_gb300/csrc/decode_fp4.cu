@@ -39,9 +39,8 @@ namespace kvq {
 
 namespace {
 
-constexpr int kWarps = 4;             // warps per CTA, each with a ring of its own
+constexpr int kWarps = kStreamWarps;  // warps per CTA, each with a ring of its own
 constexpr int kCtasPerSm = 3;         // 168 registers a thread (four, with 128 and spills: 128K 42.2 against 40.2 us)
-constexpr int kMinPart = 2;           // pages of a part, at least: a pair
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 // Weights are 2^(s2 - M + base): below 2^16 / 2 ^ (exponent of V's largest block scale), so
@@ -106,9 +105,6 @@ KVQ_DEVINL Span span_of(const Fp4Params& p, int b, bool report = false) {
   s.n = (s.len + kPage - 1) / kPage - s.first;
   return s;
 }
-// Pages of a part, an even number: the stream in `parts` equal ones.
-KVQ_DEVINL int part_pages(int total, int parts) { return max(kMinPart, ((total + parts - 1) / parts + 1) & ~1); }
-
 // Where a warp's part [pos, end) of the page stream begins: in sequence b, `before`
 // pages (of one KV head) after the stream's start.  Lengths that another stream
 // changes while the call runs give wrong results, but every loop here ends, every
@@ -630,10 +626,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) decode_fp4_kernel(con
   // Are all of the CTA's parts, more than one, of one (sequence, KV head)?  Then
   // their states meet at the end: one row of partials instead of four.  The warps
   // tell each other, so that all of them go by the same answer.
-  const int c0 = (index - warp) * part.chunk, c1 = min(part.total, c0 + kWarps * part.chunk);
   const int x0 = feeder.before * p.Hkv + feeder.h * feeder.sp.n;
   const bool some = part.pos < part.end;
-  if (lane == 0) s_view[warp] = !some ? 0 : c1 - c0 > part.chunk && x0 <= c0 && c1 <= x0 + feeder.sp.n ? 2 : 1;
+  if (lane == 0) s_view[warp] = !some ? 0 : parts_join((index - warp) * part.chunk, part.chunk, part.total, x0, feeder.sp.n) ? 2 : 1;
   __syncthreads();
   if (!some) return;
   bool joined = true;
@@ -758,23 +753,12 @@ __global__ void __launch_bounds__(NW * 32) decode_fp4_combine_kernel(const Fp4Pa
   }
   const int chunk = part_pages(total * p.Hkv, p.parts);
   const int x = before * p.Hkv + h * n;
-  const int first = x / chunk, last = (x + n - 1) / chunk;
-  if (first == last) return;  // written where it was computed
+  const StreamRows rows(x, n, total * p.Hkv, chunk);
+  if (rows.first == rows.last) return;  // written where it was computed
   const float vs = p.v_scale[h];
-  // CTAs kWarps * [c0, c1) of parts wrote one row each, the parts before and behind
-  // them their own
-  const int all = total * p.Hkv, cta = kWarps * chunk;
-  const int c0 = (x + cta - 1) / cta;
-  int c1 = (x + n) / cta;
-  if (x + n == all && all - all / cta * cta > chunk) c1 = all / cta + 1;
-  const int lead = c1 > c0 ? kWarps * c0 - first : last - first + 1;
-  const int full = c1 > c0 ? c1 - c0 : 0;
-  const int count = c1 > c0 ? lead + full + max(0, last - kWarps * c1 + 1) : lead;
+  const int count = rows.count;
   const int64_t pair = static_cast<int64_t>(b) * p.Hkv + h;
-  auto row = [&](int i) -> int64_t {
-    const int part = i < lead ? first + i : i < lead + full ? kWarps * (c0 + i - lead) : kWarps * c1 + i - lead - full;
-    return (part + pair) * p.g + qh;
-  };
+  auto row = [&](int i) -> int64_t { return (rows.part(i) + pair) * p.g + qh; };
   float m = NEG_INF, l = 0.f, acc[V] = {};
   for (int i0 = warp; i0 < count; i0 += NW * kAtOnce) {
     float e[kAtOnce];

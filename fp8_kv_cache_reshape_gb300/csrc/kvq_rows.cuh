@@ -6,8 +6,11 @@
 #include <cuda_fp4.h>
 
 #include "kvq_device.cuh"
+#include "kvq_page_plan.h"
 
 namespace kvq {
+
+static_assert(kPlanPage == kPage, "one page size");
 
 // Heads a CTA walks: as many, in halves from `most`, as leave `ctas` CTAs.
 inline int heads_per_cta(int heads, int tiles, int most, int ctas) {
@@ -206,8 +209,7 @@ KVQ_DEVINL void find_tokens(TileTokens& s, const int64_t* slots, int T, int64_t 
     slot = -1;
   }
   bool mine = slot >= 0;
-  // its page's first token is token - slot % kPage, in [16 (tile - 1), 16 tile)
-  if (aligned && mine) mine = static_cast<unsigned>(lane - static_cast<int>(slot % kPage)) < kPage;
+  if (aligned && mine) mine = tile_takes(lane, slot);
   const unsigned have = __ballot_sync(0xffffffffu, mine);
   if (mine) {
     const int at = __popc(have & ((1u << lane) - 1));
