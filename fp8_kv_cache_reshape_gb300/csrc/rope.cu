@@ -550,6 +550,11 @@ bool rows_ok(const void* x, int64_t stride, int heads, int D) {
   return aligned(x, 16) && stride % 8 == 0 && stride >= static_cast<int64_t>(heads) * D;
 }
 
+// Rows in place go by one stride: with another, a token's output is one that is still to be read.
+bool in_place_ok(const void* x, int64_t stride, const void* out, int64_t out_stride, int T) {
+  return out != x || out_stride == stride || T <= 1;
+}
+
 // Checks of the norm and the rotation; fills them in.
 kvq_status_t take_turn(TokenParams& p, const kvq_head_norm_t* norm, const kvq_rotary_t* rotary, int D, const char* where) {
   p.eps = 0.f;
@@ -640,6 +645,8 @@ extern "C" kvq_status_t kvq_qk_norm_rope(const void* q, int64_t q_stride, const 
   if ((Hq && (!rows_ok(q, q_stride, Hq, D) || !rows_ok(q_out, q_out_stride, Hq, D))) ||
       (Hkv && (!rows_ok(k, k_stride, Hkv, D) || !rows_ok(k_out, k_out_stride, Hkv, D))))
     return fail(KVQ_ERR_INVALID_ARG, "qk_norm_rope: rows must be 16-byte aligned, heads * D or more apart");
+  if ((Hq && !in_place_ok(q, q_stride, q_out, q_out_stride, T)) || (Hkv && !in_place_ok(k, k_stride, k_out, k_out_stride, T)))
+    return fail(KVQ_ERR_INVALID_ARG, "qk_norm_rope: in place, the strides must be the same");
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.k = static_cast<const __nv_bfloat16*>(k);
   p.q_stride = q_stride;
@@ -678,6 +685,8 @@ extern "C" kvq_status_t kvq_rope_and_cache(const void* q, int64_t q_stride, cons
   if (!rows_ok(k, k_stride, Hkv, D) || !rows_ok(v, v_stride, Hkv, D) || (Hq && !rows_ok(q, q_stride, Hq, D)) ||
       (Hq && q_out && !rows_ok(q_out, q_out_stride, Hq, D)))
     return fail(KVQ_ERR_INVALID_ARG, "rope_and_cache: rows must be 16-byte aligned, heads * D or more apart");
+  if (Hq && !in_place_ok(q, q_stride, q_out, q_out_stride, T))
+    return fail(KVQ_ERR_INVALID_ARG, "rope_and_cache: in place, the strides must be the same");
   st = take_cache(p, slot_mapping, k_cache, v_cache, k_scale, v_scale, fmt, D, num_blocks, dev_status, "rope_and_cache");
   if (st != KVQ_OK) return st;
   p.q = static_cast<const __nv_bfloat16*>(q);

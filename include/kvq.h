@@ -639,13 +639,14 @@ kvq_status_t kvq_qk_norm_rope(const void* q, int64_t q_stride, const void* k, in
  *             kvq_reshape_and_cache_per_token (E4M3 or E5M2; the scales are
  *             ignored and may be NULL).
  *  q_out      bf16 [T][Hq][D], tokens q_out_stride elements apart; may be q
- *             itself; or NULL.
+ *             itself (same stride); or NULL.
  *  q8         uint8 [T][Hq][D] contiguous, 16-byte aligned: E4M3 codes of
  *             fl32(q / q_scale) as kvq_quantize_query; or NULL.  Both may be
  *             given; with Hq > 0 one must be.
  *  q_scale    float32 [1], for q8.
  *  T >= 0, Hq >= 0, 1 <= Hkv, D in {64, 128} (and 256 for FP8 caches with
- *  per-head scales), P == 16.  q_out, q8 and the caches must not overlap k or v.
+ *  per-head scales), P == 16.  q_out, q8 and the caches must not overlap k or v,
+ *  nor q8 and the caches q.
  *  Declared rounding: norm and rotation in float32; the float32 result is
  *  quantized (or rounded to bf16) directly, without a rounding to bf16 before.
  */
