@@ -5,8 +5,9 @@
 // Mathematics.  y = x * rsqrt(mean x^2 + eps) * w per head, then each pair is
 // turned by a = position * inv_freq.  Norm weight and rotation fold into two
 // factors per dim that do not depend on the head: with p(d) the pair's other
-// dim, out_d = r * (x_d A_d + x_p(d) B_d), A_d = w_d cos a, B_d = -+ w_p(d) sin a,
-// r the head's norm factor.  A lane holds eight dims of one token and walks
+// dim, out_d = r x_d A_d + r x_p(d) B_d, A_d = w_d cos a, B_d = -+ w_p(d) sin a,
+// r the head's norm factor (first, so that no product with a weight leaves float32
+// whose result does not).  A lane holds eight dims of one token and walks
 // heads, so angles, sines and weights are paid once per token and CTA.
 //
 // The angle is taken in turns in 64-bit fixed point: inv_freq / 2 pi as a
@@ -22,6 +23,7 @@
 // 51% busy, the issue slots 67%.  A step of 64 tokens: 5.5 us, latency.
 #include <cfloat>
 #include <cmath>
+#include <type_traits>
 
 #include "kvq_host.h"
 #include "kvq_rows.cuh"
@@ -49,15 +51,16 @@ KVQ_DEVINL uint64_t turns_per_position(float inv_freq) {
 
 // Sine and cosine of a fraction of a turn: to the nearest quarter, then the
 // Taylor series of the rest, y up to pi / 4 either way.  The first terms left
-// out are y^11 / 11! < 2^-29 and y^12 / 12! < 2^-32; y is rounded three times, 2^-22
-// of it however small it is: the rest keeps all of its bits, in two signed halves.
+// out are y^11 / 11! < 2^-29 and y^12 / 12! < 2^-32; y is rounded three times, 2^-22 of it,
+// and cut to 55 bits of a turn, of which the lower 23 become a float32 as the
+// mantissa of 2^23 + x.
 KVQ_DEVINL void sincos_turns(uint64_t turns, float& s, float& c) {
-  const uint32_t t = static_cast<uint32_t>((turns + 0x80000000u) >> 32);
-  const int low = static_cast<int>(static_cast<uint32_t>(turns));
+  const uint32_t t = static_cast<uint32_t>(turns >> 32);
   const uint32_t quarter = (t + 0x20000000u) >> 30;
   const int rest = static_cast<int>(t - (quarter << 30));  // within an eighth of a turn
+  const float low = __uint_as_float(0x4B000000u | static_cast<uint32_t>(turns) >> 9) - 0x1p23f;
   const float turn = 6.283185307f;
-  const float y = fmaf(static_cast<float>(rest), turn * 0x1p-32f, static_cast<float>(low) * (turn * 0x1p-64f)), z = y * y;
+  const float y = fmaf(static_cast<float>(rest), turn * 0x1p-32f, low * (turn * 0x1p-55f)), z = y * y;
   float s0 = fmaf(z, 1.f / 362880, -1.f / 5040), c0 = fmaf(z, -1.f / 3628800, 1.f / 40320);
   s0 = fmaf(z, s0, 1.f / 120);
   s0 = fmaf(z, s0, -1.f / 6);
@@ -174,13 +177,15 @@ KVQ_DEVINL Turn make_turn(const TokenParams& p, const __nv_bfloat16* weight, int
   return t;
 }
 
-// The norm's factor of a row for turn_row, where float32 has not the plain way's
-// squares or products: x and y scaled by it on return.  The row's maximum is brought to
-// [1, 2), as a power of two, but eps with it no further than 2^100, where it outweighs
-// the rest.  Every lane of the warp takes part.
+// The norm's factor of a row whose squares float32 does not hold, x * y * z: the first two
+// are a power of two that brings the row's maximum to [1, 2), but eps with it no further than
+// 2^100, where it outweighs the rest; the third is the factor of that row.  Every lane of the
+// warp takes part.  Not inlined: its code between the others' costs 2 to 4%.
 template <int D>
-KVQ_DEVINL void norm_scaled(float eps, float2 (&x)[4], float2 (&y)[4]) {
+__device__ __noinline__ float3 norm_factors(float eps, uint4 raw) {
   constexpr int LPT = D / 8;
+  float2 x[4];
+  unpack8_bf16(raw, x);
   float top = amax8(x);
 #pragma unroll
   for (int off = 1; off < LPT; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -193,40 +198,27 @@ KVQ_DEVINL void norm_scaled(float eps, float2 (&x)[4], float2 (&y)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     x[i] = fmul2(fmul2(x[i], make_float2(f, f)), make_float2(g, g));
-    y[i] = fmul2(fmul2(y[i], make_float2(f, f)), make_float2(g, g));
     sum = ffma2(x[i], x[i], sum);
   }
   float all = sum.x + sum.y;
 #pragma unroll
   for (int off = 1; off < LPT; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-  const float r = rsqrtf(fmaf(all, 1.f / D, eps * f * f * g * g));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[i] = fmul2(x[i], make_float2(r, r));
-    y[i] = fmul2(y[i], make_float2(r, r));
-  }
+  return make_float3(f, g, rsqrtf(fmaf(all, 1.f / D, eps * f * f * g * g)));
 }
 
-// A lane's eight dims x and their pairs' others y, from the warp's stage.
-KVQ_DEVINL void load_row(const Turn& t, uint32_t stage, int lane, float2 (&x)[4], float2 (&y)[4]) {
-  const uint4 raw = lds128(stage + lane * 16), other = lds128(stage + t.from * 16);
+// Norm and rotation of a lane's eight dims, `other` those of lane t.from; every
+// lane of the warp takes part.
+template <int D>
+KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, const uint4& other, float2 (&o)[4]) {
+  constexpr int LPT = D / 8;
   const uint32_t w[4] = {other.x, other.y, other.z, other.w};
+  float2 x[4], y[4];
   unpack8_bf16(raw, x);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t u = w[i];
     y[i] = make_float2(__uint_as_float(__byte_perm(u, 0, t.px)), __uint_as_float(__byte_perm(u, 0, t.py)));
   }
-}
-
-// Norm and rotation of a lane's eight dims; every lane of the warp takes part.
-template <int D>
-KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, uint32_t stage, int lane, float2 (&o)[4]) {
-  constexpr int LPT = D / 8;
-  float2 x[4], y[4];
-  load_row(t, stage, lane, x, y);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
   if (norm) {
     float2 sum = fmul2(x[0], x[0]);
 #pragma unroll
@@ -234,24 +226,32 @@ KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, uint32_t stage, in
     float all = sum.x + sum.y;
 #pragma unroll
     for (int off = 1; off < LPT; off <<= 1) all += __shfl_xor_sync(0xffffffffu, all, off);
-    const float mean = fmaf(all, 1.f / D, eps), r = rsqrtf(mean);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmul2(o[i], make_float2(r, r));
-    // Squares that float32 has not, or products before r that it has not or not in full:
-    // from a mean of 2^-40 on, what a subnormal product loses is below 2^-129 of the result.
-    // Only such values take the other result; a warp without any pays for the comparisons
-    // and a vote (16,383 tokens: 58.0 us without them, 58.9 so).
-    const bool plain = mean >= 0x1p-40f && mean <= 0x1p100f && amax8_nan(o) <= FLT_MAX;
+    const float mean = fmaf(all, 1.f / D, eps);
+    float r;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(mean));
+    // Squares that float32 does not hold: of a sum beyond it, or below 2^-149 beside a mean
+    // that they would be part of.  Only such rows take the other factor; a warp without any
+    // pays for a comparison and a vote.
+    const bool plain = __float_as_uint(mean) - 0x13000000u < 0x7F800000u - 0x13000000u;  // 2^-89 <= mean < infinity
     if (__any_sync(0xffffffffu, !plain)) {
-      load_row(t, stage, lane, x, y);  // again: holding them spills
-      norm_scaled<D>(eps, x, y);
+      const float3 f = norm_factors<D>(eps, raw);
+      if (!plain) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 u = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
-        if (!plain) o[i] = u;
+        for (int i = 0; i < 4; ++i) {
+          x[i] = fmul2(fmul2(x[i], make_float2(f.x, f.x)), make_float2(f.y, f.y));
+          y[i] = fmul2(fmul2(y[i], make_float2(f.x, f.x)), make_float2(f.y, f.y));
+        }
+        r = f.z;
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = fmul2(x[i], make_float2(r, r));
+      y[i] = fmul2(y[i], make_float2(r, r));
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = ffma2(x[i], t.a[i], fmul2(y[i], t.b[i]));
 }
 
 // Rows of a warp's tokens on their way through shared memory: a stage is the 16
@@ -289,17 +289,23 @@ KVQ_DEVINL void turn_rows(const TokenParams& p, uint32_t ring, bool is_q, int ti
   if (dst) dst += row * (is_q ? p.q_out_stride : p.k_out_stride) + h0 * D + 8 * j;
   uint8_t* codes = is_q && p.q8 ? p.q8 + (static_cast<int64_t>(row) * p.Hq + h0) * D + 8 * j : nullptr;
   const Divisor s(codes ? __ldg(p.q_scale) : 1.f);
-  for (int i = 0; i < n; ++i) {
-    copy_wait<kStages - 2>();
-    __syncwarp();  // the other lanes' copies too, and they are done with the stage before
-    issue(i + kStages - 1);
-    const uint32_t at = ring + i % kStages * kStageB;
-    float2 o[4];
-    turn_row<D>(turn, weight != nullptr, p.eps, at, lane, o);
-    if (!live) continue;
-    if (dst) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(o);
-    if (codes) *reinterpret_cast<uint2*>(codes + i * D) = quant8_fp8<false>(o, s);
-  }
+  auto walk = [&](auto normed) {  // a loop each: without norms 3% less
+    for (int i = 0; i < n; ++i) {
+      copy_wait<kStages - 2>();
+      __syncwarp();  // the other lanes' copies too, and they are done with the stage before
+      issue(i + kStages - 1);
+      const uint32_t at = ring + i % kStages * kStageB;
+      float2 o[4];
+      turn_row<D>(turn, normed.value, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), o);
+      if (!live) continue;
+      if (dst) *reinterpret_cast<uint4*>(dst + i * D) = pack8_bf16(o);
+      if (codes) *reinterpret_cast<uint2*>(codes + i * D) = quant8_fp8<false>(o, s);
+    }
+  };
+  if (weight)
+    walk(std::true_type{});
+  else
+    walk(std::false_type{});
 }
 
 // Bytes between tokens of a V page in shared memory, before its transposition:
@@ -413,7 +419,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
       const uint4 vraw = lds128(at + kStageB + lane * 16);
       float2 ko[4], vo[4];
       if constexpr (TURN)
-        turn_row<D>(turn, p.k_weight != nullptr, p.eps, at, lane, ko);
+        turn_row<D>(turn, p.k_weight != nullptr, p.eps, lds128(at + lane * 16), lds128(at + turn.from * 16), ko);
       else
         unpack8_bf16(lds128(at + lane * 16), ko);
       unpack8_bf16(vraw, vo);
@@ -496,7 +502,7 @@ KVQ_DEVINL void cache_rows(const TokenParams& p, uint32_t ring, int tile, int h0
 }
 
 // Three CTAs of 256 threads an SM (80 registers) where there is a cache to write, four (64)
-// for rows alone (16,383 tokens: 58.8 us, with three 61.3).
+// for rows alone (16,000 tokens normed: 56.9 us, with three 58.0; 8,000 of head dim 256: 35.7 and 45.1).
 template <int D, int FMT, bool TURN = true>
 __global__ void __launch_bounds__(kPage * D / 8, (FMT == kRowsOnly ? 1024 : 768) / (2 * D)) token_kernel(const TokenParams p) {
   __shared__ __align__(16) uint8_t ring_mem[D / 16 * Ring<D>::kBytes];

@@ -568,11 +568,10 @@ kvq_status_t kvq_evict_tokens(const float* weights, int64_t weights_stride, void
  *               height and width of an image's or video's patch, each pair
  *               following one of them.
  *  inv_freq     float32 [rot_dim / 2], radians per position, finite.  The
- *               angle is the exact product reduced in 64-bit fixed point: off
- *               by at most 2^-32 of a turn for |positions| up to 2^31 and
- *               |inv_freq| up to 1, and small angles by at most 2^-30 of
- *               themselves for |inv_freq| from 2^-31 on; sine and cosine
- *               are float32's to 2^-21 of themselves.
+ *               angle is the exact product reduced in 64-bit fixed point: for
+ *               |inv_freq| up to 1 off by at most 2^-54 of a turn and 2^-63
+ *               of one per position (2^-32 in all up to 2^31); sine and cosine
+ *               of it are float32's, to 2^-21 of themselves.
  *  pair_axis    int32 [rot_dim / 2], each in [0, num_axes); NULL: all 0.
  *  num_axes     1 to 4.
  *  rot_dim      a multiple of 16, 16 to D.
