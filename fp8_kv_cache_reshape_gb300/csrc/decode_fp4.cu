@@ -10,12 +10,13 @@
 // moves to the other operand, P, one multiplication for two weights instead of one
 // for every two of V's 16 x 16 values.
 //
-// Bound: memory, 9/16 byte per element of K and V, and close behind it the issue
-// slots (58% full; ALU pipe 48%: half of it the conversions, an instruction for
-// two codes).  Over longer contexts a call grows by 28 us per 128K tokens of 8 KV
-// heads of 128, 5.4 TB/s; with the scores alone, or the outputs alone, it grows by 22,
-// the copies' own time.  One request of 128K: 38 us, 4.0 TB/s with its fixed
-// part of about 10; eight of 20K: 48 us, 4.0 TB/s.
+// Bound: memory in principle, 9/16 byte per element of K and V; in practice latency, with
+// three warps a scheduler: no unit is full (issue slots 59%, ALU pipe 49%: half of it the
+// conversions, an instruction for two codes; tensor pipe 22%).  Over longer contexts a call grows
+// by 28 us per 128K tokens of 8 KV heads of 128, 5.5 TB/s; with the scores alone, or the
+// outputs alone, it grows by 22, the copies' own time.  One request of 128K: 38.5 us, 3.9 TB/s with
+// its fixed part of about 10; eight of 20K: 48.3 us, 4.0 TB/s; 64 of 500 to 1,000: 24 us for a
+// floor of 8.
 //
 // Layout.  A warp takes two pages (32 tokens of a KV head) at a time from stages
 // of its own in shared memory, filled by 16-byte asynchronous copies: no barrier,
@@ -40,7 +41,7 @@ namespace kvq {
 namespace {
 
 constexpr int kWarps = kStreamWarps;  // warps per CTA, each with a ring of its own
-constexpr int kCtasPerSm = 3;         // 168 registers a thread (four, with 128 and spills: 128K 42.2 against 40.2 us)
+constexpr int kCtasPerSm = 3;         // 168 registers a thread (four, with 128 and spills, at an earlier step: 128K 42.2 against 40.2 us)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLag = 3.f;           // by how much scores may pass the stabilizer
 // Weights are 2^(s2 - M + base): below 2^16 / 2 ^ (exponent of V's largest block scale), so
@@ -851,7 +852,10 @@ kvq_status_t launch_fp4(const Fp4Params& p, cudaStream_t s) {
   if (e != cudaSuccess) return cuda_status(e, "paged_decode_fp4 launch");
   cfg.dynamicSmemBytes = 0;
   const unsigned rows = static_cast<unsigned>(p.B) * p.Hq;
-  // few rows have many pieces (about four of which are one row of partials): more warps, 32 dims to a CTA
+  // Few rows have many pieces (about four of which are one row of partials): more warps, 32 dims
+  // to a CTA.  By the mean over the rows.  128K, us with 32, 8, 2 warps: one KV head 19.9, 23.6, 36.8,
+  // two 22.1, 23.0, 31.5, eight 39.4, 38.5, 42.3; 16 x 4,000 tokens 57, 26.8, 25.9, 64 x 500 to
+  // 1,000 149, 30.8, 24.2.
   const int64_t pieces = p.parts / (static_cast<int64_t>(p.B) * p.Hkv);
   if (pieces >= 512) {
     cfg.gridDim = dim3(rows, D / 32);

@@ -15,12 +15,12 @@
 // turns.  No float64 (two operations a clock per SM here) and no position too
 // far for float32.
 //
-// Bound: memory in principle (every row is read once and written once); in
-// practice the conversions share the limit.  16,383 tokens, 32 + 8 heads of 128,
-// normed and turned along three axes: 58 us, 5.8 TB/s of the measured copy
-// rate of 6.8, the issue slots two thirds full.  4,096 tokens into an E4M3 cache,
-// queries quantized: 20 us, 3.8 TB/s, where the ALU pipe (conversions, selections of bytes) is
-// 51% busy, the issue slots 67%.  A step of 64 tokens: 5.5 us, latency.
+// Bound: memory in principle (every row is read once and written once).  16,383 tokens,
+// 32 + 8 heads of 128, normed and turned along three axes: 58.5 us, 5.7 TB/s of the
+// measured copy rate of 6.8, the issue slots 71% full.  4,096 tokens into an E4M3 cache,
+// queries quantized: 19.5 us, 3.9 TB/s (normed: 24), where no unit is full (issue slots 65%, ALU pipe,
+// which converts and selects bytes, 51%): a row's chain of dependent steps, with five of six
+// warps a scheduler there on average, is what it waits for.  A step of 64 tokens: 5.5 us, latency.
 #include <cfloat>
 #include <cmath>
 #include <type_traits>
@@ -257,8 +257,8 @@ KVQ_DEVINL void turn_row(const Turn& t, bool norm, float eps, const uint4& raw, 
 // Rows of a warp's tokens on their way through shared memory: a stage is the 16
 // bytes of each lane, of one row (or of a k and a v row).  The copies of all stages but one
 // are in flight, which costs no registers, and a pair's other dims are a second read
-// instead of four shuffles (4,096 tokens into an E4M3 cache: 22.3 us with rows in
-// registers, 19.9 so; 16,383 tokens' rows: 61.5 and 58).
+// instead of four shuffles (at the step that brought it: 4,096 tokens into an E4M3 cache
+// 22.8 -> 20.3 us, 16,383 tokens' rows 59.8 -> 58).
 template <int D>
 struct Ring {
   static constexpr int kBytes = D == 256 ? 2048 : 4096;  // of a warp (of 16 at D = 256)
@@ -520,16 +520,16 @@ __global__ void __launch_bounds__(kPage * D / 8, (FMT == kRowsOnly ? 1024 : 768)
   }
 }
 
-// Heads to a CTA: angles and weights are paid once per CTA (16,383 tokens: 68 us
-// with 8 query heads, 62 with 16, 60 with 32), but the SMs want filling: about a
-// CTA of the cache's rows for each, and two of the queries' (4,096 tokens: 19.9 us;
-// 21.9 with twice as many of the first, 20.3 and 20.5 with half and twice as many of the second;
-// 1,777 tokens of head dim 64: 10.2 us, 12.4 and 12.1 with half and twice the first).
+// Heads to a CTA: angles and weights are paid once per CTA (16,383 tokens: 66.4 us
+// with 8 query heads, 57.9 with 16, 58.5 with 32), but the SMs want filling: about a
+// CTA of the cache's rows for each, and two of the queries' (4,096 tokens: 19.4 us;
+// 21.2 with twice as many of the first, 20.2 and 20.8 with half and twice as many of the second;
+// 1,777 tokens of head dim 64: 10.1 us, 12.6 and 11.7 with half and twice the first).
 // Without queries as many of the cache's CTAs as run at once, three to an SM (3,500
-// tokens, 4 bits: 7.4 us with 440 CTAs, 8.5 with 220; 4,096 tokens: 10.8 with 514, 9.2 with 257).
+// tokens, 4 bits: 7.9 us; 11.1 and 9.0 with half and twice as many).
 // Aligned tiles pay from a few hundred tokens in order on (256 tokens of one
-// prompt 7.2 us against 8.2, 1,024: 17.5 against 21.2) and cost steps of many sequences a
-// little (256: 10.8 against 9.5, 1,024: 25.9 against 24.9).
+// prompt 6.4 us against 8.0, 1,024: 9.2 against 14.7) and cost steps of many sequences a
+// little (256: 10.3 against 8.3, 1,024: 21.4 against 20.0).
 template <int FMT, bool TURN = true>
 kvq_status_t launch_tokens(TokenParams& p, int D, cudaStream_t s, const char* where) {
   p.tiles = (p.T - 1) / kPage + 1;

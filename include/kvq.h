@@ -690,7 +690,8 @@ kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, 
  *  The attended pages of all sequences and KV heads are laid end to end and cut
  *  into equal parts, one per warp, so that ragged batches balance; a part's
  *  share of a (sequence, KV head) is merged by log-sum-exps in FP32.  The plan is a
- *  function of the lengths alone: results are deterministic.
+ *  function of the lengths, the window, the sizes (max_blocks among them: the
+ *  order of the merge goes by it) and the device: results are deterministic.
  *  Declared rounding: the query enters as f16(fl32(q * sigma)) as for
  *  kvq_paged_decode_attention; K enters as code * block scale, exact in float16; scores
  *  are FP32 sums t times c = fl32(fl32(k_scale * sm_scale) * log2(e)) / sigma;
@@ -699,9 +700,9 @@ kvq_status_t kvq_gather_cache(const int64_t* slot_mapping, const void* k_cache, 
  *  largest exponent so far is above 0, are rounded to float16, multiplied by V's
  *  block scale with another rounding to float16 (each half a step of 2^-10;
  *  below 2^-14 steps of 2^-24),
- *  and contracted with V's codes, exact in float16, in FP32 per page
- *  of 16 tokens, then added into a running FP32 sum; the row sum adds them
- *  unrounded.  The output is rounded to bf16 once, at the end.
+ *  and contracted with V's codes, exact in float16, in FP32 per two pages
+ *  (32 tokens), then added into a running FP32 sum; the row sum adds them
+ *  unrounded.  The output, times v_scale, is rounded to bf16 once, at the end.
  */
 size_t kvq_decode_fp4_workspace_size(int B, int Hq, int Hkv, int D, int P, int max_blocks);
 kvq_status_t kvq_paged_decode_attention_fp4(const void* q, const void* k_cache, const void* v_cache,
